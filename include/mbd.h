@@ -12,6 +12,9 @@
  *   mbd_fused_allreduce_add_rmsnorm[_quant_fp8]
  *                                    the norm fed by n partial activations summed on the way in
  *   mbd_run_program                  a list of the above operations as ONE persistent kernel launch
+ *   mbd_kv_cache_append, mbd_paged_attention_decode, mbd_kv_cache_evict
+ *                                    the decode step's paged key-value cache: new tokens in, the attention of
+ *                                    one new token per sequence over it, eviction by accumulated weight
  *
  * Definitions (cited by page title and section):
  *   [TRT] "TensorRT-LLM: Compiling Inference Engines Ahead of Time", section "Fusing operations, measured":
@@ -85,7 +88,8 @@ typedef enum {
  * mbd_swiglu_quant_fp8 in dynamic mode); wider rows return MBD_ERR_UNSUPPORTED. */
 #define MBD_MAX_REDUCED_WIDTH 262144
 
-/* ABI version of this header (bumped on any signature change or added entry point). */
+/* ABI version of this header (bumped on any signature change or added entry point). The key-value cache's
+ * section at the end has a version of its own, MBD_KV_ABI_VERSION. */
 #define MBD_ABI_VERSION 9
 int mbd_abi_version(void);
 
@@ -102,6 +106,10 @@ uint64_t mbd_kernel_launches(void);
  * through distributed shared memory and waits for its peers with a bounded wait (about one second); if
  * the wait ever ran out, the kernel set this bit and returned without writing its outputs. */
 #define MBD_DEVERR_EXCHANGE_TIMEOUT 1u
+/* A key-value cache kernel met a page number outside the pool, a length outside [0, pages_per_seq * page_size] or
+ * a new token without a slot: it read and wrote nothing there (a length is clamped, a slot on such a page counts
+ * as masked, a token without a slot is dropped). */
+#define MBD_DEVERR_BAD_INDEX 2u
 
 /* Copy the OR of the library's device error words on the CURRENT device into *flags and, if clear != 0,
  * reset them. Synchronous (a device-to-host copy on the legacy default stream). Returns MBD_ERR_INVALID_ARG
@@ -435,6 +443,120 @@ int mbd_tuning_get(mbd_tuning_entry* entries, int capacity);
  * a null output), the width checks of the entry point (MBD_ERR_MISALIGNED, MBD_ERR_UNSUPPORTED). */
 mbd_status mbd_launch_shape(int kind, int mode, int64_t n_tokens, int64_t width, int32_t* ctas_per_row,
                             int32_t* vectors_per_thread, int32_t* threads);
+
+/*
+ * The key-value cache of a decode step. Attention over the cache is the one operation of a decode step besides the
+ * fusions above that is bound by bytes: each cached key and value is read once for one new token. No counterpart
+ * among the page's fusions; [FP8] names the cache as one of the tensors that FP8 halves, and its convention of a
+ * scale per tensor or per block is the one used here.
+ *
+ * Layout. k and v are pools of pages, [n_pages, n_kv_heads, page_size, head_dim], each page dense, page_stride
+ * elements from one page to the next (so that k and v may interleave in one pool). A page table, int32
+ * [n_seqs, pages_per_seq] on the device, names the pages of each sequence: slot s of sequence b lies in page
+ * page_table[b][s / page_size] at s % page_size. Entries behind a sequence's last page are not looked at. Lengths
+ * (seq_lens) are int32 [n_seqs] on the device, read when the kernel runs, so one captured graph serves a growing
+ * cache. What a table names twice (a shared prefix) may be read by any number of sequences; it must not be
+ * appended to or evicted from through more than one.
+ *
+ * Stored elements. MBD_KV_BF16: as they are. MBD_KV_FP8: E4M3 codes under this library's scale convention (value ~
+ * code * scale): MBD_SCALE_STATIC_PER_TENSOR, k_scale and v_scale ONE fp32 value each; MBD_SCALE_DYNAMIC_PER_TOKEN, one
+ * for each token and head, fp32 [n_pages, n_kv_heads, page_size], written by the append.
+ *
+ * weight and position, both [n_pages, n_kv_heads, page_size] and dense, are for caches that evict (else null): the
+ * attention weight that a slot has been given so far, and the position of its token in the sequence.
+ *
+ * Errors are those of the conventions above; besides, an unknown format or mode, a non-zero `reserved`, or k and v
+ * that overlap give MBD_ERR_INVALID_ARG; k or v not 16-byte aligned, the other arrays not 4-byte aligned, or a stride
+ * that is not a multiple of 16 bytes MBD_ERR_MISALIGNED; a head_dim other than 64, 128 and 256, a page_size that is no
+ * power of two or above 65536, or sizes beyond the limits below MBD_ERR_UNSUPPORTED. Page numbers and lengths live on
+ * the device: the kernels check each before they use it (MBD_DEVERR_BAD_INDEX). What the entry points write must
+ * not overlap what they read, their cache apart; that is checked for the tensors of a call.
+ * n_seqs == 0 (append: n_tokens == 0) is a no-op; the cache's description and the sizes are checked even so.
+ */
+#define MBD_KV_ABI_VERSION 1
+int mbd_kv_abi_version(void);
+
+typedef enum { MBD_KV_BF16 = 0, MBD_KV_FP8 = 1 } mbd_kv_format;
+
+typedef struct {
+    void* k;               /* bf16 or E4M3 codes */
+    void* v;
+    float* k_scale;        /* MBD_KV_FP8 */
+    float* v_scale;
+    float* weight;         /* or null */
+    int32_t* position;     /* or null */
+    int64_t n_pages;       /* 1 .. 2^31 - 1 */
+    int64_t page_stride;   /* elements; 0: n_kv_heads * page_size * head_dim */
+    int32_t page_size;
+    int32_t n_kv_heads;
+    int32_t head_dim;
+    int32_t format;        /* mbd_kv_format */
+    int32_t mode;          /* MBD_KV_FP8: mbd_scale_mode */
+    int32_t reserved;      /* must be 0 */
+} mbd_kv_cache;
+
+/* Largest pages_per_seq * page_size, and of n_seqs * n_q_heads (append: of n_tokens). */
+#define MBD_KV_MAX_CAPACITY (1 << 30)
+#define MBD_KV_MAX_ROWS (1 << 24)
+
+/*
+ * Append the new tokens' keys and values: one per sequence (a decode step) or any number (prompts).
+ *   k, v      : n_tokens rows of n_kv_heads * head_dim bf16, row_stride elements apart (0: dense): slices of the
+ *               stacked projection need no copy.
+ *   cu_tokens : int32 [n_seqs + 1] on the device, ascending from 0: rows cu_tokens[b] .. cu_tokens[b + 1] - 1 belong to
+ *               sequence b (none, if equal). Rows from cu_tokens[n_seqs] on are padding and left alone. Null: n_tokens
+ *               == n_seqs and row b belongs to sequence b.
+ *   seq_lens  : lengths WITH the new tokens: the last of them goes to slot seq_lens[b] - 1. So the call changes no
+ *               length, and making it twice stores the same twice.
+ *   positions : int32 [n_tokens] or null (a token's position is its slot); stored if the cache has `position`.
+ * FP8: code = e4m3(value / scale), both divisions rounded to nearest; dynamic: scale = amax / 448 of the head's
+ * head_dim values, zero codes where that is 0. If the cache has `weight`, the new slots' is set to 0.
+ */
+mbd_status mbd_kv_cache_append(const mbd_kv_cache* cache, const void* k, const void* v, int64_t row_stride,
+                               const int32_t* page_table, int64_t pages_per_seq, const int32_t* seq_lens, int64_t n_seqs,
+                               int64_t n_tokens, const int32_t* cu_tokens, const int32_t* positions,
+                               mbd_stream_t stream);
+
+/*
+ * Attention of one new token per sequence over the cache. Query head h reads key-value head h / (n_q_heads /
+ * n_kv_heads). Over the slots j in view -- 0 .. seq_lens[b] - 1, with window > 0 the last `window` of them:
+ *     x_j = scale * (q . k_j),   lse = log(sum_j exp(x_j)),   out = bf16(sum_j exp(x_j - lse) * v_j)
+ * A sequence with nothing in view gives zeros and lse = -inf; what lies in masked slots is not read.
+ *   out        : [n_seqs, n_q_heads * head_dim] bf16, 16-byte aligned, written.
+ *   q          : n_seqs rows of n_q_heads * head_dim bf16, q_stride elements apart (0: dense).
+ *   scale      : finite, usually 1 / sqrt(head_dim).   window : 0 (none) or the number of slots in view.
+ *   lse        : fp32 [n_seqs, n_q_heads], written, or null.
+ *   accumulate : != 0 adds to weight[j] of each slot in view the sum of exp(x_j - lse) over the query heads that read
+ *                it (the cache must have `weight`; sequences must not share pages then).
+ *   workspace  : device memory of the caller, 256-byte aligned, mbd_paged_attention_workspace_bytes() long for the
+ *                same arguments on the same device (0 for arguments that the call refuses). It holds nothing between
+ *                calls and need not be set; calls that may run at the same time need one each.
+ * Sums are fp32; the result does not depend on what else runs, and equal calls give equal bits.
+ */
+size_t mbd_paged_attention_workspace_bytes(const mbd_kv_cache* cache, int64_t pages_per_seq, int64_t n_seqs,
+                                           int64_t n_q_heads, int accumulate);
+mbd_status mbd_paged_attention_decode(void* out, const void* q, int64_t q_stride, const mbd_kv_cache* cache,
+                                      const int32_t* page_table, int64_t pages_per_seq, const int32_t* seq_lens,
+                                      int64_t n_seqs, int64_t n_q_heads, float scale, int64_t window, float* lse,
+                                      int accumulate, void* workspace, size_t workspace_bytes, mbd_stream_t stream);
+
+/*
+ * Evict from every sequence longer than `budget` slots, each key-value head for itself: the `budget` best slots stay
+ * and become slots 0 .. budget - 1. Best are first the slots whose position is greater than (the largest position of
+ * the head's slots) - recent, then those of the greatest weight; among equals the lowest slot (NaN counts as the
+ * least weight). A slot that stays and lies before `budget` is not moved; the others that stay go, in ascending order,
+ * to the slots given up, in ascending order, with their scales, weight and position. Attention does not depend on
+ * the order of the slots; `position` keeps that of the tokens. Slots from `budget` on keep their old contents, and their
+ * pages may be freed.
+ *   new_lens : int32 [n_seqs], written: min(seq_lens[b], budget). Must not overlap seq_lens (heads read it while others
+ *              are done already).
+ *   budget   : 0 .. MBD_KV_MAX_CAPACITY;   recent : 0 .. budget.
+ * The cache must have `weight` and `position`. Limit: pages_per_seq * page_size <= MBD_KV_MAX_EVICT_CAPACITY.
+ */
+#define MBD_KV_MAX_EVICT_CAPACITY 425984
+mbd_status mbd_kv_cache_evict(const mbd_kv_cache* cache, int32_t* new_lens, const int32_t* seq_lens,
+                              const int32_t* page_table, int64_t pages_per_seq, int64_t n_seqs, int64_t budget,
+                              int64_t recent, mbd_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -60,6 +60,19 @@ class TuningEntry(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+KV_BF16, KV_FP8 = 0, 1
+KV_FORMATS = {"bf16": KV_BF16, "fp8": KV_FP8, KV_BF16: KV_BF16, KV_FP8: KV_FP8}
+
+
+class KVCache(ctypes.Structure):
+    """A paged key-value cache (the C struct mbd_kv_cache); kv_cache() makes one."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("position", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("format", ctypes.c_int32),
+                ("mode", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 OP_NAMES = {0: "add_rmsnorm", 1: "add_rmsnorm_quant_fp8", 2: "add_rmsnorm_quant_nvfp4", 3: "swiglu",
             4: "swiglu_quant_fp8", 5: "swiglu_quant_nvfp4"}
 OP_KINDS = {v: k for k, v in OP_NAMES.items()}
@@ -101,6 +114,14 @@ def _load() -> ctypes.CDLL:
     lib.mbd_tuning_set.restype = cint
     lib.mbd_tuning_get.argtypes = [ctypes.POINTER(TuningEntry), cint]
     lib.mbd_tuning_get.restype = cint
+    kvp = ctypes.POINTER(KVCache)
+    lib.mbd_kv_abi_version.restype = cint
+    lib.mbd_kv_cache_append.argtypes = [kvp, vp, vp, i64, vp, i64, vp, i64, i64, vp, vp, vp]
+    lib.mbd_paged_attention_workspace_bytes.argtypes = [kvp, i64, i64, i64, cint]
+    lib.mbd_paged_attention_workspace_bytes.restype = ctypes.c_size_t
+    lib.mbd_paged_attention_decode.argtypes = [vp, vp, i64, kvp, vp, i64, vp, i64, i64, f32, i64, vp, cint, vp,
+                                               ctypes.c_size_t, vp]
+    lib.mbd_kv_cache_evict.argtypes = [kvp, vp, vp, vp, i64, i64, i64, i64, vp]
     i32p = ctypes.POINTER(ctypes.c_int32)
     lib.mbd_launch_shape.argtypes = [cint, cint, i64, i64, i32p, i32p, i32p]
     lib.mbd_launch_shape.restype = cint
@@ -108,7 +129,8 @@ def _load() -> ctypes.CDLL:
                "mbd_fused_allreduce_add_rmsnorm", "mbd_fused_allreduce_add_rmsnorm_quant_fp8",
                "mbd_fused_add_rmsnorm_quant_nvfp4", "mbd_swiglu_quant_nvfp4", "mbd_run_program",
                "mbd_run_independent", "mbd_run_independent_with_program", "mbd_program_plan_build", "mbd_program_plan_launch", "mbd_program_plan_upload",
-               "mbd_program_plan_launch_uploaded", "mbd_program_plan_launch_static"):
+               "mbd_program_plan_launch_uploaded", "mbd_program_plan_launch_static", "mbd_kv_cache_append",
+               "mbd_paged_attention_decode", "mbd_kv_cache_evict"):
         getattr(lib, fn).restype = cint
     return lib
 
@@ -186,6 +208,7 @@ def kernel_launches() -> int:
 
 
 DEVERR_EXCHANGE_TIMEOUT = 1
+DEVERR_BAD_INDEX = 2
 
 
 def device_error_flags(clear: bool = False) -> int:
@@ -257,6 +280,56 @@ def swiglu_quant_fp8(out_q, gate_up, n_tokens: int, inter: int, mode, scale, str
 def swiglu_quant_nvfp4(out_q, out_sf, gate_up, n_tokens: int, inter: int, tensor_scale, stream=None) -> None:
     _check(get_lib().mbd_swiglu_quant_nvfp4(_ptr(out_q), _ptr(out_sf), _ptr(gate_up), int(n_tokens), int(inter),
                                             _ptr(tensor_scale), _stream(stream)), "swiglu_quant_nvfp4")
+
+
+# ------------------------------------------------------------------------------------------------ key-value cache
+
+def kv_abi_version() -> int:
+    return get_lib().mbd_kv_abi_version()
+
+
+def kv_cache(k, v, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, fmt="bf16", mode="static", k_scale=None,
+             v_scale=None, weight=None, position=None, page_stride: int = 0) -> KVCache:
+    """The description of a paged cache: pools k and v of n_pages pages [n_kv_heads, page_size, head_dim], page_stride
+    elements apart (0: dense), in `fmt` "bf16" or "fp8" (with `mode` and scales), and the accumulated weights and
+    positions of a cache that evicts. It holds the tensors' device pointers, not the tensors."""
+    return KVCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(weight), _ptr(position), int(n_pages),
+                   int(page_stride), int(page_size), int(n_kv_heads), int(head_dim),
+                   KV_FORMATS[fmt] if isinstance(fmt, str) else int(fmt), _mode(mode), 0)
+
+
+def kv_cache_append(cache: KVCache, k, v, row_stride: int, page_table, pages_per_seq: int, seq_lens, n_seqs: int,
+                    n_tokens: int, cu_tokens=None, positions=None, stream=None) -> None:
+    """Store the new tokens' keys and values; seq_lens are the lengths with them (mbd_kv_cache_append)."""
+    _check(get_lib().mbd_kv_cache_append(cache, _ptr(k), _ptr(v), int(row_stride), _ptr(page_table), int(pages_per_seq),
+                                         _ptr(seq_lens), int(n_seqs), int(n_tokens), _ptr(cu_tokens), _ptr(positions),
+                                         _stream(stream)), "kv_cache_append")
+
+
+def paged_attention_workspace_bytes(cache: KVCache, pages_per_seq: int, n_seqs: int, n_q_heads: int,
+                                    accumulate: bool = False) -> int:
+    """Device bytes that paged_attention_decode needs for these arguments on the current device."""
+    return int(get_lib().mbd_paged_attention_workspace_bytes(cache, int(pages_per_seq), int(n_seqs), int(n_q_heads),
+                                                             int(bool(accumulate))))
+
+
+def paged_attention_decode(out, q, q_stride: int, cache: KVCache, page_table, pages_per_seq: int, seq_lens,
+                           n_seqs: int, n_q_heads: int, scale: float, window: int = 0, lse=None,
+                           accumulate: bool = False, workspace=None, workspace_bytes: int = 0, stream=None) -> None:
+    """Attention of one new token per sequence over the cache (mbd_paged_attention_decode)."""
+    _check(get_lib().mbd_paged_attention_decode(_ptr(out), _ptr(q), int(q_stride), cache, _ptr(page_table),
+                                                int(pages_per_seq), _ptr(seq_lens), int(n_seqs), int(n_q_heads),
+                                                float(scale), int(window), _ptr(lse), int(bool(accumulate)),
+                                                _ptr(workspace), int(workspace_bytes), _stream(stream)),
+           "paged_attention_decode")
+
+
+def kv_cache_evict(cache: KVCache, new_lens, seq_lens, page_table, pages_per_seq: int, n_seqs: int, budget: int,
+                   recent: int, stream=None) -> None:
+    """Keep the `budget` slots of the greatest accumulated weight, the newest `recent` in any case
+    (mbd_kv_cache_evict)."""
+    _check(get_lib().mbd_kv_cache_evict(cache, _ptr(new_lens), _ptr(seq_lens), _ptr(page_table), int(pages_per_seq),
+                                        int(n_seqs), int(budget), int(recent), _stream(stream)), "kv_cache_evict")
 
 
 # ------------------------------------------------------------------------------------------------ programs

@@ -11,6 +11,7 @@
 #include <cuda.h>
 
 #include "mbd.h"
+#include "kv.h"
 #include "launch.h"
 
 namespace mbd {
@@ -889,6 +890,13 @@ mbd_status run_independent(const PlanImpl* plan, const void* schedule, const mbd
 
 }  // namespace
 
+namespace mbd {
+
+int kv_sm_count() { return sm_count_of_current_device(); }
+int kv_finish_launch(cudaError_t e) { return finish_launch(e); }
+
+}  // namespace mbd
+
 extern "C" {
 
 int mbd_abi_version(void) { return MBD_ABI_VERSION; }
@@ -916,12 +924,15 @@ mbd_status mbd_device_error_flags(uint32_t* flags, int clear) {
     if (e == cudaSuccess) e = mbd::device_error_flags_selftest(&c, clear != 0);
     unsigned int d = 0;
     if (e == cudaSuccess) e = mbd::device_error_flags_program(&d, clear != 0);
+    unsigned int f = 0, g = 0;
+    if (e == cudaSuccess) e = mbd::device_error_flags_kv_cache(&f, clear != 0);
+    if (e == cudaSuccess) e = mbd::device_error_flags_kv_attention(&g, clear != 0);
     if (e != cudaSuccess) {
         g_last_cuda_error = static_cast<int>(e);
         (void)cudaGetLastError();
         return MBD_ERR_CUDA;
     }
-    *flags = a | b | c | d;
+    *flags = a | b | c | d | f | g;
     return MBD_OK;
 }
 

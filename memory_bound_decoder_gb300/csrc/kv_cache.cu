@@ -1,0 +1,412 @@
+// Paged key-value cache: appending new tokens, and eviction by accumulated attention weight.
+//
+// Append. Row (token t, head h) of the stacked projection goes to slot lens[seq] - (new tokens of seq) + i of its
+// sequence, as it is (bf16) or as E4M3 codes of value / scale; the dynamic scale is amax / 448 of the head's row.
+// Both divisions are IEEE divisions, so codes and scales are those of the definition, ties included. Bound by
+// bytes (2 D in, D or 2 D out for each of k and v) and, for a decode step's few rows, by latency. head_dim / 8
+// lanes own a row, 16 bytes of k and of v each, so the maximum of a row is a few shuffles and nothing is staged.
+//
+// Eviction. Of the `len` slots of one sequence and head the `budget` best stay: first those whose position is
+// among the newest `recent`, then those of the largest weight, equal ones by the lowest slot. A kept row behind
+// the budget moves into a slot before it that is given up, the i-th such row into the i-th such slot, so sources
+// (>= budget) and destinations (< budget) never meet: nothing is staged, rows that may stay where they are do, and
+// the order of the moves is free. One cluster owns a sequence's head: each CTA keeps its share of the slots as
+// order-preserving 32-bit keys in shared memory (read from HBM once), the budget-th largest key is found by a
+// radix selection of 8 bits a pass whose histograms are added up through distributed shared memory, and the
+// ranks of the moving rows come from ballots and one scan in slot order.
+#include <cooperative_groups.h>
+
+#include "kv_common.cuh"
+
+namespace mbd {
+
+namespace {
+
+// ------------------------------------------------------------------------------------------ append
+
+constexpr int kAppendThreads = 256;
+constexpr int kAppendMaxTokens = 16;   // tokens of one CTA
+
+// The sequence that owns row t of the new tokens: the last b with cu[b] <= t.
+__device__ __forceinline__ int64_t owner_of(const int32_t* cu, int64_t n_seqs, int64_t t) {
+    int64_t lo = 0, hi = n_seqs;
+    while (hi - lo > 1) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (cu[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+struct Quad {
+    float v[8];
+};
+
+__device__ __forceinline__ Quad unpack(const uint4& w) {
+    Quad q;
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        q.v[2 * i] = bf16_lo(x[i]);
+        q.v[2 * i + 1] = bf16_hi(x[i]);
+    }
+    return q;
+}
+
+// Eight values over one scale as E4M3 codes; a zero scale gives zero codes.
+__device__ __forceinline__ uint2 encode(const Quad& q, float scale) {
+    if (scale == 0.0f) return make_uint2(0u, 0u);
+    float d[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d[i] = __fdiv_rn(q.v[i], scale);
+    return make_uint2(pack_e4m3x4(d[0], d[1], d[2], d[3]), pack_e4m3x4(d[4], d[5], d[6], d[7]));
+}
+
+template <int STORE, int LANES>   // LANES = head_dim / 8: the lanes that own one head's row
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ AppendParams p,
+                                                                   int tokens_per_cta) {
+    __shared__ int64_t s_page[kAppendMaxTokens], s_slot[kAppendMaxTokens];
+    pdl_trigger();
+    pdl_wait();
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * tokens_per_cta;
+    const int tid = threadIdx.x;
+    if (tid < tokens_per_cta) {
+        const int64_t t = first + tid;
+        int64_t page = -1, slot = 0;
+        if (t < p.n_tokens) {
+            const int64_t seq = p.cu_tokens ? owner_of(p.cu_tokens, p.n_seqs, t) : t;
+            const int64_t begin = p.cu_tokens ? p.cu_tokens[seq] : t, end = p.cu_tokens ? p.cu_tokens[seq + 1] : t + 1;
+            if (t >= begin && t < end) {   // rows behind the last sequence's are padding
+                slot = static_cast<int64_t>(p.seq_lens[seq]) - end + t;
+                if (slot >= 0 && slot < p.c.capacity) page = kv_page(p.c, seq, slot);
+                else kv_bad_index();
+            }
+        }
+        s_page[tid] = page;
+        s_slot[tid] = slot;
+    }
+    __syncthreads();
+    float ks = 0.0f, vs = 0.0f;
+    if constexpr (STORE == kKvFp8Static) {
+        ks = *p.c.k_scale;
+        vs = *p.c.v_scale;
+    }
+    const int per_token = p.c.n_kv_heads * LANES;      // 16-byte vectors of one token's keys
+    const int total = tokens_per_cta * per_token;
+    const int lane = tid % LANES;
+    // Every lane of a warp stays in the loop as long as one of them has a row: the dynamic scale shuffles.
+    for (int base = tid - (tid & 31); base < total; base += kAppendThreads) {
+        const int i = base + (tid & 31);
+        const int local = i / per_token, head = (i - local * per_token) / LANES;
+        const int64_t page = i < total ? s_page[local] : -1, slot = i < total ? s_slot[local] : 0;
+        const bool live = page >= 0;
+        uint4 k = make_uint4(0, 0, 0, 0), v = k;
+        const int64_t t = first + local;
+        if (live) {
+            const int64_t at = t * p.row_bytes + (static_cast<int64_t>(head) * LANES + lane) * 16;
+            k = load_stream(reinterpret_cast<const uint4*>(static_cast<const char*>(p.k) + at));
+            v = load_stream(reinterpret_cast<const uint4*>(static_cast<const char*>(p.v) + at));
+        }
+        const int64_t meta = live ? kv_meta(p.c, page, head, slot) : 0;
+        if constexpr (STORE == kKvBf16) {
+            if (live) {
+                const int64_t to = kv_row(p.c, page, head, slot, LANES * 16) + lane * 16;
+                *reinterpret_cast<uint4*>(static_cast<char*>(p.c.k) + to) = k;
+                *reinterpret_cast<uint4*>(static_cast<char*>(p.c.v) + to) = v;
+            }
+        } else {
+            const Quad a = unpack(k), b = unpack(v);
+            if constexpr (STORE == kKvFp8Dynamic) {
+                float ka = 0.0f, va = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    ka = fmaxf(ka, fabsf(a.v[e]));
+                    va = fmaxf(va, fabsf(b.v[e]));
+                }
+#pragma unroll
+                for (int o = LANES / 2; o > 0; o >>= 1) {
+                    ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, o));
+                    va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, o));
+                }
+                ks = __fdiv_rn(ka, 448.0f);
+                vs = __fdiv_rn(va, 448.0f);
+                if (live && lane == 0) {
+                    p.c.k_scale[meta] = ks;
+                    p.c.v_scale[meta] = vs;
+                }
+            }
+            if (live) {
+                const int64_t to = kv_row(p.c, page, head, slot, LANES * 8) + lane * 8;
+                *reinterpret_cast<uint2*>(static_cast<char*>(p.c.k) + to) = encode(a, ks);
+                *reinterpret_cast<uint2*>(static_cast<char*>(p.c.v) + to) = encode(b, vs);
+            }
+        }
+        if (live && lane == 0) {
+            if (p.c.weight) p.c.weight[meta] = 0.0f;
+            if (p.c.position) p.c.position[meta] = p.positions ? p.positions[t] : static_cast<int32_t>(slot);
+        }
+    }
+}
+
+template <int STORE>
+cudaError_t launch_append(const AppendParams& p, unsigned grid, int tokens, cudaStream_t s) {
+    switch (p.c.head_dim) {
+        case 64: return kv_launch(kv_append_kernel<STORE, 8>, grid, kAppendThreads, 0, 1, s, p, tokens);
+        case 128: return kv_launch(kv_append_kernel<STORE, 16>, grid, kAppendThreads, 0, 1, s, p, tokens);
+        case 256: return kv_launch(kv_append_kernel<STORE, 32>, grid, kAppendThreads, 0, 1, s, p, tokens);
+    }
+    return cudaErrorInvalidValue;
+}
+
+// ------------------------------------------------------------------------------------------ eviction
+
+constexpr int kEvictThreads = 512;
+constexpr int kEvictWarps = kEvictThreads / 32;
+
+struct EvictSmem {
+    unsigned hist[2][256];   // alternate: peers may still read one while the next is cleared
+    unsigned warp_sum[kEvictWarps][2];
+    unsigned total[2][2];    // this CTA's counts, read by its peers
+    int max_position;
+    unsigned bin, need, count;
+};
+
+// A weight as an unsigned key of the same order; -0 counts as 0 and what is not a number comes last.
+__device__ __forceinline__ uint32_t order_key(float w) {
+    if (w != w) return 0u;
+    const uint32_t u = w == 0.0f ? 0u : __float_as_uint(w);
+    return u ^ ((u & 0x80000000u) ? 0xffffffffu : 0x80000000u);
+}
+
+// Exclusive sums over the warps of two counts per warp, and the CTA's totals in sm.total[which]. One barrier in,
+// one out.
+__device__ __forceinline__ uint2 scan_warps(EvictSmem& sm, unsigned a, unsigned b, int which) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __syncthreads();
+    if (lane == 0) {
+        sm.warp_sum[warp][0] = a;
+        sm.warp_sum[warp][1] = b;
+    }
+    __syncthreads();
+    uint2 before = make_uint2(0, 0), all = before;
+    for (int w = 0; w < kEvictWarps; ++w) {
+        const unsigned x = sm.warp_sum[w][0], y = sm.warp_sum[w][1];
+        if (w < warp) before = make_uint2(before.x + x, before.y + y);
+        all = make_uint2(all.x + x, all.y + y);
+    }
+    if (threadIdx.x == 0) {
+        sm.total[which][0] = all.x;
+        sm.total[which][1] = all.y;
+    }
+    return before;
+}
+
+__global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const __grid_constant__ EvictParams p) {
+    extern __shared__ uint32_t slots[];   // keys [slots_per_cta], then positions, later the lists of moves
+    __shared__ EvictSmem sm;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ctas = p.ctas_per_row, rank = static_cast<int>(blockIdx.x) % ctas;
+    const int64_t row = blockIdx.x / ctas;
+    const int64_t seq = row / p.c.n_kv_heads;
+    const int head = static_cast<int>(row - seq * p.c.n_kv_heads);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    pdl_trigger();
+    pdl_wait();
+    const int64_t len = kv_len(p.c, p.seq_lens[seq]);
+    if (head == 0 && rank == 0 && tid == 0) p.new_lens[seq] = static_cast<int32_t>(len < p.budget ? len : p.budget);
+    if (len <= p.budget || p.budget == 0) return;   // the whole cluster
+
+    const int share = static_cast<int>((len + ctas - 1) / ctas);
+    const int64_t first = static_cast<int64_t>(rank) * share;
+    const int n = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(share), len - first)));
+    uint32_t* key = slots;
+    int* aux = reinterpret_cast<int*>(slots + p.slots_per_cta);
+
+    int newest = INT32_MIN;
+    for (int i = tid; i < n; i += kEvictThreads) {
+        const int64_t page = kv_page(p.c, seq, first + i);
+        uint32_t k = 0u;
+        int at = INT32_MIN;
+        if (page >= 0) {
+            const int64_t m = kv_meta(p.c, page, head, first + i);
+            k = order_key(p.c.weight[m]);
+            at = p.c.position[m];
+        }
+        key[i] = k;
+        aux[i] = at;
+        newest = max(newest, at);
+    }
+    if (tid == 0) sm.max_position = INT32_MIN;
+    if (tid < 256) sm.hist[0][tid] = 0;
+    __syncthreads();
+    newest = __reduce_max_sync(0xffffffffu, newest);
+    if (lane == 0) atomicMax(&sm.max_position, newest);
+    if (p.recent > 0) {   // protected slots come before every weight
+        cluster.sync();
+        int all = INT32_MIN;
+        for (int r = 0; r < ctas; ++r) all = max(all, *cluster.map_shared_rank(&sm.max_position, r));
+        const int64_t from = static_cast<int64_t>(all) - p.recent;
+        for (int i = tid; i < n; i += kEvictThreads)
+            if (aux[i] > from) key[i] = 0xffffffffu;
+        __syncthreads();
+    }
+
+    // The budget-th largest key: kept are the slots whose masked key is above `value`, and `need` of the `count`
+    // slots where it is equal to it.
+    uint32_t mask = 0, value = 0;
+    unsigned need = static_cast<unsigned>(p.budget), count = 0;
+    for (int pass = 0; pass < 4; ++pass) {
+        const int shift = 24 - 8 * pass;
+        unsigned* hist = sm.hist[pass & 1];
+        for (int i = tid; i < n; i += kEvictThreads)
+            if ((key[i] & mask) == value) atomicAdd(&hist[(key[i] >> shift) & 255u], 1u);
+        cluster.sync();
+        unsigned mine = 0, at_least = 0;
+        if (tid < 256) {
+            for (int r = 0; r < ctas; ++r) mine += cluster.map_shared_rank(hist, r)[tid];
+            sm.hist[(pass + 1) & 1][tid] = 0;
+            at_least = mine;   // of this bin and the higher ones: within the warp, then over the warps
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned x = __shfl_down_sync(0xffffffffu, at_least, o);
+                if (lane + o < 32) at_least += x;
+            }
+            if (lane == 0) sm.warp_sum[warp][0] = at_least;
+        }
+        __syncthreads();
+        if (tid < 256) {
+            for (int w = warp + 1; w < 8; ++w) at_least += sm.warp_sum[w][0];
+            if (at_least >= need && at_least - mine < need) {
+                sm.bin = tid;
+                sm.need = need - (at_least - mine);
+                sm.count = mine;
+            }
+        }
+        __syncthreads();
+        mask |= 255u << shift;
+        value |= sm.bin << shift;
+        need = sm.need;
+        count = sm.count;
+        if (need == count) break;   // all of them stay: the lower bits decide nothing
+        __syncthreads();            // bin, need and count are read before the next pass writes them
+    }
+
+    // Ranks in slot order: each warp owns a contiguous share of this CTA's slots, 32 at a time.
+    const int per_warp = (n + kEvictThreads - 1) / kEvictThreads * 32;
+    const int lo = min(n, warp * per_warp), hi = min(n, lo + per_warp);
+    unsigned equal_before = 0;
+    if (need != count) {
+        unsigned equal = 0;
+        for (int i = lo; i < hi; i += 32)
+            equal += __popc(__ballot_sync(0xffffffffu, i + lane < hi && (key[i + lane] & mask) == value));
+        equal_before = scan_warps(sm, equal, 0, 0).x;
+        cluster.sync();
+        for (int r = 0; r < rank; ++r) equal_before += cluster.map_shared_rank(&sm.total[0][0], r)[0];
+    }
+    // kept(): whether lane's slot i + lane stays; `equal` counts the equal slots before i.
+    auto kept = [&](int i, unsigned& equal) {
+        const bool in = i + lane < hi;
+        const uint32_t k = in ? key[i + lane] & mask : 0u;
+        const bool same = in && k == value;
+        bool keep = in && k > value;
+        if (need == count) return keep || same;
+        const unsigned who = __ballot_sync(0xffffffffu, same);
+        keep |= same && equal + __popc(who & ((1u << lane) - 1u)) < need;
+        equal += __popc(who);
+        return keep;
+    };
+    unsigned holes = 0, movers = 0, equal = equal_before;
+    for (int i = lo; i < hi; i += 32) {
+        const bool in = i + lane < hi, low = first + i + lane < p.budget, keep = kept(i, equal);
+        holes += __popc(__ballot_sync(0xffffffffu, in && low && !keep));
+        movers += __popc(__ballot_sync(0xffffffffu, in && !low && keep));
+    }
+    uint2 at = scan_warps(sm, holes, movers, 1);
+    cluster.sync();
+    unsigned moves = 0;
+    for (int r = 0; r < ctas; ++r) {
+        const unsigned* t = cluster.map_shared_rank(&sm.total[1][0], r);
+        if (r < rank) at = make_uint2(at.x + t[0], at.y + t[1]);
+        moves += t[1];
+    }
+    // The lists, entry i with CTA i / chunk of the cluster: slots given up, then the rows that take their places.
+    const unsigned chunk = (moves + ctas - 1) / ctas;
+    if (moves > 0) {
+        const unsigned below = (1u << lane) - 1u;
+        equal = equal_before;
+        for (int i = lo; i < hi; i += 32) {
+            const bool in = i + lane < hi, low = first + i + lane < p.budget, keep = kept(i, equal);
+            const unsigned h = __ballot_sync(0xffffffffu, in && low && !keep);
+            const unsigned m = __ballot_sync(0xffffffffu, in && !low && keep);
+            const bool hole = (h >> lane) & 1u, mover = (m >> lane) & 1u;
+            if (hole || mover) {
+                const unsigned e = hole ? at.x + __popc(h & below) : at.y + __popc(m & below);
+                int* list = cluster.map_shared_rank(aux, e / chunk);
+                list[(e % chunk) * 2 + (mover ? 1 : 0)] = static_cast<int>(first) + i + lane;
+            }
+            at = make_uint2(at.x + __popc(h), at.y + __popc(m));
+        }
+    }
+    cluster.sync();   // the lists are complete; no CTA touches another's shared memory from here on
+    if (moves == 0) return;
+    const int mine = static_cast<int>(max(0, min(static_cast<int>(chunk), static_cast<int>(moves) - rank * static_cast<int>(chunk))));
+    const int row_bytes = p.c.head_dim * (p.c.store == kKvBf16 ? 2 : 1);
+    const int lanes = row_bytes / 16, part = tid % lanes;   // 4 to 32 lanes own a row
+    for (int i = tid / lanes; i < mine; i += kEvictThreads / lanes) {
+        const int64_t to = aux[2 * i], from = aux[2 * i + 1];
+        const int64_t page_to = kv_page(p.c, seq, to), page_from = kv_page(p.c, seq, from);
+        if (page_to < 0 || page_from < 0) continue;
+        const int64_t a = kv_row(p.c, page_from, head, from, row_bytes) + part * 16;
+        const int64_t b = kv_row(p.c, page_to, head, to, row_bytes) + part * 16;
+        const uint4 k = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.c.k) + a);
+        const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.c.v) + a);
+        *reinterpret_cast<uint4*>(static_cast<char*>(p.c.k) + b) = k;
+        *reinterpret_cast<uint4*>(static_cast<char*>(p.c.v) + b) = v;
+        const int64_t ma = kv_meta(p.c, page_from, head, from), mb = kv_meta(p.c, page_to, head, to);
+        if (part == 0) p.c.weight[mb] = p.c.weight[ma];
+        if (part == 1) p.c.position[mb] = p.c.position[ma];
+        if (p.c.store == kKvFp8Dynamic) {
+            if (part == 2) p.c.k_scale[mb] = p.c.k_scale[ma];
+            if (part == 3) p.c.v_scale[mb] = p.c.v_scale[ma];
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const AppendParams& p, int sms, cudaStream_t s) {
+    // Few tokens: one to a CTA, as many SMs as there are. Many: up to 16, so that a CTA has several rows to load
+    // at once.
+    int64_t tokens = p.n_tokens / (4 * int64_t{sms});
+    tokens = tokens < 1 ? 1 : (tokens > kAppendMaxTokens ? kAppendMaxTokens : tokens);
+    const unsigned grid = static_cast<unsigned>((p.n_tokens + tokens - 1) / tokens);
+    const int t = static_cast<int>(tokens);
+    switch (p.c.store) {
+        case kKvBf16: return launch_append<kKvBf16>(p, grid, t, s);
+        case kKvFp8Static: return launch_append<kKvFp8Static>(p, grid, t, s);
+        case kKvFp8Dynamic: return launch_append<kKvFp8Dynamic>(p, grid, t, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_kv_evict(const EvictParams& p, cudaStream_t s) {
+    const size_t smem = (static_cast<size_t>(p.slots_per_cta) * 2 + 4) * sizeof(uint32_t);
+    cudaError_t e = cudaSuccess;
+    if (smem > 40 * 1024)
+        e = cudaFuncSetAttribute(kv_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e == cudaSuccess && p.ctas_per_row > 8)
+        e = cudaFuncSetAttribute(kv_evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = static_cast<unsigned>(p.n_seqs * p.c.n_kv_heads * p.ctas_per_row);
+    return kv_launch(kv_evict_kernel, grid, kEvictThreads, smem, p.ctas_per_row, s, p);
+}
+
+cudaError_t device_error_flags_kv_cache(unsigned int* flags, bool clear) {
+    cudaError_t e = cudaMemcpyFromSymbol(flags, g_device_error_flags, sizeof(unsigned int));
+    if (e == cudaSuccess && clear) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_device_error_flags, &zero, sizeof(unsigned int));
+    }
+    return e;
+}
+
+}  // namespace mbd
