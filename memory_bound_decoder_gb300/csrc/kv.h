@@ -60,6 +60,12 @@ struct AttendParams {
     float scale_log2;           // scale * log2(e)
     int n_q_heads;
     int group;                  // query heads of a key-value head
+    int chunk_heads;            // query heads that a CTA takes at once: 8 or 16
+    int chunks;                 // of a group
+    int grid;                   // CTAs: the shares that the work is cut into
+    float* part_o;              // workspace: [grid, 2, chunk_heads, head_dim], sums of the items that are cut
+    float4* part_ml;            // workspace: [grid, 2, chunk_heads], their maxima, sums and exponents
+    int4* cut;                  // workspace: [grid], the item that begins in a share and ends in a later one
     int logit_heads;
     int accumulate;
 };
@@ -74,6 +80,12 @@ struct EvictParams {
     int ctas_per_row;           // cluster size: the CTAs that share one sequence's head
     int slots_per_cta;          // slots of the longest row that one of them holds
 };
+
+// How the attention covers a call: chunk_heads, chunks and grid of AttendParams; `rows`: n_seqs * n_kv_heads.
+struct AttendPlan {
+    int chunk_heads, chunks, grid;
+};
+void plan_kv_attend(int head_dim, int store, int group, int sms, int64_t capacity, int64_t rows, AttendPlan* plan);
 
 cudaError_t launch_kv_append(const AppendParams& p, int sms, cudaStream_t s);
 cudaError_t launch_kv_attend(const AttendParams& p, cudaStream_t s);

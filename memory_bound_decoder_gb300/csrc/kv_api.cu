@@ -40,6 +40,11 @@ int log2_of(int64_t x) {
     return n;
 }
 
+int store_of(const mbd_kv_cache* c) {
+    if (c->format == MBD_KV_BF16) return mbd::kKvBf16;
+    return c->mode == MBD_SCALE_DYNAMIC_PER_TOKEN ? mbd::kKvFp8Dynamic : mbd::kKvFp8Static;
+}
+
 // Sizes and kinds (pointers apart), and the table's extent. They are checked for empty calls too.
 mbd_status check_shape(const mbd_kv_cache* c, int64_t pages_per_seq, int64_t n_seqs) {
     if (!c || c->reserved != 0 || (c->format != MBD_KV_BF16 && c->format != MBD_KV_FP8)) return MBD_ERR_INVALID_ARG;
@@ -64,8 +69,7 @@ mbd_status check_shape(const mbd_kv_cache* c, int64_t pages_per_seq, int64_t n_s
 }
 
 // The pointers of a cache whose shape has been checked.
-mbd_status check_cache(const mbd_kv_cache* c, const int32_t* page_table, int64_t pages_per_seq, int64_t n_seqs,
-                       Cache* out) {
+mbd_status check_cache(const mbd_kv_cache* c, const int32_t* page_table, int64_t pages_per_seq, Cache* out) {
     const bool fp8 = c->format == MBD_KV_FP8, dynamic = fp8 && c->mode == MBD_SCALE_DYNAMIC_PER_TOKEN;
     const uint64_t size = fp8 ? 1 : 2;
     if (!c->k || !c->v || !page_table || (fp8 && (!c->k_scale || !c->v_scale))) return MBD_ERR_INVALID_ARG;
@@ -108,8 +112,7 @@ mbd_status check_cache(const mbd_kv_cache* c, const int32_t* page_table, int64_t
     v.capacity = pages_per_seq << v.page_shift;
     v.n_kv_heads = c->n_kv_heads;
     v.head_dim = c->head_dim;
-    v.store = !fp8 ? mbd::kKvBf16 : (dynamic ? mbd::kKvFp8Dynamic : mbd::kKvFp8Static);
-    (void)n_seqs;
+    v.store = store_of(c);
     return MBD_OK;
 }
 
@@ -126,20 +129,30 @@ mbd_status check_stride(int64_t* stride, int64_t width) {
     return MBD_OK;
 }
 
-// Parts of the attention's workspace, in bytes from its start.
-struct AttendWorkspace {
-    uint64_t lse2, logits, total;
-};
-
 uint64_t round_up(uint64_t n) { return (n + 255) / 256 * 256; }
 
-AttendWorkspace attend_workspace(const mbd_kv_cache* c, int64_t pages_per_seq, int64_t n_seqs, int64_t n_q_heads,
-                                 int accumulate) {
-    AttendWorkspace w{};
+// The attention's plan, and the parts of its workspace in bytes from its start.
+struct AttendLayout {
+    mbd::AttendPlan plan;
+    int logit_heads;
+    uint64_t part_o, part_ml, cut, lse2, logits, total;
+};
+
+AttendLayout attend_layout(const mbd_kv_cache* c, int64_t pages_per_seq, int64_t n_seqs, int64_t n_q_heads,
+                           int accumulate) {
+    AttendLayout w{};
+    const int group = static_cast<int>(n_q_heads / c->n_kv_heads);
+    const int64_t capacity = pages_per_seq * c->page_size;
+    mbd::plan_kv_attend(c->head_dim, store_of(c), group, mbd::kv_sm_count(), capacity, n_seqs * c->n_kv_heads, &w.plan);
+    w.logit_heads = (group + 1) / 2 * 2;   // pairs of heads are stored together
+    const uint64_t parts = uint64_t(w.plan.grid) * 2 * w.plan.chunk_heads;
+    w.part_ml = round_up(parts * c->head_dim * 4);
+    w.cut = w.part_ml + round_up(parts * 16);
+    w.total = w.cut + round_up(uint64_t(w.plan.grid) * 16);
     if (!accumulate) return w;
-    w.lse2 = 0;
-    w.logits = round_up(uint64_t(n_seqs) * n_q_heads * 4);
-    w.total = w.logits + round_up(uint64_t(n_seqs) * n_q_heads * pages_per_seq * c->page_size * 4);
+    w.lse2 = w.total;
+    w.logits = w.lse2 + round_up(uint64_t(n_seqs) * n_q_heads * 4);
+    w.total = w.logits + round_up(uint64_t(n_seqs) * c->n_kv_heads * capacity * w.logit_heads * 4);
     return w;
 }
 
@@ -173,7 +186,7 @@ mbd_status mbd_kv_cache_append(const mbd_kv_cache* cache, const void* k, const v
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(seq_lens, 4) || !aligned(cu_tokens, 4) || !aligned(positions, 4))
         return MBD_ERR_MISALIGNED;
     Cache c;
-    st = check_cache(cache, page_table, pages_per_seq, n_seqs, &c);
+    st = check_cache(cache, page_table, pages_per_seq, &c);
     if (st != MBD_OK) return st;
     const uint64_t rows = rows_bytes(n_tokens, row_stride, width);
     const Range reads[] = {{k, rows},
@@ -203,7 +216,7 @@ mbd_status mbd_kv_cache_append(const mbd_kv_cache* cache, const void* k, const v
 size_t mbd_paged_attention_workspace_bytes(const mbd_kv_cache* cache, int64_t pages_per_seq, int64_t n_seqs,
                                            int64_t n_q_heads, int accumulate) {
     if (check_attend(cache, pages_per_seq, n_seqs, n_q_heads) != MBD_OK || n_seqs == 0) return 0;
-    return attend_workspace(cache, pages_per_seq, n_seqs, n_q_heads, accumulate).total;
+    return attend_layout(cache, pages_per_seq, n_seqs, n_q_heads, accumulate).total;
 }
 
 mbd_status mbd_paged_attention_decode(void* out, const void* q, int64_t q_stride, const mbd_kv_cache* cache,
@@ -220,18 +233,16 @@ mbd_status mbd_paged_attention_decode(void* out, const void* q, int64_t q_stride
     if (!out || !q || !seq_lens || (accumulate && !cache->weight)) return MBD_ERR_INVALID_ARG;
     if (!aligned(out, 16) || !aligned(q, 16) || !aligned(seq_lens, 4) || !aligned(lse, 4)) return MBD_ERR_MISALIGNED;
     Cache c;
-    st = check_cache(cache, page_table, pages_per_seq, n_seqs, &c);
+    st = check_cache(cache, page_table, pages_per_seq, &c);
     if (st != MBD_OK) return st;
-    const AttendWorkspace ws = attend_workspace(cache, pages_per_seq, n_seqs, n_q_heads, accumulate);
-    if (ws.total > 0) {
-        if (!workspace || workspace_bytes < ws.total) return MBD_ERR_INVALID_ARG;
-        if (!aligned(workspace, 256)) return MBD_ERR_MISALIGNED;
-    }
+    const AttendLayout ws = attend_layout(cache, pages_per_seq, n_seqs, n_q_heads, accumulate);
+    if (!workspace || workspace_bytes < ws.total) return MBD_ERR_INVALID_ARG;
+    if (!aligned(workspace, 256)) return MBD_ERR_MISALIGNED;
     const Range table{page_table, uint64_t(n_seqs) * pages_per_seq * 4}, lens{seq_lens, uint64_t(n_seqs) * 4};
     const Range qr{q, rows_bytes(n_seqs, q_stride, width)}, none{nullptr, 0};
     const Range writes[] = {{out, uint64_t(n_seqs) * width * 2},
                             {lse, uint64_t(n_seqs) * n_q_heads * 4},
-                            {ws.total ? workspace : nullptr, ws.total},
+                            {workspace, ws.total},
                             accumulate ? c.weight : none};
     for (const Range& r : {qr, table, lens, c.k, c.v, c.k_scale, c.v_scale})
         if (overlaps_any(r, writes)) return MBD_ERR_INVALID_ARG;
@@ -251,9 +262,15 @@ mbd_status mbd_paged_attention_decode(void* out, const void* q, int64_t q_stride
     p.scale_log2 = scale * 1.44269504088896341f;
     p.n_q_heads = static_cast<int>(n_q_heads);
     p.group = static_cast<int>(n_q_heads / cache->n_kv_heads);
-    p.logit_heads = p.group;
+    p.chunk_heads = ws.plan.chunk_heads;
+    p.chunks = ws.plan.chunks;
+    p.grid = ws.plan.grid;
+    p.logit_heads = ws.logit_heads;
     p.accumulate = accumulate != 0;
     char* base = static_cast<char*>(workspace);
+    p.part_o = reinterpret_cast<float*>(base + ws.part_o);
+    p.part_ml = reinterpret_cast<float4*>(base + ws.part_ml);
+    p.cut = reinterpret_cast<int4*>(base + ws.cut);
     p.lse2 = reinterpret_cast<float*>(base + ws.lse2);
     p.logits = reinterpret_cast<float*>(base + ws.logits);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -276,7 +293,7 @@ mbd_status mbd_kv_cache_evict(const mbd_kv_cache* cache, int32_t* new_lens, cons
     if (!new_lens || !seq_lens || !cache->weight || !cache->position) return MBD_ERR_INVALID_ARG;
     if (!aligned(new_lens, 4) || !aligned(seq_lens, 4)) return MBD_ERR_MISALIGNED;
     Cache c;
-    st = check_cache(cache, page_table, pages_per_seq, n_seqs, &c);
+    st = check_cache(cache, page_table, pages_per_seq, &c);
     if (st != MBD_OK) return st;
     const Range lens{new_lens, uint64_t(n_seqs) * 4};
     const Range table{page_table, uint64_t(n_seqs) * pages_per_seq * 4}, old{seq_lens, uint64_t(n_seqs) * 4};
