@@ -19,8 +19,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libmbd.so")
 SOURCES = ["api.cu", "norm.cu", "swiglu.cu", "program.cu", "selftest.cu", "kv_api.cu", "kv_cache.cu",
-           "kv_attention.cu"]
-HEADERS = ["common.cuh", "launch.h", "norm_impl.cuh", "swiglu_impl.cuh", "kv.h", "kv_common.cuh"]
+           "kv_attention.cu", "kv_attention_fp8.cu", "kv_attention_fp8_dynamic.cu"]
+HEADERS = ["common.cuh", "launch.h", "norm_impl.cuh", "swiglu_impl.cuh", "kv.h", "kv_common.cuh",
+           "kv_attention_impl.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]

@@ -924,15 +924,19 @@ mbd_status mbd_device_error_flags(uint32_t* flags, int clear) {
     if (e == cudaSuccess) e = mbd::device_error_flags_selftest(&c, clear != 0);
     unsigned int d = 0;
     if (e == cudaSuccess) e = mbd::device_error_flags_program(&d, clear != 0);
-    unsigned int f = 0, g = 0;
-    if (e == cudaSuccess) e = mbd::device_error_flags_kv_cache(&f, clear != 0);
-    if (e == cudaSuccess) e = mbd::device_error_flags_kv_attention(&g, clear != 0);
+    unsigned int kv = 0;
+    for (auto read : {mbd::device_error_flags_kv_cache, mbd::device_error_flags_kv_attention,
+                      mbd::device_error_flags_kv_attention_fp8, mbd::device_error_flags_kv_attention_fp8_dynamic}) {
+        unsigned int f = 0;
+        if (e == cudaSuccess) e = read(&f, clear != 0);
+        kv |= f;
+    }
     if (e != cudaSuccess) {
         g_last_cuda_error = static_cast<int>(e);
         (void)cudaGetLastError();
         return MBD_ERR_CUDA;
     }
-    *flags = a | b | c | d | f | g;
+    *flags = a | b | c | d | kv;
     return MBD_OK;
 }
 

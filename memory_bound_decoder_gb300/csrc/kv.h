@@ -88,11 +88,15 @@ struct AttendPlan {
 void plan_kv_attend(int head_dim, int store, int group, int sms, int64_t capacity, int64_t rows, AttendPlan* plan);
 
 cudaError_t launch_kv_append(const AppendParams& p, int sms, cudaStream_t s);
-cudaError_t launch_kv_attend(const AttendParams& p, cudaStream_t s);
+cudaError_t launch_kv_attend(const AttendParams& p, cudaStream_t s);   // any store; the other two: their own
+cudaError_t launch_kv_attend_fp8(const AttendParams& p, cudaStream_t s);
+cudaError_t launch_kv_attend_fp8_dynamic(const AttendParams& p, cudaStream_t s);
 cudaError_t launch_kv_weights(const AttendParams& p, cudaStream_t s);
 cudaError_t launch_kv_evict(const EvictParams& p, cudaStream_t s);
 cudaError_t device_error_flags_kv_cache(unsigned int* flags, bool clear);
 cudaError_t device_error_flags_kv_attention(unsigned int* flags, bool clear);
+cudaError_t device_error_flags_kv_attention_fp8(unsigned int* flags, bool clear);
+cudaError_t device_error_flags_kv_attention_fp8_dynamic(unsigned int* flags, bool clear);
 
 // What the C-ABI layer keeps for every entry point (api.cu): the SM count of the current device, and the status of
 // a launch (counts it, or keeps its cudaError_t).

@@ -1,748 +1,10 @@
-// Attention of one new token per sequence over the paged key-value cache.
-//
-// For query head h of sequence b, with its key-value head's keys K and values V of the slots in view:
-//     x_j = scale * q . K_j,  lse = log sum_j exp(x_j),  p_j = exp(x_j - lse),  out = sum_j p_j V_j
-// and, where weights are accumulated, weight[j] += sum over the group's query heads of p_j.
-//
-// Bound by bytes: every key and value is read once for the few query heads of its group (g operations a byte), so the
-// kernel is a stream that has to keep loads in flight, and the arithmetic must stay out of the way. fp32 units
-// would be busy at g = 4 already, so both products run on mma.sync (m16n8k16) with the cache as the 16-row operand and
-// 8 query heads as its 8 columns: S^T = K q^T, then O^T = V^T P^T. tcgen05 would want 64 or 128 rows of one operand
-// staged in shared memory; here one warp owns 16 keys and no operand is used twice, so fragments are loaded from
-// global memory straight into the registers the instruction reads, with no shared memory, barrier or bank in the way:
-//   - the contraction's order is free, so q is loaded in the order in which a lane's 16-byte vectors of K arrive;
-//   - V^T wants pairs of keys in one register: one byte permutation of two keys' vectors (E4M3: before conversion);
-//   - the probabilities change from accumulator to operand layout by one movmatrix per 8 keys.
-// E4M3 codes become f16 by the hardware conversion (exact), so the FP8 path multiplies in f16, with q scaled by a power of
-// two per head so that its elements are normal f16 numbers (bf16's 8 bits fit) and p by 2^6 (flushing below 2^-30).
-// In the bf16 path p goes in as the sum of two bf16 terms (2^-16): rounding it once would cost as much accuracy as
-// rounding the output does, and the tensor cores idle anyway.
-//
-// Work is cut by keys, not by sequences: all tiles (4 warps' steps) of all sequences and heads in a row, the CTAs of a
-// resident grid take equal shares, wherever they begin and end. A share covers whole (sequence, head) items, written
-// at once, and at most two cut ones, whose sums go to the workspace; kv_join_kernel adds those up in a fixed order.
-// A warp keeps a step of K and of V in flight at all times, across the ends of items too.
-#include "kv_common.cuh"
+// Decode attention over a paged cache (kv_attention_impl.cuh): the bf16 cache, the plan of a call, and the
+// accumulation of attention weights.
+#include "kv_attention_impl.cuh"
 
 namespace mbd {
 
 namespace {
-
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
-constexpr int kJoinThreads = 256;
-constexpr float kLazy = 8.0f;    // units of log2 that a logit may exceed the kept maximum by (p <= 2^8)
-constexpr float kShift = 6.0f;   // E4M3: p is multiplied by 2^kShift (p <= 2^14 in f16)
-constexpr float kLn2 = 0.693147180559945309f;
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint4 ld16(const char* p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint2 ld8(const char* p) {
-    uint2 v;
-    asm volatile("ld.global.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
-    return v;
-}
-
-template <bool F16>
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
-    if constexpr (F16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
-    uint32_t d;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
-    return d;
-}
-
-// Two E4M3 codes (low 16 bits) to f16, exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<unsigned short>(w)));
-    return h;
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-// What a (D, STORE) variant loads and holds. A step is 16 NG keys of one warp, 4 KB of K and of V where rows are at
-// most 256 bytes.
-template <int D, int STORE>
-struct Shape {
-    static constexpr bool kF8 = STORE != kKvBf16;
-    static constexpr int kRow = D * (kF8 ? 1 : 2);           // bytes of a row
-    static constexpr int kKv = kRow / 64;                    // 16-byte vectors of a K row in one lane (4 lanes a row)
-    static constexpr int kVb = kRow / 8 < 16 ? 8 : 16;       // bytes of a vector of V (8 lanes a row)
-    static constexpr int kVv = kRow / 8 / kVb;               // of them in one lane
-    static constexpr int kVw = kVb / 4;                      // words of one
-    static constexpr int kVd = kVb / (kF8 ? 1 : 2);          // elements of one
-    static constexpr int kGroups = kRow >= 256 ? 1 : 256 / kRow;
-    static constexpr int kStep = 16 * kGroups;               // keys
-    static constexpr int kTile = kStep * kWarps;
-    static constexpr int kK = D / 16;                        // k-steps of S^T, m-tiles of O^T
-};
-
-// One (sequence, key-value head, chunk of query heads) in view of a CTA, at one of its tiles.
-struct Cursor {
-    int seq;
-    int len, first;    // keys [first, len) are in view; tiles count from first, rounded down to a step
-    int tile, tiles;
-    int head;          // key-value head * chunks + chunk
-};
-
-template <class S>
-__device__ __forceinline__ int origin(int first) { return first & ~(S::kStep - 1); }
-
-// View and tiles of a sequence.
-template <class S>
-__device__ __forceinline__ int view_of(const AttendParams& p, int64_t seq, int* first, int* len) {
-    *len = static_cast<int>(kv_len(p.c, p.seq_lens[seq]));
-    *first = p.window > 0 && p.window < *len ? *len - static_cast<int>(p.window) : 0;
-    return *len > 0 ? (*len - origin<S>(*first) + S::kTile - 1) / S::kTile : 0;
-}
-
-// (seq, head) `cur` is at the end of its tiles: the next item that has some.
-template <class S>
-__device__ __forceinline__ void next_item(const AttendParams& p, Cursor& cur, int heads) {
-    cur.tile = 0;
-    if (++cur.head < heads) return;
-    cur.head = 0;
-    do {
-        if (++cur.seq >= p.n_seqs) return;
-        cur.tiles = view_of<S>(p, cur.seq, &cur.first, &cur.len);
-    } while (cur.tiles == 0);
-}
-
-// Sums of one item (or of a part of it) over the warps of a CTA, per query head of the chunk.
-template <int D, int HT>
-struct MergeSmem {
-    float o[kWarps][HT][D + 4];
-    float4 ml[kWarps][HT];   // maximum of the logits, sum, exponent that o is relative to
-};
-
-template <int D, int STORE, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 && D < 256 ? 3 : 2)
-    kv_attend_kernel(const __grid_constant__ AttendParams p) {
-    using S = Shape<D, STORE>;
-    constexpr bool kF8 = S::kF8, kDyn = STORE == kKvFp8Dynamic;
-    constexpr int HT = 8 * NT, NG = S::kGroups, KV = S::kKv, VV = S::kVv, VW = S::kVw, KK = S::kK;
-    __shared__ MergeSmem<D, HT> sm;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const int heads = p.c.n_kv_heads * p.chunks;
-    pdl_trigger();
-    pdl_wait();
-
-    // The total of tiles, then this CTA's share of them: every warp scans the lengths for itself.
-    int64_t total = 0;
-    for (int64_t b0 = 0; b0 < p.n_seqs; b0 += 32) {
-        int first, len;
-        int64_t t = b0 + lane < p.n_seqs ? view_of<S>(p, b0 + lane, &first, &len) : 0;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        total += t;
-    }
-    total *= heads;
-    const int64_t cta = blockIdx.x, grid = min(static_cast<int64_t>(gridDim.x), total);   // shares, none of them empty
-    const int64_t begin = cta < grid ? cta * total / grid : 0, end = cta < grid ? (cta + 1) * total / grid : 0;
-    // Sequences with nothing in view: zeros, shared out over the CTAs.
-    for (int64_t b = cta; b < p.n_seqs; b += gridDim.x) {
-        int first, len;
-        if (view_of<S>(p, b, &first, &len) > 0) continue;
-        for (int i = threadIdx.x; i < p.n_q_heads * D / 8; i += kThreads)
-            reinterpret_cast<uint4*>(p.out)[b * p.n_q_heads * (D / 8) + i] = make_uint4(0, 0, 0, 0);
-        for (int i = threadIdx.x; p.lse && i < p.n_q_heads; i += kThreads) p.lse[b * p.n_q_heads + i] = -INFINITY;
-    }
-    if (threadIdx.x == 0) p.cut[cta] = make_int4(-1, 0, 0, 0);
-    if (begin >= end) return;
-
-    Cursor ld{};   // of the step whose loads are issued next
-    {
-        int64_t before = 0;
-        for (int64_t b0 = 0; b0 < p.n_seqs; b0 += 32) {
-            int first = 0, len = 0;
-            const int t = b0 + lane < p.n_seqs ? view_of<S>(p, b0 + lane, &first, &len) : 0;
-            int64_t upto = t;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += x;
-            }
-            const unsigned hit = __ballot_sync(0xffffffffu, (before + upto) * heads > begin);
-            if (hit) {
-                const int src = __ffs(hit) - 1;
-                const int64_t off = begin - (before + __shfl_sync(0xffffffffu, upto - t, src)) * heads;
-                ld.tiles = __shfl_sync(0xffffffffu, t, src);
-                ld.first = __shfl_sync(0xffffffffu, first, src);
-                ld.len = __shfl_sync(0xffffffffu, len, src);
-                ld.seq = static_cast<int>(b0) + src;
-                ld.head = static_cast<int>(off / ld.tiles);
-                ld.tile = static_cast<int>(off % ld.tiles);
-                break;
-            }
-            before += __shfl_sync(0xffffffffu, upto, 31);
-        }
-    }
-    const bool small_pages = p.c.page_shift < 4;
-    const float k_static = STORE == kKvFp8Static ? *p.c.k_scale : 1.0f;
-    const float v_static = STORE == kKvFp8Static ? *p.c.v_scale : 1.0f;
-
-    uint4 kx[NG][2][KV];
-    uint32_t vx[NG][4][VV][VW];
-    uint32_t q[NT][KK][2];
-    float ks[NG][2], vs[NG][2];      // dynamic scales of the keys r and r + 8: k's, and log2 of v's
-    float ks_next[NG][2], vs_next[NG][2];
-    int64_t row[NG];                 // byte offset of the group's first row (small pages: of row lane % 16)
-    unsigned live[NG], live_next[NG];   // bit i: key i of the group is in view
-    int page[NG];                    // of the step after the next
-
-    // Page numbers of the step at `cur`; -1 behind the sequence.
-    auto load_pages = [&](const Cursor& cur) {
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const int key = origin<S>(cur.first) + (cur.tile * kWarps + warp) * S::kStep + g * 16 +
-                            (small_pages ? lane & 15 : 0);
-            page[g] = key < cur.len ? p.c.table[static_cast<int64_t>(cur.seq) * p.c.pages_per_seq + (key >> p.c.page_shift)] : -1;
-        }
-    };
-    // Rows and view of the step at `cur`, whose page numbers were loaded.
-    auto place = [&](const Cursor& cur) {
-        const int kv_head = p.chunks == 1 ? cur.head : cur.head / p.chunks;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const int key = origin<S>(cur.first) + (cur.tile * kWarps + warp) * S::kStep + g * 16;
-            const int mine = key + (small_pages ? lane & 15 : 0);
-            const bool good = static_cast<uint32_t>(page[g]) < static_cast<uint64_t>(p.c.n_pages);
-            const int left = cur.len - key, skip = cur.first - key;
-            unsigned m = left >= 16 ? 0xffffu : (left <= 0 ? 0u : (1u << left) - 1u);
-            if (skip > 0) m &= skip >= 16 ? 0u : ~((1u << skip) - 1u);
-            if (!good && (small_pages ? (m >> (lane & 15)) & 1u : m)) kv_bad_index();
-            if (small_pages) m &= __ballot_sync(0xffffffffu, good);
-            else if (!good) m = 0u;
-            live_next[g] = m;
-            row[g] = good ? kv_row(p.c, page[g], kv_head, mine, S::kRow) : 0;
-            if constexpr (kDyn) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    ks_next[g][i] = vs_next[g][i] = 0.0f;
-                    const int at = r + 8 * i;
-                    const int pg = small_pages ? __shfl_sync(0xffffffffu, page[g], at) : page[g];
-                    if ((m >> at) & 1u) {
-                        const int64_t meta = kv_meta(p.c, pg, kv_head, key + at);
-                        ks_next[g][i] = p.c.k_scale[meta];
-                        vs_next[g][i] = p.c.v_scale[meta];
-                    }
-                }
-            }
-        }
-    };
-    // Byte offset of row `at` (0..15) of group g.
-    auto row_of = [&](int g, int at) {
-        return small_pages ? __shfl_sync(0xffffffffu, row[g], at) : row[g] + at * S::kRow;
-    };
-    auto load_k = [&] {
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const char* at = static_cast<const char*>(p.c.k) + row_of(g, r + 8 * i) + c * 16;
-                if (live_next[g] == 0xffffu) {
-#pragma unroll
-                    for (int j = 0; j < KV; ++j) kx[g][i][j] = ld16(at + j * 64);
-                } else {
-                    const bool in = (live_next[g] >> (r + 8 * i)) & 1u;
-#pragma unroll
-                    for (int j = 0; j < KV; ++j) kx[g][i][j] = in ? ld16(at + j * 64) : make_uint4(0, 0, 0, 0);
-                }
-            }
-    };
-    auto load_v = [&] {
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int at = 2 * c + (i & 1) + 8 * (i >> 1);
-                const char* from = static_cast<const char*>(p.c.v) + row_of(g, at) + r * S::kVb;
-                const bool in = live_next[g] == 0xffffu || ((live_next[g] >> at) & 1u);
-#pragma unroll
-                for (int j = 0; j < VV; ++j) {
-                    if constexpr (VW == 4) {
-                        uint4 x = make_uint4(0, 0, 0, 0);
-                        if (in) x = ld16(from + j * 8 * S::kVb);
-                        vx[g][i][j][0] = x.x;
-                        vx[g][i][j][1] = x.y;
-                        vx[g][i][j][2] = x.z;
-                        vx[g][i][j][3] = x.w;
-                    } else {
-                        uint2 x = make_uint2(0, 0);
-                        if (in) x = ld8(from + j * 8 * S::kVb);
-                        vx[g][i][j][0] = x.x;
-                        vx[g][i][j][1] = x.y;
-                    }
-                }
-            }
-    };
-    // Query heads of the chunk at `cur`, lane r's: bf16 in the order of K's vectors (E4M3: 16 elements a vector).
-    auto load_q = [&](const Cursor& cur) {
-        const int kv_head = p.chunks == 1 ? cur.head : cur.head / p.chunks;
-        const int h0 = p.chunks == 1 ? 0 : (cur.head - kv_head * p.chunks) * HT;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int h = h0 + nt * 8 + r;
-            const char* from = static_cast<const char*>(p.q) + static_cast<int64_t>(cur.seq) * p.q_bytes +
-                               (static_cast<int64_t>(kv_head) * p.group + h) * D * 2;
-#pragma unroll
-            for (int j = 0; j < KK / 2; ++j) {
-                const int vec = kF8 ? ((j >> 1) * 4 + c) * 2 + (j & 1) : j * 4 + c;
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (h < p.group) x = ld16(from + vec * 16);
-                q[nt][2 * j][0] = x.x;
-                q[nt][2 * j][1] = x.y;
-                q[nt][2 * j + 1][0] = x.z;
-                q[nt][2 * j + 1][1] = x.w;
-            }
-        }
-    };
-
-    float factor[NT][2];            // logit in units of log2 over the product, query heads 2c and 2c + 1
-    // q as the products want it, and the factors.
-    auto ready_q = [&] {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            factor[nt][0] = factor[nt][1] = p.scale_log2 * k_static;
-            if constexpr (kF8) {
-                float top = 0.0f;
-#pragma unroll
-                for (int k = 0; k < KK; ++k)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        top = fmaxf(top, fmaxf(fabsf(bf16_lo(q[nt][k][i])), fabsf(bf16_hi(q[nt][k][i]))));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                // 2^(141 - e) brings the largest element into [2^14, 2^15); e within the normal numbers.
-                const int e = min(max(static_cast<int>(__float_as_uint(top) >> 23), 16), 254);
-                const float up = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
-                const float down = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
-#pragma unroll
-                for (int k = 0; k < KK; ++k)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        q[nt][k][i] = pack_f16x2(bf16_lo(q[nt][k][i]) * up, bf16_hi(q[nt][k][i]) * up);
-                factor[nt][0] *= __shfl_sync(0xffffffffu, down, 8 * c);
-                factor[nt][1] *= __shfl_sync(0xffffffffu, down, 8 * c + 4);
-            }
-        }
-    };
-
-    float o[NT][KK][4];
-    float m[NT][2], mo[NT][2], sum[NT][2];   // kept maxima (of the logits; of logit + log2 v's scale), partial sums
-    auto clear = [&] {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int k = 0; k < KK; ++k)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[nt][k][i] = 0.0f;
-            m[nt][0] = m[nt][1] = mo[nt][0] = mo[nt][1] = -INFINITY;
-            sum[nt][0] = sum[nt][1] = 0.0f;
-        }
-    };
-
-    int64_t left = end - begin;
-    Cursor cur = ld;
-    int seg_first = cur.tile;    // first tile of the current item in this share
-    load_pages(ld);
-    place(ld);
-    load_k();
-    load_v();
-    load_q(ld);
-    // The step after: its cursor, and its page numbers on the way.
-    auto advance = [&] {
-        if (++ld.tile == ld.tiles) next_item<S>(p, ld, heads);
-    };
-    if (left > 1) {
-        advance();
-        load_pages(ld);
-    }
-    ready_q();
-    clear();
-
-    while (true) {
-        const bool more = left > 1;
-        const bool closes = !more || ld.tile == 0;   // the last step of the current item in this share
-#pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            live[g] = live_next[g];
-            if constexpr (kDyn)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    ks[g][i] = ks_next[g][i];
-                    vs[g][i] = __log2f(vs_next[g][i]);
-                }
-        }
-        // S^T: rows are keys (r and r + 8), columns query heads (2c and 2c + 1).
-        float s[NG][NT][4];
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[g][nt][i] = 0.0f;
-#pragma unroll
-        for (int j = 0; j < KV; ++j)
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                const uint32_t a[4] = {kx[g][0][j].x, kx[g][0][j].y, kx[g][0][j].z, kx[g][0][j].w};
-                const uint32_t b[4] = {kx[g][1][j].x, kx[g][1][j].y, kx[g][1][j].z, kx[g][1][j].w};
-                if constexpr (kF8) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t a0 = e4m3x2_to_f16x2(a[i]), a2 = e4m3x2_to_f16x2(a[i] >> 16);
-                        const uint32_t a1 = e4m3x2_to_f16x2(b[i]), a3 = e4m3x2_to_f16x2(b[i] >> 16);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma<true>(s[g][nt], a0, a1, a2, a3, q[nt][j * 4 + i][0], q[nt][j * 4 + i][1]);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma<false>(s[g][nt], a[2 * i], b[2 * i], a[2 * i + 1], b[2 * i + 1], q[nt][j * 2 + i][0],
-                                       q[nt][j * 2 + i][1]);
-                }
-            }
-        if (more) {
-            place(ld);
-            load_k();
-            if (closes) load_q(ld);
-        }
-
-        // Softmax of the step: x in place of s, then p in place of x.
-        unsigned any_live = 0;
-#pragma unroll
-        for (int g = 0; g < NG; ++g) any_live |= live[g];
-        if (any_live) {
-            bool rise = false;
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float x = s[g][nt][i] * factor[nt][i & 1];
-                        if constexpr (kDyn) x *= ks[g][i >> 1];
-                        if (!((live[g] >> (r + 8 * (i >> 1))) & 1u)) x = -INFINITY;
-                        s[g][nt][i] = x;
-                        rise |= x > m[nt][i & 1] + kLazy;
-                        if constexpr (kDyn) rise |= x + vs[g][i >> 1] > mo[nt][i & 1] + kLazy;
-                    }
-            if (p.accumulate) {
-                const int kv_head = p.chunks == 1 ? cur.head : cur.head / p.chunks;
-                const int h0 = p.chunks == 1 ? 0 : (cur.head - kv_head * p.chunks) * HT;
-                const int key = origin<S>(cur.first) + (cur.tile * kWarps + warp) * S::kStep;
-                float* to = p.logits + ((static_cast<int64_t>(cur.seq) * p.c.n_kv_heads + kv_head) * p.c.capacity + key) * p.logit_heads;
-#pragma unroll
-                for (int g = 0; g < NG; ++g)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int h = h0 + nt * 8 + 2 * c, at = r + 8 * i;
-                            if (h < p.group && ((live[g] >> at) & 1u))
-                                *reinterpret_cast<float2*>(to + static_cast<int64_t>(g * 16 + at) * p.logit_heads + h) =
-                                    make_float2(s[g][nt][2 * i], s[g][nt][2 * i + 1]);
-                        }
-            }
-            if (__any_sync(0xffffffffu, rise)) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float top = m[nt][h], topo = mo[nt][h];
-#pragma unroll
-                        for (int g = 0; g < NG; ++g)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                top = fmaxf(top, s[g][nt][2 * i + h]);
-                                if constexpr (kDyn) topo = fmaxf(topo, s[g][nt][2 * i + h] + vs[g][i]);
-                            }
-#pragma unroll
-                        for (int x = 4; x < 32; x <<= 1) {
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                            if constexpr (kDyn) topo = fmaxf(topo, __shfl_xor_sync(0xffffffffu, topo, x));
-                        }
-                        if constexpr (!kDyn) topo = top;
-                        const float old = top == -INFINITY ? 1.0f : ex2(m[nt][h] - top);
-                        const float oldo = kDyn ? (topo == -INFINITY ? 1.0f : ex2(mo[nt][h] - topo)) : old;
-                        m[nt][h] = top;
-                        mo[nt][h] = topo;
-                        sum[nt][h] *= old;
-#pragma unroll
-                        for (int k = 0; k < KK; ++k) {
-                            o[nt][k][h] *= oldo;
-                            o[nt][k][2 + h] *= oldo;
-                        }
-                    }
-            }
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                uint32_t hi[NT][2], lo[NT][2];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float w[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float base = m[nt][i & 1] == -INFINITY ? 0.0f : m[nt][i & 1];
-                        const float pj = ex2(s[g][nt][i] - base);
-                        sum[nt][i & 1] += pj;
-                        if constexpr (kDyn) {
-                            const float baseo = mo[nt][i & 1] == -INFINITY ? 0.0f : mo[nt][i & 1];
-                            w[i] = ex2(s[g][nt][i] + vs[g][i >> 1] - baseo + kShift);
-                        } else if constexpr (kF8) {
-                            w[i] = pj * 0x1p6f;
-                        } else {
-                            w[i] = pj;
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if constexpr (kF8) {
-                            hi[nt][i] = transpose8x8(pack_f16x2(w[2 * i], w[2 * i + 1]));
-                        } else {
-                            const uint32_t a = pack_bf16x2(w[2 * i], w[2 * i + 1]);
-                            hi[nt][i] = transpose8x8(a);
-                            lo[nt][i] = transpose8x8(pack_bf16x2(w[2 * i] - bf16_lo(a), w[2 * i + 1] - bf16_hi(a)));
-                        }
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < VV; ++j)
-#pragma unroll
-                    for (int i = 0; i < VW; ++i) {
-                        const uint32_t w0 = vx[g][0][j][i], w1 = vx[g][1][j][i], w2 = vx[g][2][j][i], w3 = vx[g][3][j][i];
-                        if constexpr (kF8) {
-#pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                const uint32_t a = __byte_perm(w0, w1, half ? 0x7362 : 0x5140);
-                                const uint32_t b = __byte_perm(w2, w3, half ? 0x7362 : 0x5140);
-                                const uint32_t a0 = e4m3x2_to_f16x2(a), a1 = e4m3x2_to_f16x2(a >> 16);
-                                const uint32_t a2 = e4m3x2_to_f16x2(b), a3 = e4m3x2_to_f16x2(b >> 16);
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
-                                    mma<true>(o[nt][(j * VW + i) * 2 + half], a0, a1, a2, a3, hi[nt][0], hi[nt][1]);
-                            }
-                        } else {
-                            const uint32_t a0 = __byte_perm(w0, w1, 0x5410), a1 = __byte_perm(w0, w1, 0x7632);
-                            const uint32_t a2 = __byte_perm(w2, w3, 0x5410), a3 = __byte_perm(w2, w3, 0x7632);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                mma<false>(o[nt][j * VW + i], a0, a1, a2, a3, hi[nt][0], hi[nt][1]);
-                                mma<false>(o[nt][j * VW + i], a0, a1, a2, a3, lo[nt][0], lo[nt][1]);
-                            }
-                        }
-                    }
-            }
-        }
-        if (more) load_v();
-
-        if (closes) {
-            // The four warps' sums join in shared memory.
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int head = nt * 8 + 2 * c + h;
-#pragma unroll
-                    for (int k = 0; k < KK; k += 2) {
-                        constexpr int per = S::kVd / 2;   // m-tiles of one vector
-                        const int dim = ((k / per) * 8 + r) * S::kVd + 2 * (k % per);
-                        *reinterpret_cast<float4*>(&sm.o[warp][head][dim]) =
-                            make_float4(o[nt][k][h], o[nt][k][2 + h], o[nt][k + 1][h], o[nt][k + 1][2 + h]);
-                    }
-                    float t = sum[nt][h];
-#pragma unroll
-                    for (int x = 4; x < 32; x <<= 1) t += __shfl_xor_sync(0xffffffffu, t, x);
-                    if (r == 0) sm.ml[warp][head] = make_float4(m[nt][h], t, kF8 ? mo[nt][h] - kShift : mo[nt][h], 0.0f);
-                }
-            __syncthreads();
-            const int kv_head = p.chunks == 1 ? cur.head : cur.head / p.chunks;
-            const int h0 = p.chunks == 1 ? 0 : (cur.head - kv_head * p.chunks) * HT;
-            const int n = min(HT, p.group - h0);
-            const int64_t out_head = static_cast<int64_t>(cur.seq) * p.n_q_heads + kv_head * p.group + h0;
-            const bool from_start = seg_first == 0, whole = from_start && cur.tile + 1 == cur.tiles;
-            const int slot = from_start ? 1 : 0;
-            for (int i = threadIdx.x; i < n * (D / 4); i += kThreads) {
-                const int h = i / (D / 4), dim = i % (D / 4) * 4;
-                float4 ml[kWarps];
-                float top = -INFINITY, topo = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    ml[w] = sm.ml[w][h];
-                    top = fmaxf(top, ml[w].x);
-                    topo = fmaxf(topo, ml[w].z);
-                }
-                float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                float t = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    if (ml[w].x != -INFINITY) t += ml[w].y * ex2(ml[w].x - top);
-                    if (ml[w].z == -INFINITY) continue;
-                    const float f = ex2(ml[w].z - topo);
-                    const float4 x = *reinterpret_cast<const float4*>(&sm.o[w][h][dim]);
-                    acc.x += x.x * f;
-                    acc.y += x.y * f;
-                    acc.z += x.z * f;
-                    acc.w += x.w * f;
-                }
-                if (whole) {
-                    const float f = topo == -INFINITY ? 0.0f : ex2(topo - top) / t * v_static;
-                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + (out_head + h) * D + dim) =
-                        make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
-                    if (dim == 0) {
-                        const float lse2 = top == -INFINITY ? -INFINITY : top + log2f(t);
-                        if (p.lse) p.lse[out_head + h] = lse2 * kLn2;
-                        if (p.accumulate) p.lse2[out_head + h] = lse2;
-                    }
-                } else {
-                    const int64_t part = (cta * 2 + slot) * HT + h;
-                    *reinterpret_cast<float4*>(p.part_o + part * D + dim) = acc;
-                    if (dim == 0) p.part_ml[part] = make_float4(top, t, topo, 0.0f);
-                }
-            }
-            if (!whole && from_start && threadIdx.x == 0) {
-                // The share that holds the item's last tile: the last one that begins at or before it.
-                const int64_t item_end = begin + (end - begin - left) + 1 - (cur.tile + 1) + cur.tiles;   // exclusive
-                const int64_t last = (item_end * grid - 1) / total;
-                p.cut[cta] = make_int4(cur.seq, cur.head, static_cast<int>(last), n);
-            }
-            __syncthreads();
-            if (!more) break;
-            seg_first = 0;
-            ready_q();
-            clear();
-        }
-        cur = ld;
-        --left;
-        if (left > 1) {
-            advance();
-            load_pages(ld);
-        }
-    }
-}
-
-// Adds up the parts of the items that were cut. blockIdx.x: the share in which an item begins that ends in a later one;
-// its parts are slot 1 of that share and slot 0 of the following ones. blockIdx.y: a slice of its query heads.
-template <int D, int STORE, int NT>
-__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_constant__ AttendParams p, int heads_per_cta) {
-    constexpr int HT = 8 * NT, C = D / 4;   // columns of 4 elements
-    __shared__ float4 s_acc[kJoinThreads];
-    __shared__ float s_top[HT], s_topo[HT], s_sum[HT];
-    pdl_trigger();
-    pdl_wait();
-    const int64_t first = blockIdx.x;
-    const int4 cut = p.cut[first];
-    const int h0 = blockIdx.y * heads_per_cta, n = min(heads_per_cta, cut.w - h0);
-    if (cut.x < 0 || n <= 0) return;
-    const int parts = cut.z - static_cast<int>(first) + 1;
-    auto part_of = [&](int i) { return (i == 0 ? first * 2 + 1 : (first + i) * 2) * HT + h0; };
-    // Maxima and sums of each head: a warp per head in turn, the parts over its lanes.
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int h = warp; h < n; h += kJoinThreads / 32) {
-        float top = -INFINITY, topo = -INFINITY, t = 0.0f;
-        for (int i = lane; i < parts; i += 32) {
-            const float4 ml = p.part_ml[part_of(i) + h];
-            top = fmaxf(top, ml.x);
-            topo = fmaxf(topo, ml.z);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            topo = fmaxf(topo, __shfl_xor_sync(0xffffffffu, topo, o));
-        }
-        for (int i = lane; i < parts; i += 32) {
-            const float4 ml = p.part_ml[part_of(i) + h];
-            if (ml.x != -INFINITY) t += ml.y * ex2(ml.x - top);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        if (lane == 0) {
-            s_top[h] = top;
-            s_topo[h] = topo;
-            s_sum[h] = t;
-        }
-    }
-    __syncthreads();
-    const float v_static = STORE == kKvFp8Static ? *p.c.v_scale : 1.0f;
-    const int kv_head = cut.y / p.chunks;
-    const int64_t out_head = cut.x * static_cast<int64_t>(p.n_q_heads) + static_cast<int64_t>(kv_head) * p.group +
-                             (cut.y - kv_head * p.chunks) * HT + h0;
-    // Columns over the threads; where there are fewer columns than threads, the parts too.
-    const int columns = n * C, span = min(kJoinThreads, columns), ways = kJoinThreads / span;
-    const int way = threadIdx.x / span;
-    for (int base = 0; base < columns; base += span) {
-        const int i = base + threadIdx.x % span;
-        const int h = i / C, dim = i % C * 4;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (way < ways && i < columns) {
-#pragma unroll 4
-            for (int k = way; k < parts; k += ways) {
-                const int64_t part = part_of(k) + h;
-                const float e = p.part_ml[part].z;
-                const float4 x = *reinterpret_cast<const float4*>(p.part_o + part * D + dim);
-                const float f = e == -INFINITY ? 0.0f : ex2(e - s_topo[h]);
-                acc.x += x.x * f;
-                acc.y += x.y * f;
-                acc.z += x.z * f;
-                acc.w += x.w * f;
-            }
-        }
-        if (ways > 1) {
-            s_acc[threadIdx.x] = acc;
-            __syncthreads();
-            if (way == 0)
-                for (int w = 1; w < ways; ++w) {
-                    const float4 x = s_acc[w * span + threadIdx.x];
-                    acc.x += x.x;
-                    acc.y += x.y;
-                    acc.z += x.z;
-                    acc.w += x.w;
-                }
-            __syncthreads();
-        }
-        if (way == 0 && i < columns) {
-            const float f = s_topo[h] == -INFINITY ? 0.0f : ex2(s_topo[h] - s_top[h]) / s_sum[h] * v_static;
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + (out_head + h) * D + dim) =
-                make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
-            if (dim == 0) {
-                const float lse2 = s_top[h] == -INFINITY ? -INFINITY : s_top[h] + log2f(s_sum[h]);
-                if (p.lse) p.lse[out_head + h] = lse2 * kLn2;
-                if (p.accumulate) p.lse2[out_head + h] = lse2;
-            }
-        }
-    }
-}
 
 // weight[slot] += sum over the group's query heads of exp2(logit - lse2): a thread per slot.
 __global__ void __launch_bounds__(256) kv_weights_kernel(const __grid_constant__ AttendParams p, int blocks_per_row) {
@@ -764,41 +26,6 @@ __global__ void __launch_bounds__(256) kv_weights_kernel(const __grid_constant__
     }
 }
 
-template <int D, int STORE, int NT>
-cudaError_t launch_nt(const AttendParams& p, cudaStream_t s) {
-    const cudaError_t e = kv_launch(kv_attend_kernel<D, STORE, NT>, p.grid, kThreads, 0, 1, s, p);
-    if (e != cudaSuccess) return e;
-    // Few items: many parts each, so a CTA per query head. Many: two parts as a rule, and one CTA for all of them.
-    const bool few = p.n_seqs * p.c.n_kv_heads * p.chunks < p.grid;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3(p.grid, few ? (p.group < 8 * NT ? p.group : 8 * NT) : 1);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = s;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, STORE, NT>, p, few ? 1 : 8 * NT);
-}
-
-template <int D, int STORE>
-cudaError_t launch_store(const AttendParams& p, cudaStream_t s) {
-    if constexpr (D < 256)
-        if (p.chunk_heads == 16) return launch_nt<D, STORE, 2>(p, s);
-    return launch_nt<D, STORE, 1>(p, s);
-}
-
-template <int D>
-cudaError_t launch_d(const AttendParams& p, cudaStream_t s) {
-    switch (p.c.store) {
-        case kKvBf16: return launch_store<D, kKvBf16>(p, s);
-        case kKvFp8Static: return launch_store<D, kKvFp8Static>(p, s);
-        case kKvFp8Dynamic: return launch_store<D, kKvFp8Dynamic>(p, s);
-    }
-    return cudaErrorInvalidValue;
-}
-
 }  // namespace
 
 void plan_kv_attend(int head_dim, int store, int group, int sms, int64_t capacity, int64_t rows, AttendPlan* plan) {
@@ -806,10 +33,9 @@ void plan_kv_attend(int head_dim, int store, int group, int sms, int64_t capacit
     // accumulators would not fit the registers), in chunks of 16 (8).
     plan->chunk_heads = group > 8 && head_dim < 256 ? 16 : 8;
     plan->chunks = (group + plan->chunk_heads - 1) / plan->chunk_heads;
-    const int row = head_dim * (store == kKvBf16 ? 2 : 1), step = row >= 256 ? 16 : 16 * 256 / row;
-    const int64_t tile = int64_t{step} * kWarps;
-    // CTAs that are resident at once (__launch_bounds__), no more than there can be tiles.
-    const int64_t resident = int64_t{sms} * (plan->chunk_heads == 8 && head_dim < 256 ? 3 : 2);
+    const int64_t tile = int64_t{step_keys(head_dim, store)} * kWarps;
+    // CTAs that are resident at once, no more than there can be tiles.
+    const int64_t resident = int64_t{sms} * resident_ctas(head_dim, store, plan->chunk_heads / 8);
     const int64_t items = rows * plan->chunks;
     const int64_t tiles_per_item = (capacity + tile - 1) / tile + 1;
     plan->grid = static_cast<int>(items >= resident || items * tiles_per_item >= resident ? resident
@@ -817,10 +43,10 @@ void plan_kv_attend(int head_dim, int store, int group, int sms, int64_t capacit
 }
 
 cudaError_t launch_kv_attend(const AttendParams& p, cudaStream_t s) {
-    switch (p.c.head_dim) {
-        case 64: return launch_d<64>(p, s);
-        case 128: return launch_d<128>(p, s);
-        case 256: return launch_d<256>(p, s);
+    switch (p.c.store) {
+        case kKvBf16: return launch_store<kKvBf16>(p, s);
+        case kKvFp8Static: return launch_kv_attend_fp8(p, s);
+        case kKvFp8Dynamic: return launch_kv_attend_fp8_dynamic(p, s);
     }
     return cudaErrorInvalidValue;
 }
@@ -831,13 +57,6 @@ cudaError_t launch_kv_weights(const AttendParams& p, cudaStream_t s) {
     return kv_launch(kv_weights_kernel, static_cast<unsigned>(rows * per_row), 256, 0, 1, s, p, per_row);
 }
 
-cudaError_t device_error_flags_kv_attention(unsigned int* flags, bool clear) {
-    cudaError_t e = cudaMemcpyFromSymbol(flags, g_device_error_flags, sizeof(unsigned int));
-    if (e == cudaSuccess && clear) {
-        const unsigned int zero = 0;
-        e = cudaMemcpyToSymbol(g_device_error_flags, &zero, sizeof(unsigned int));
-    }
-    return e;
-}
+cudaError_t device_error_flags_kv_attention(unsigned int* flags, bool clear) { return kv_error_flags(flags, clear); }
 
 }  // namespace mbd

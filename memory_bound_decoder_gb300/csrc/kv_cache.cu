@@ -400,13 +400,6 @@ cudaError_t launch_kv_evict(const EvictParams& p, cudaStream_t s) {
     return kv_launch(kv_evict_kernel, grid, kEvictThreads, smem, p.ctas_per_row, s, p);
 }
 
-cudaError_t device_error_flags_kv_cache(unsigned int* flags, bool clear) {
-    cudaError_t e = cudaMemcpyFromSymbol(flags, g_device_error_flags, sizeof(unsigned int));
-    if (e == cudaSuccess && clear) {
-        const unsigned int zero = 0;
-        e = cudaMemcpyToSymbol(g_device_error_flags, &zero, sizeof(unsigned int));
-    }
-    return e;
-}
+cudaError_t device_error_flags_kv_cache(unsigned int* flags, bool clear) { return kv_error_flags(flags, clear); }
 
 }  // namespace mbd

@@ -36,4 +36,14 @@ __device__ __forceinline__ int64_t kv_len(const KvView& c, int32_t len) {
     return len < 0 ? 0 : c.capacity;
 }
 
+// Read (and clear) the error word of the including translation unit.
+static inline cudaError_t kv_error_flags(unsigned int* flags, bool clear) {
+    cudaError_t e = cudaMemcpyFromSymbol(flags, g_device_error_flags, sizeof(unsigned int));
+    if (e == cudaSuccess && clear) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_device_error_flags, &zero, sizeof(unsigned int));
+    }
+    return e;
+}
+
 }  // namespace mbd
