@@ -65,7 +65,8 @@ struct AttendParams {
     int grid;                   // CTAs: the shares that the work is cut into
     float* part_o;              // workspace: [grid, 2, chunk_heads, head_dim], sums of the items that are cut
     float4* part_ml;            // workspace: [grid, 2, chunk_heads], their maxima, sums and exponents
-    int4* cut;                  // workspace: [grid], the item that begins in a share and ends in a later one
+    unsigned long long* arrived;   // workspace: [2, grid], where the deliveries of parts meet
+    unsigned long long call;    // the call's number
     int logit_heads;
     int accumulate;
 };

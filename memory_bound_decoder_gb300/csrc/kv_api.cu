@@ -1,5 +1,7 @@
 // C ABI of the paged key-value cache: host-side argument checks, workspaces and dispatch. As everywhere in the
 // library, every check runs before anything is enqueued.
+#include <atomic>
+#include <chrono>
 #include <cmath>
 #include <cstdint>
 
@@ -135,7 +137,7 @@ uint64_t round_up(uint64_t n) { return (n + 255) / 256 * 256; }
 struct AttendLayout {
     mbd::AttendPlan plan;
     int logit_heads;
-    uint64_t part_o, part_ml, cut, lse2, logits, total;
+    uint64_t part_o, part_ml, arrived, lse2, logits, total;
 };
 
 AttendLayout attend_layout(const mbd_kv_cache* c, int64_t pages_per_seq, int64_t n_seqs, int64_t n_q_heads,
@@ -147,13 +149,26 @@ AttendLayout attend_layout(const mbd_kv_cache* c, int64_t pages_per_seq, int64_t
     w.logit_heads = (group + 1) / 2 * 2;   // pairs of heads are stored together
     const uint64_t parts = uint64_t(w.plan.grid) * 2 * w.plan.chunk_heads;
     w.part_ml = round_up(parts * c->head_dim * 4);
-    w.cut = w.part_ml + round_up(parts * 16);
-    w.total = w.cut + round_up(uint64_t(w.plan.grid) * 16);
+    w.arrived = w.part_ml + round_up(parts * 16);
+    w.total = w.arrived + round_up(uint64_t(w.plan.grid) * 2 * 8);
     if (!accumulate) return w;
     w.lse2 = w.total;
     w.logits = w.lse2 + round_up(uint64_t(n_seqs) * n_q_heads * 4);
     w.total = w.logits + round_up(uint64_t(n_seqs) * c->n_kv_heads * capacity * w.logit_heads * 4);
     return w;
+}
+
+// A number that no other call of this process has, and that memory which no call has used is not expected to hold: 64
+// bits, counted up (by an odd step, never 0) from where the clock and the address space put the first one.
+unsigned long long next_call() {
+    static std::atomic<uint64_t> next{[] {
+        const uint64_t t = static_cast<uint64_t>(std::chrono::steady_clock::now().time_since_epoch().count());
+        const uint64_t x = (t ^ reinterpret_cast<uintptr_t>(&next_call) ^ (reinterpret_cast<uintptr_t>(&t) << 20)) *
+                           0x9e3779b97f4a7c15ull;   // spreads the bits over the word
+        return x ^ (x >> 29);
+    }()};
+    const uint64_t n = next.fetch_add(0x2545f4914f6cdd1dull, std::memory_order_relaxed);
+    return n != 0 ? n : next.fetch_add(0x2545f4914f6cdd1dull, std::memory_order_relaxed);
 }
 
 mbd_status check_attend(const mbd_kv_cache* c, int64_t pages_per_seq, int64_t n_seqs, int64_t n_q_heads) {
@@ -270,7 +285,8 @@ mbd_status mbd_paged_attention_decode(void* out, const void* q, int64_t q_stride
     char* base = static_cast<char*>(workspace);
     p.part_o = reinterpret_cast<float*>(base + ws.part_o);
     p.part_ml = reinterpret_cast<float4*>(base + ws.part_ml);
-    p.cut = reinterpret_cast<int4*>(base + ws.cut);
+    p.arrived = reinterpret_cast<unsigned long long*>(base + ws.arrived);
+    p.call = next_call();
     p.lse2 = reinterpret_cast<float*>(base + ws.lse2);
     p.logits = reinterpret_cast<float*>(base + ws.logits);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

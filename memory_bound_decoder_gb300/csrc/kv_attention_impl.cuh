@@ -20,8 +20,8 @@
 //
 // Work is cut by keys, not by sequences: all tiles (4 warps' steps) of all sequences and heads in a row, the CTAs of a
 // resident grid take equal shares, wherever they begin and end. A share covers whole (sequence, head) items, written
-// at once, and at most two cut ones, whose sums go to the workspace; kv_join_kernel adds those up in a fixed order.
-// A warp keeps a step of K and of V in flight at all times, across the ends of items too.
+// at once, and at most two cut ones, whose sums go to the workspace; whichever CTA delivers the last part of an item adds
+// them up, in the order of the parts, behind its share. A warp keeps a step of K and of V in flight at all times.
 #pragma once
 
 #include "kv_common.cuh"
@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kJoinThreads = 256;
+constexpr int kJoinParts = 16;   // parts of a cut item that are added up at once
 constexpr float kLazy = 8.0f;    // units of log2 that a logit may exceed the kept maximum by (p <= 2^8)
 constexpr float kShift = 6.0f;   // E4M3: p is multiplied by 2^kShift (p <= 2^14 in f16)
 constexpr float kLn2 = 0.693147180559945309f;
@@ -131,6 +131,9 @@ __device__ __forceinline__ int tiles_of(int first, int len) {
     return len > 0 ? (len - origin<S>(first) + S::kTile - 1) / S::kTile : 0;
 }
 
+// What an item counts in the shares: two units a tile, and one for its end (merging the warps, writing the result).
+__device__ __forceinline__ int units_of(int tiles) { return tiles > 0 ? 2 * tiles + 1 : 0; }
+
 // View and tiles of a sequence.
 template <class S>
 __device__ __forceinline__ int view_of(const AttendParams& p, int64_t seq, int* first, int* len) {
@@ -139,18 +142,16 @@ __device__ __forceinline__ int view_of(const AttendParams& p, int64_t seq, int* 
     return tiles_of<S>(*first, *len);
 }
 
-// The next tile: of the item, else of the next item that has some. True if that is another item.
+// The first tile of the next item that has some. False behind the last sequence.
 template <class S>
-__device__ __forceinline__ bool advance(const AttendParams& p, Cursor& cur) {
-    cur.key += S::kTile;
-    if (cur.key < cur.len) return false;
+__device__ __forceinline__ bool next_item(const AttendParams& p, Cursor& cur) {
     if (++cur.chunk == p.chunks) {
         cur.chunk = 0;
         if (++cur.head == p.c.n_kv_heads) {
             cur.head = 0;
             int tiles = 0;
             do {
-                if (++cur.seq >= p.n_seqs) return true;   // not reached while the share has tiles left
+                if (++cur.seq >= p.n_seqs) return false;
                 tiles = view_of<S>(p, cur.seq, &cur.first, &cur.len);
             } while (tiles == 0);
             cur.table = p.c.table + static_cast<int64_t>(cur.seq) * p.c.pages_per_seq;
@@ -160,12 +161,116 @@ __device__ __forceinline__ bool advance(const AttendParams& p, Cursor& cur) {
     return true;
 }
 
+// An item that is cut: it has a part in each of the shares head .. tail. Up to kJoinParts of them join at once; where
+// there are more, each run of kJoinParts does, in its first part's place, and then the runs.
+struct Cut {
+    int64_t out_head;   // its first row of the output
+    int n;              // query heads
+    int head, tail;
+    int last;           // this CTA delivered the last part of its run: it has them to join
+};
+
+// Part `me` of `parts` has been delivered; true for the last of them. Parts meet in pairs up a binary tree: whoever
+// finds the call's number in the pair's word is the second there and goes on, and leaves the word at 0 for the next
+// replay of a captured call, whose number is the same. So nobody has to clear a counter first, and no more than two
+// meet at a word. The pair that joins parts [a, a + 2^l) and [a + 2^l, ...) has word a + 2^l.
+__device__ __forceinline__ bool arrive(unsigned long long* words, unsigned long long call, int me, int parts) {
+    __threadfence();
+    for (int l = 1; l < parts; l <<= 1) {
+        const int right = (me & ~(2 * l - 1)) + l;
+        if (right >= parts) continue;   // nobody to meet
+        unsigned long long was;
+        asm volatile("atom.acq_rel.gpu.global.exch.b64 %0, [%1], %2;" : "=l"(was) : "l"(words + right), "l"(call) : "memory");
+        if (was != call) return false;
+        words[right] = 0;
+    }
+    __threadfence();
+    return true;
+}
+
 // Sums of one item (or of a part of it) over the warps of a CTA, per query head of the chunk.
 template <int D, int HT>
 struct MergeSmem {
     float o[kWarps][HT][D + 4];
     float4 ml[kWarps][HT];   // maximum of the logits, sum, exponent that o is relative to
+    Cut cut[2];              // the items that the share ends in and begins in, if they are cut
+    int last;
 };
+
+// Four elements of an output row from their sums (relative to mo) and the row's maximum and sum; with the first of them,
+// its lse.
+template <int D, int STORE>
+__device__ __forceinline__ void write_out(const AttendParams& p, int64_t head, int dim, const float4& acc, float m, float t,
+                                          float mo) {
+    const float one = STORE == kKvFp8Dynamic ? ex2(mo - m) : (STORE == kKvFp8Static ? *p.c.v_scale : 1.0f);
+    const float f = mo == -INFINITY ? 0.0f : one / t;
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + head * D + dim) =
+        make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+    if (dim == 0) {
+        const float lse2 = m == -INFINITY ? -INFINITY : m + log2f(t);
+        if (p.lse) p.lse[head] = lse2 * kLn2;
+        if (p.accumulate) p.lse2[head] = lse2;
+    }
+}
+
+// Adds up the parts in the shares a, a + step, .. b of a cut item: into its output rows, or in place of the first of them.
+template <int D, int STORE, int HT>
+__device__ __forceinline__ void join(const AttendParams& p, const Cut& cut, int a, int b, int step, bool to_output) {
+    constexpr int kLanes = kThreads / HT, kVecs = D / 4 / kLanes;   // threads of a query head, vectors of each
+    constexpr int kBatch = 16 / (kVecs + 1);                        // parts loaded at once
+    const int h = threadIdx.x / kLanes, dim = threadIdx.x % kLanes * 4, parts = (b - a) / step + 1;
+    if (h >= cut.n) return;
+    auto part_of = [&](int i) {
+        const int share = a + i * step;
+        return static_cast<int64_t>(share * 2 + (share == cut.head ? 1 : 0)) * HT + h;
+    };
+    float4 acc[kVecs];
+#pragma unroll
+    for (int e = 0; e < kVecs; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float m = -INFINITY, mo = -INFINITY, t = 0.0f;
+#pragma unroll 1
+    for (int i = 0; i < parts; i += kBatch) {
+        float4 ml[kBatch], x[kBatch][kVecs];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            ml[k] = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
+            if (i + k >= parts) continue;
+            ml[k] = __ldcg(p.part_ml + part_of(i + k));
+#pragma unroll
+            for (int e = 0; e < kVecs; ++e)
+                x[k][e] = __ldcg(reinterpret_cast<const float4*>(p.part_o + part_of(i + k) * D + dim + e * kLanes * 4));
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if (ml[k].x != -INFINITY) {
+                const float top = fmaxf(m, ml[k].x);
+                t = t * ex2(m - top) + ml[k].y * ex2(ml[k].x - top);
+                m = top;
+            }
+            if (ml[k].z == -INFINITY) continue;
+            const float top = fmaxf(mo, ml[k].z), f = ex2(mo - top), g = ex2(ml[k].z - top);
+            mo = top;
+#pragma unroll
+            for (int e = 0; e < kVecs; ++e) {
+                acc[e].x = acc[e].x * f + x[k][e].x * g;
+                acc[e].y = acc[e].y * f + x[k][e].y * g;
+                acc[e].z = acc[e].z * f + x[k][e].z * g;
+                acc[e].w = acc[e].w * f + x[k][e].w * g;
+            }
+        }
+    }
+    if (to_output) {
+#pragma unroll
+        for (int e = 0; e < kVecs; ++e) write_out<D, STORE>(p, cut.out_head + h, dim + e * kLanes * 4, acc[e], m, t, mo);
+        return;
+    }
+    // The row's maximum, sum and exponent are read by all of its threads (half a warp or a quarter) before one writes.
+    __syncwarp(((1u << kLanes) - 1u) << ((threadIdx.x & 31) / kLanes * kLanes));
+#pragma unroll
+    for (int e = 0; e < kVecs; ++e)
+        *reinterpret_cast<float4*>(p.part_o + part_of(0) * D + dim + e * kLanes * 4) = acc[e];
+    if (dim == 0) p.part_ml[part_of(0)] = make_float4(m, t, mo, 0.0f);
+}
 
 template <int D, int STORE, int NT, bool SMALL>   // SMALL: pages of fewer than 16 slots, looked up for each key
 __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
@@ -179,17 +284,19 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
     pdl_trigger();
     pdl_wait();
 
-    // The total of tiles, then this CTA's share of them: every warp scans the lengths for itself.
+    // The total of units, then this CTA's share of them, which has the tiles that begin in it: every warp scans the
+    // lengths for itself.
     int64_t total = 0;
     for (int64_t b0 = 0; b0 < p.n_seqs; b0 += 32) {
         int first, len;
-        int64_t t = b0 + lane < p.n_seqs ? view_of<S>(p, b0 + lane, &first, &len) : 0;
+        int64_t t = b0 + lane < p.n_seqs ? units_of(view_of<S>(p, b0 + lane, &first, &len)) : 0;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
         total += t;
     }
     total *= heads;
-    const int64_t cta = blockIdx.x, grid = min(static_cast<int64_t>(gridDim.x), total);   // shares, none of them empty
+    // Shares of at least two units: every share between those of an item's first and last tile has a tile of it.
+    const int64_t cta = blockIdx.x, grid = min(static_cast<int64_t>(gridDim.x), total / 2);
     const int64_t begin = cta < grid ? cta * total / grid : 0, end = cta < grid ? (cta + 1) * total / grid : 0;
     // Sequences with nothing in view: zeros, shared out over the CTAs.
     for (int64_t b = cta; b < p.n_seqs; b += gridDim.x) {
@@ -199,15 +306,17 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
             reinterpret_cast<uint4*>(p.out)[b * p.n_q_heads * (D / 8) + i] = make_uint4(0, 0, 0, 0);
         for (int i = threadIdx.x; p.lse && i < p.n_q_heads; i += kThreads) p.lse[b * p.n_q_heads + i] = -INFINITY;
     }
-    if (threadIdx.x == 0) p.cut[cta] = make_int4(-1, 0, 0, 0);
     if (begin >= end) return;
+    if (threadIdx.x < 2) sm.cut[threadIdx.x].last = 0;
 
-    Cursor ld{};   // of the step whose loads are issued next
+    // The share's first tile.
+    Cursor cur{};
+    int64_t unit = begin;   // the tile's
     {
         int64_t before = 0;
         for (int64_t b0 = 0; b0 < p.n_seqs; b0 += 32) {
             int first = 0, len = 0;
-            const int t = b0 + lane < p.n_seqs ? view_of<S>(p, b0 + lane, &first, &len) : 0;
+            const int t = b0 + lane < p.n_seqs ? units_of(view_of<S>(p, b0 + lane, &first, &len)) : 0;
             int64_t upto = t;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -218,21 +327,31 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
             if (hit) {
                 const int src = __ffs(hit) - 1;
                 const int64_t off = begin - (before + __shfl_sync(0xffffffffu, upto - t, src)) * heads;
-                const int tiles = __shfl_sync(0xffffffffu, t, src), item = static_cast<int>(off / tiles);
-                ld.first = __shfl_sync(0xffffffffu, first, src);
-                ld.len = __shfl_sync(0xffffffffu, len, src);
-                ld.seq = static_cast<int>(b0) + src;
-                ld.head = item / p.chunks;
-                ld.chunk = item - ld.head * p.chunks;
-                ld.key = origin<S>(ld.first) + static_cast<int>(off - static_cast<int64_t>(item) * tiles) * S::kTile;
-                ld.table = p.c.table + static_cast<int64_t>(ld.seq) * p.c.pages_per_seq;
+                const int units = __shfl_sync(0xffffffffu, t, src), item = static_cast<int>(off / units);
+                const int at = static_cast<int>(off - static_cast<int64_t>(item) * units);
+                cur.first = __shfl_sync(0xffffffffu, first, src);
+                cur.len = __shfl_sync(0xffffffffu, len, src);
+                cur.seq = static_cast<int>(b0) + src;
+                cur.head = item / p.chunks;
+                cur.chunk = item - cur.head * p.chunks;
+                cur.key = origin<S>(cur.first) + at / 2 * S::kTile;
+                cur.table = p.c.table + static_cast<int64_t>(cur.seq) * p.c.pages_per_seq;
+                if ((at & 1) || at == units - 1) {   // not where a tile begins
+                    if (at + 2 >= units) {
+                        next_item<S>(p, cur);
+                        unit += units - at;
+                    } else {
+                        cur.key += S::kTile;
+                        ++unit;
+                    }
+                }
                 break;
             }
             before += __shfl_sync(0xffffffffu, upto, 31);
         }
     }
+    if (unit >= end) return;
     const float k_static = STORE == kKvFp8Static ? *p.c.k_scale : 1.0f;
-    const float v_static = STORE == kKvFp8Static ? *p.c.v_scale : 1.0f;
     // This lane's places in a step whose first row is row 0 of the pools: keys r and r + 8 of K; 2c, 2c + 1 and these
     // plus 8 of V.
     const char* k_lane = static_cast<const char*>(p.c.k) + (SMALL ? 0 : r * S::kRow) + c * 16;
@@ -248,17 +367,17 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
     unsigned live[NG], live_next[NG];      // bit i: key i of the group is in view
     int page[NG];                          // of the step after the next
 
-    // Page numbers of the step at `cur`; -1 behind the sequence.
-    auto load_pages = [&](const Cursor& cur) {
+    // Page numbers of this warp's step in the tile at `tile`; -1 behind the sequence.
+    auto load_pages = [&](int tile) {
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            const int key = cur.key + warp * S::kStep + g * 16 + (SMALL ? lane & 15 : 0);
+            const int key = tile + warp * S::kStep + g * 16 + (SMALL ? lane & 15 : 0);
             page[g] = key < cur.len ? cur.table[key >> p.c.page_shift] : -1;
         }
     };
-    // Rows and view of the step at `cur`, whose page numbers were loaded.
-    auto place = [&](const Cursor& cur) {
-        const int step = cur.key + warp * S::kStep;
+    // Rows and view of the step, whose page numbers were loaded.
+    auto place = [&](int tile) {
+        const int step = tile + warp * S::kStep;
         full_next = step >= cur.first && step + S::kStep <= cur.len;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
@@ -364,8 +483,8 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
                 if ((live_next[g] >> (2 * c + kRows[i])) & 1u) load_v_row(g, i, from);
             }
     };
-    // Query heads of the chunk at `cur`, lane r's: bf16 in the order of K's vectors (E4M3: 16 elements a vector).
-    auto load_q = [&](const Cursor& cur) {
+    // Query heads of the chunk, lane r's: bf16 in the order of K's vectors (E4M3: 16 elements a vector).
+    auto load_q = [&] {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int h = cur.chunk * HT + nt * 8 + r;
@@ -434,24 +553,39 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
         }
     };
 
-    int64_t left = end - begin;
-    Cursor cur = ld;
-    bool from_start = cur.key == origin<S>(cur.first);   // this share has the current item's first tile
-    load_pages(ld);
-    place(ld);
-    load_k();
-    load_v();
-    load_q(ld);
-    bool other = false;                                  // the step after begins another item
-    if (left > 1) {
-        other = advance<S>(p, ld);
-        load_pages(ld);
-    }
-    ready_q();
-    clear();
+    // Warms L2 with this warp's rows of the tile at `tile`: a bulk prefetch for each 16 rows (SMALL: each row) of K, by
+    // lanes 0 .., and of V, by lanes 16 .. .
+    auto warm = [&](const Cursor& at, int tile) {
+        const int key = tile + warp * S::kStep + (SMALL ? lane & 15 : (lane & 15) * 16);
+        if (key >= at.len || !(SMALL || (lane & 15) < NG)) return;
+        const int pg = at.table[key >> p.c.page_shift];
+        if (static_cast<uint32_t>(pg) >= static_cast<uint32_t>(p.c.n_pages)) return;
+        const char* pool = static_cast<const char*>(lane < 16 ? p.c.k : p.c.v);
+        prefetch_l2_bulk(pool + kv_row(p.c, pg, at.head, key, S::kRow), (SMALL ? 1 : 16) * S::kRow);
+    };
+    constexpr int kAhead = NT == 2 ? 2 : 0;
+
+    // Starts on the part of an item that begins at cur.key: `tiles` of the `left` tiles that the item has from there.
+    int left, tiles;
+    auto start = [&] {
+        left = (cur.len - cur.key + S::kTile - 1) / S::kTile;
+        tiles = static_cast<int>(min(static_cast<int64_t>(left), (end - unit + 1) / 2));
+        load_pages(cur.key);
+        load_q();
+        place(cur.key);
+        load_k();
+        load_v();
+        if (tiles > 1) load_pages(cur.key + S::kTile);
+    };
+    start();
 
     while (true) {
-        const bool more = left > 1, closes = !more || other;
+        ready_q();
+        clear();
+        const int last_tile = cur.key + (tiles - 1) * S::kTile;
+#pragma unroll 1
+        for (int tile = cur.key; tile <= last_tile; tile += S::kTile) {
+        const bool more = tile < last_tile;
         full = full_next;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
@@ -496,9 +630,10 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
                 }
             }
         if (more) {
-            place(ld);
+            place(tile + S::kTile);
             load_k();
-            if (other) load_q(ld);
+            if (tile + S::kTile < last_tile) load_pages(tile + 2 * S::kTile);
+            if (kAhead > 0 && tile + (kAhead + 1) * S::kTile <= last_tile) warm(cur, tile + (kAhead + 1) * S::kTile);
         }
 
         // Softmax of the step: x in place of s, then p in place of x.
@@ -522,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
         }
         if (p.accumulate) {
             const int h0 = cur.chunk * HT + 2 * c;
-            float* to = p.logits + ((static_cast<int64_t>(cur.seq) * p.c.n_kv_heads + cur.head) * p.c.capacity + cur.key +
+            float* to = p.logits + ((static_cast<int64_t>(cur.seq) * p.c.n_kv_heads + cur.head) * p.c.capacity + tile +
                                     warp * S::kStep + r) * p.logit_heads + h0;
 #pragma unroll
             for (int g = 0; g < NG; ++g)
@@ -633,8 +768,21 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
                 }
         }
         if (more) load_v();
+        }
 
-        if (closes) {
+        // The part is over: on to the next item before its end is dealt with.
+        const bool from_start = cur.key == origin<S>(cur.first), to_end = tiles == left;
+        const int h0 = cur.chunk * HT, n = min(HT, p.group - h0);
+        const int64_t out_head = static_cast<int64_t>(cur.seq) * p.n_q_heads + cur.head * p.group + h0;
+        const int64_t last_unit = unit + 2 * (static_cast<int64_t>(left) - 1);   // of the item's last tile; its first:
+        const int64_t first_unit = unit - 2 * static_cast<int64_t>((cur.key - origin<S>(cur.first)) / S::kTile);
+        unit = last_unit + 3;
+        const bool more = unit < end;
+        if (more) {
+            next_item<S>(p, cur);
+            start();
+        }
+        {
             // The four warps' sums join in shared memory.
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -656,9 +804,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
                     if (r == 0) sm.ml[warp][head] = make_float4(m, t, mo, 0.0f);
                 }
             __syncthreads();
-            const int h0 = cur.chunk * HT, n = min(HT, p.group - h0);
-            const int64_t out_head = static_cast<int64_t>(cur.seq) * p.n_q_heads + cur.head * p.group + h0;
-            const bool to_end = cur.key + S::kTile >= cur.len, whole = from_start && to_end;
+            const bool whole = from_start && to_end;
             const int slot = from_start ? 1 : 0;
             for (int i = threadIdx.x; i < n * (D / 4); i += kThreads) {
                 const int h = i / (D / 4), dim = i % (D / 4) * 4;
@@ -684,150 +830,46 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
                     acc.w += x.w * f;
                 }
                 if (whole) {
-                    const float f = mo == -INFINITY ? 0.0f : (kDyn ? ex2(mo - m) : v_static) / t;
-                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + (out_head + h) * D + dim) =
-                        make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
-                    if (dim == 0) {
-                        const float lse2 = m == -INFINITY ? -INFINITY : m + log2f(t);
-                        if (p.lse) p.lse[out_head + h] = lse2 * kLn2;
-                        if (p.accumulate) p.lse2[out_head + h] = lse2;
-                    }
+                    write_out<D, STORE>(p, out_head + h, dim, acc, m, t, mo);
                 } else {
                     const int64_t part = (cta * 2 + slot) * HT + h;
                     *reinterpret_cast<float4*>(p.part_o + part * D + dim) = acc;
                     if (dim == 0) p.part_ml[part] = make_float4(m, t, mo, 0.0f);
                 }
             }
-            if (from_start && !to_end && threadIdx.x == 0) {
-                // The share that holds the item's last tile: the last one that begins at or before it.
-                const int64_t item_end = end - left + (cur.len - cur.key + S::kTile - 1) / S::kTile;   // exclusive
-                const int64_t last = (item_end * grid - 1) / total;
-                p.cut[cta] = make_int4(cur.seq, cur.head * p.chunks + cur.chunk, static_cast<int>(last), n);
-            }
             __syncthreads();
-            if (!more) break;
-            from_start = true;
-            ready_q();
-            clear();
+            if (!whole && threadIdx.x == 0) {
+                const int head = static_cast<int>(((first_unit + 1) * grid - 1) / total);
+                const int tail = static_cast<int>(((last_unit + 1) * grid - 1) / total);
+                const int run = (static_cast<int>(cta) - head) / kJoinParts * kJoinParts + head;
+                const bool last = arrive(p.arrived + run, p.call, static_cast<int>(cta) - run, min(tail - run + 1, kJoinParts));
+                sm.cut[slot] = Cut{out_head, n, head, tail, last};
+            }
         }
-        cur = ld;
-        --left;
-        if (left > 1) {
-            other = advance<S>(p, ld);
-            load_pages(ld);
-        }
+        if (!more) break;
     }
-}
 
-// Adds up the parts of the items that were cut. blockIdx.x: the share in which an item begins that ends in a later one;
-// its parts are slot 1 of that share and slot 0 of the following ones. blockIdx.y: a slice of its query heads.
-template <int D, int STORE, int NT>
-__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(const __grid_constant__ AttendParams p, int heads_per_cta) {
-    constexpr int HT = 8 * NT, C = D / 4;   // columns of 4 elements
-    __shared__ float4 s_acc[kJoinThreads];
-    __shared__ float s_top[HT], s_topo[HT], s_sum[HT];
-    pdl_trigger();
-    pdl_wait();
-    const int64_t first = blockIdx.x;
-    const int4 cut = p.cut[first];
-    const int h0 = blockIdx.y * heads_per_cta, n = min(heads_per_cta, cut.w - h0);
-    if (cut.x < 0 || n <= 0) return;
-    const int parts = cut.z - static_cast<int>(first) + 1;
-    auto part_of = [&](int i) { return (i == 0 ? first * 2 + 1 : (first + i) * 2) * HT + h0; };
-    // Maxima and sums of each head: a warp per head in turn, the parts over its lanes.
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int h = warp; h < n; h += kJoinThreads / 32) {
-        float top = -INFINITY, topo = -INFINITY, t = 0.0f;
-        for (int i = lane; i < parts; i += 32) {
-            const float4 ml = p.part_ml[part_of(i) + h];
-            top = fmaxf(top, ml.x);
-            topo = fmaxf(topo, ml.z);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            topo = fmaxf(topo, __shfl_xor_sync(0xffffffffu, topo, o));
-        }
-        for (int i = lane; i < parts; i += 32) {
-            const float4 ml = p.part_ml[part_of(i) + h];
-            if (ml.x != -INFINITY) t += ml.y * ex2(ml.x - top);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-        if (lane == 0) {
-            s_top[h] = top;
-            s_topo[h] = topo;
-            s_sum[h] = t;
-        }
-    }
+    // The cut items whose parts are complete.
     __syncthreads();
-    const float v_static = STORE == kKvFp8Static ? *p.c.v_scale : 1.0f;
-    const int kv_head = cut.y / p.chunks;
-    const int64_t out_head = cut.x * static_cast<int64_t>(p.n_q_heads) + static_cast<int64_t>(kv_head) * p.group +
-                             (cut.y - kv_head * p.chunks) * HT + h0;
-    // Columns over the threads; where there are fewer columns than threads, the parts too.
-    const int columns = n * C, span = min(kJoinThreads, columns), ways = kJoinThreads / span;
-    const int way = threadIdx.x / span;
-    for (int base = 0; base < columns; base += span) {
-        const int i = base + threadIdx.x % span;
-        const int h = i / C, dim = i % C * 4;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (way < ways && i < columns) {
-#pragma unroll 4
-            for (int k = way; k < parts; k += ways) {
-                const int64_t part = part_of(k) + h;
-                const float e = p.part_ml[part].z;
-                const float4 x = *reinterpret_cast<const float4*>(p.part_o + part * D + dim);
-                const float f = e == -INFINITY ? 0.0f : ex2(e - s_topo[h]);
-                acc.x += x.x * f;
-                acc.y += x.y * f;
-                acc.z += x.z * f;
-                acc.w += x.w * f;
-            }
-        }
-        if (ways > 1) {
-            s_acc[threadIdx.x] = acc;
-            __syncthreads();
-            if (way == 0)
-                for (int w = 1; w < ways; ++w) {
-                    const float4 x = s_acc[w * span + threadIdx.x];
-                    acc.x += x.x;
-                    acc.y += x.y;
-                    acc.z += x.z;
-                    acc.w += x.w;
-                }
-            __syncthreads();
-        }
-        if (way == 0 && i < columns) {
-            const float f = s_topo[h] == -INFINITY ? 0.0f : ex2(s_topo[h] - s_top[h]) * v_static / s_sum[h];
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + (out_head + h) * D + dim) =
-                make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
-            if (dim == 0) {
-                const float lse2 = s_top[h] == -INFINITY ? -INFINITY : s_top[h] + log2f(s_sum[h]);
-                if (p.lse) p.lse[out_head + h] = lse2 * kLn2;
-                if (p.accumulate) p.lse2[out_head + h] = lse2;
-            }
-        }
+#pragma unroll 1
+    for (int slot = 0; slot < 2; ++slot) {
+        const Cut cut = sm.cut[slot];
+        if (!cut.last) continue;
+        const int runs = (cut.tail - cut.head) / kJoinParts + 1, mine = (static_cast<int>(cta) - cut.head) / kJoinParts;
+        const int run = cut.head + mine * kJoinParts;
+        join<D, STORE, HT>(p, cut, run, min(cut.tail, run + kJoinParts - 1), 1, runs == 1);
+        if (runs == 1) continue;
+        __syncthreads();
+        if (threadIdx.x == 0) sm.last = arrive(p.arrived + p.grid + cut.head, p.call, mine, runs);
+        __syncthreads();
+        if (sm.last) join<D, STORE, HT>(p, cut, cut.head, cut.tail, kJoinParts, true);
     }
 }
 
 template <int D, int STORE, int NT>
 cudaError_t launch_nt(const AttendParams& p, cudaStream_t s) {
-    const cudaError_t e = p.c.page_shift < 4 ? kv_launch(kv_attend_kernel<D, STORE, NT, true>, p.grid, kThreads, 0, 1, s, p)
-                                            : kv_launch(kv_attend_kernel<D, STORE, NT, false>, p.grid, kThreads, 0, 1, s, p);
-    if (e != cudaSuccess) return e;
-    // Few items: many parts each, so a CTA per query head. Many: two parts as a rule, and one CTA for all of them.
-    const bool few = p.n_seqs * p.c.n_kv_heads * p.chunks < p.grid;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3(p.grid, few ? (p.group < 8 * NT ? p.group : 8 * NT) : 1);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = s;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv_join_kernel<D, STORE, NT>, p, few ? 1 : 8 * NT);
+    return p.c.page_shift < 4 ? kv_launch(kv_attend_kernel<D, STORE, NT, true>, p.grid, kThreads, 0, 1, s, p)
+                              : kv_launch(kv_attend_kernel<D, STORE, NT, false>, p.grid, kThreads, 0, 1, s, p);
 }
 
 template <int D, int STORE>
