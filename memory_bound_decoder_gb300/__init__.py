@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import sys
 from typing import Any, List, Optional
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -177,14 +178,12 @@ def _mode(mode: Any) -> int:
 
 
 def _stream(stream: Any) -> Optional[int]:
+    """The raw stream: torch's current one (of its current device) if none is given and torch uses CUDA."""
     if stream is None:
-        try:
-            import torch
-            if torch.cuda.is_available() and torch.cuda.is_initialized():
-                return int(torch.cuda.current_stream().cuda_stream)
-        except ImportError:
-            pass
-        return None
+        torch = sys.modules.get("torch")
+        if torch is None or not torch.cuda.is_initialized():
+            return None
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return int(getattr(stream, "cuda_stream"))

@@ -324,12 +324,12 @@ mbd_status mbd_kv_cache_evict(const mbd_kv_cache* cache, int32_t* new_lens, cons
     p.n_seqs = n_seqs;
     p.budget = budget;
     p.recent = recent;
-    // CTAs of a row: as many as its slots need at kMaxSlots each, more while the grid leaves SMs without work (two CTAs
-    // fit an SM) and each keeps a thousand slots.
+    // CTAs of a row: as many as its slots need at kMaxSlots each, more while all of them stay resident at once (two fit an
+    // SM) and each keeps a thousand slots.
     constexpr int64_t kMaxSlots = MBD_KV_MAX_EVICT_CAPACITY / 16;
     const int64_t rows = n_seqs * cache->n_kv_heads, sms = mbd::kv_sm_count();
     int ctas = 1;
-    while (ctas < 16 && (capacity > kMaxSlots * ctas || (rows * ctas < 2 * sms && capacity >= int64_t{2048} * ctas)))
+    while (ctas < 16 && (capacity > kMaxSlots * ctas || (2 * rows * ctas <= 2 * sms && capacity >= int64_t{2048} * ctas)))
         ctas *= 2;
     p.ctas_per_row = ctas;
     p.slots_per_cta = static_cast<int>((capacity + ctas - 1) / ctas);

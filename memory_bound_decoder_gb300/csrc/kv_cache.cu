@@ -201,7 +201,13 @@ __device__ __forceinline__ uint2 scan_warps(EvictSmem& sm, unsigned a, unsigned 
     return before;
 }
 
+__device__ __forceinline__ bool on_pool(int page, const KvView& c) {
+    return static_cast<uint32_t>(page) < static_cast<uint32_t>(c.n_pages);
+}
+
 __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const __grid_constant__ EvictParams p) {
+    constexpr int kLoads = 8;   // slots of a thread whose weight and position are in flight
+    constexpr int kMoves = 4;   // rows of a lane group in flight
     extern __shared__ uint32_t slots[];   // keys [slots_per_cta], then positions, later the lists of moves
     __shared__ EvictSmem sm;
     cg::cluster_group cluster = cg::this_cluster();
@@ -220,22 +226,38 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const __grid
     const int64_t first = static_cast<int64_t>(rank) * share;
     const int n = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(share), len - first)));
     uint32_t* key = slots;
+    const int32_t* const table = p.c.table + seq * p.c.pages_per_seq;
     int* aux = reinterpret_cast<int*>(slots + p.slots_per_cta);
 
+    // Loads are issued kLoads at a time without a branch between them: a thread behind the end repeats the last slot, a
+    // bad page counts as page 0 until its slot's key is set.
     int newest = INT32_MIN;
-    for (int i = tid; i < n; i += kEvictThreads) {
-        const int64_t page = kv_page(p.c, seq, first + i);
-        uint32_t k = 0u;
-        int at = INT32_MIN;
-        if (page >= 0) {
-            const int64_t m = kv_meta(p.c, page, head, first + i);
-            k = order_key(p.c.weight[m]);
-            at = p.c.position[m];
+    bool bad = false;
+    for (int i0 = tid; i0 < n; i0 += kEvictThreads * kLoads) {
+        int page[kLoads], at[kLoads];
+        float w[kLoads];
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u)
+            page[u] = table[(first + min(i0 + u * kEvictThreads, n - 1)) >> p.c.page_shift];
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            const int64_t m = kv_meta(p.c, on_pool(page[u], p.c) ? page[u] : 0, head, first + min(i0 + u * kEvictThreads, n - 1));
+            w[u] = p.c.weight[m];
+            at[u] = p.c.position[m];
         }
-        key[i] = k;
-        aux[i] = at;
-        newest = max(newest, at);
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+            const int i = i0 + u * kEvictThreads;
+            const bool good = on_pool(page[u], p.c);
+            bad |= !good;
+            if (i < n) {
+                key[i] = good ? order_key(w[u]) : 0u;
+                aux[i] = good ? at[u] : INT32_MIN;
+            }
+            newest = max(newest, good ? at[u] : INT32_MIN);
+        }
     }
+    if (bad) kv_bad_index();
     if (tid == 0) sm.max_position = INT32_MIN;
     if (tid < 256) sm.hist[0][tid] = 0;
     __syncthreads();
@@ -263,7 +285,16 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const __grid
         cluster.sync();
         unsigned mine = 0, at_least = 0;
         if (tid < 256) {
-            for (int r = 0; r < ctas; ++r) mine += cluster.map_shared_rank(hist, r)[tid];
+            if (ctas == 16) {
+                unsigned part[16];   // all at once: each is a round trip to another SM
+#pragma unroll
+                for (int r = 0; r < 16; ++r) part[r] = cluster.map_shared_rank(hist, r)[tid];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) mine += part[r];
+            } else {
+#pragma unroll 4
+                for (int r = 0; r < ctas; ++r) mine += cluster.map_shared_rank(hist, r)[tid];
+            }
             sm.hist[(pass + 1) & 1][tid] = 0;
             at_least = mine;   // of this bin and the higher ones: within the warp, then over the warps
             for (int o = 1; o < 32; o <<= 1) {
@@ -331,6 +362,8 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const __grid
     // The lists, entry i with CTA i / chunk of the cluster: slots given up, then the rows that take their places.
     const unsigned chunk = (moves + ctas - 1) / ctas;
     if (moves > 0) {
+        // e / chunk by a product: exact while e * chunk < 2^32, and 425984 slots give at most 212992 * 13312.
+        const unsigned inverse = chunk > 1 ? 0xffffffffu / chunk + 1 : 0;
         const unsigned below = (1u << lane) - 1u;
         equal = equal_before;
         for (int i = lo; i < hi; i += 32) {
@@ -340,33 +373,63 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const __grid
             const bool hole = (h >> lane) & 1u, mover = (m >> lane) & 1u;
             if (hole || mover) {
                 const unsigned e = hole ? at.x + __popc(h & below) : at.y + __popc(m & below);
-                int* list = cluster.map_shared_rank(aux, e / chunk);
-                list[(e % chunk) * 2 + (mover ? 1 : 0)] = static_cast<int>(first) + i + lane;
+                const unsigned owner = chunk > 1 ? __umulhi(e, inverse) : e;
+                int* list = cluster.map_shared_rank(aux, owner);
+                list[(e - owner * chunk) * 2 + (mover ? 1 : 0)] = static_cast<int>(first) + i + lane;
             }
             at = make_uint2(at.x + __popc(h), at.y + __popc(m));
         }
     }
     cluster.sync();   // the lists are complete; no CTA touches another's shared memory from here on
-    if (moves == 0) return;
-    const int mine = static_cast<int>(max(0, min(static_cast<int>(chunk), static_cast<int>(moves) - rank * static_cast<int>(chunk))));
+    const int mine = min(static_cast<int>(chunk), static_cast<int>(moves) - rank * static_cast<int>(chunk));
+    if (mine <= 0) return;
     const int row_bytes = p.c.head_dim * (p.c.store == kKvBf16 ? 2 : 1);
-    const int lanes = row_bytes / 16, part = tid % lanes;   // 4 to 32 lanes own a row
-    for (int i = tid / lanes; i < mine; i += kEvictThreads / lanes) {
-        const int64_t to = aux[2 * i], from = aux[2 * i + 1];
-        const int64_t page_to = kv_page(p.c, seq, to), page_from = kv_page(p.c, seq, from);
-        if (page_to < 0 || page_from < 0) continue;
-        const int64_t a = kv_row(p.c, page_from, head, from, row_bytes) + part * 16;
-        const int64_t b = kv_row(p.c, page_to, head, to, row_bytes) + part * 16;
-        const uint4 k = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.c.k) + a);
-        const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const char*>(p.c.v) + a);
-        *reinterpret_cast<uint4*>(static_cast<char*>(p.c.k) + b) = k;
-        *reinterpret_cast<uint4*>(static_cast<char*>(p.c.v) + b) = v;
-        const int64_t ma = kv_meta(p.c, page_from, head, from), mb = kv_meta(p.c, page_to, head, to);
-        if (part == 0) p.c.weight[mb] = p.c.weight[ma];
-        if (part == 1) p.c.position[mb] = p.c.position[ma];
+    const int lanes = row_bytes / 16, part = tid % lanes, groups = kEvictThreads / lanes;   // 4 to 32 lanes own a row
+    // Weights, positions and scales, a thread for a row: neighbours in the lists are neighbours in the cache, and share
+    // sectors. (With the row's own lanes, one word each, they took longer than k and v: 26 of 58 thousand cycles at
+    // 1546 rows of 128 bytes a CTA.)
+    for (int i = tid; i < mine; i += kEvictThreads) {
+        const int2 move = reinterpret_cast<const int2*>(aux)[i];
+        const int page_to = table[move.x >> p.c.page_shift], page_from = table[move.y >> p.c.page_shift];
+        if (!on_pool(page_to, p.c) || !on_pool(page_from, p.c)) continue;
+        const int64_t a = kv_meta(p.c, page_from, head, move.y), b = kv_meta(p.c, page_to, head, move.x);
+        const float w = p.c.weight[a];
+        const int32_t at_position = p.c.position[a];
+        float ks = 0.0f, vs = 0.0f;
         if (p.c.store == kKvFp8Dynamic) {
-            if (part == 2) p.c.k_scale[mb] = p.c.k_scale[ma];
-            if (part == 3) p.c.v_scale[mb] = p.c.v_scale[ma];
+            ks = p.c.k_scale[a];
+            vs = p.c.v_scale[a];
+        }
+        p.c.weight[b] = w;
+        p.c.position[b] = at_position;
+        if (p.c.store == kKvFp8Dynamic) {
+            p.c.k_scale[b] = ks;
+            p.c.v_scale[b] = vs;
+        }
+    }
+    for (int i0 = tid / lanes; i0 < mine; i0 += groups * kMoves) {   // loads without a branch between them, as above
+        int page_to[kMoves], page_from[kMoves];
+        uint4 k[kMoves], v[kMoves];
+#pragma unroll
+        for (int u = 0; u < kMoves; ++u) {
+            const int2 move = reinterpret_cast<const int2*>(aux)[min(i0 + u * groups, mine - 1)];
+            page_to[u] = table[move.x >> p.c.page_shift];
+            page_from[u] = table[move.y >> p.c.page_shift];
+        }
+#pragma unroll
+        for (int u = 0; u < kMoves; ++u) {
+            const int from = aux[2 * min(i0 + u * groups, mine - 1) + 1], page = on_pool(page_from[u], p.c) ? page_from[u] : 0;
+            const int64_t a = kv_row(p.c, page, head, from, row_bytes) + part * 16;
+            k[u] = load_stream(reinterpret_cast<const uint4*>(static_cast<const char*>(p.c.k) + a));
+            v[u] = load_stream(reinterpret_cast<const uint4*>(static_cast<const char*>(p.c.v) + a));
+        }
+#pragma unroll
+        for (int u = 0; u < kMoves; ++u) {
+            if (i0 + u * groups >= mine || !on_pool(page_from[u], p.c) || !on_pool(page_to[u], p.c)) continue;
+            const int to = aux[2 * (i0 + u * groups)];
+            const int64_t b = kv_row(p.c, page_to[u], head, to, row_bytes) + part * 16;
+            *reinterpret_cast<uint4*>(static_cast<char*>(p.c.k) + b) = k[u];
+            *reinterpret_cast<uint4*>(static_cast<char*>(p.c.v) + b) = v[u];
         }
     }
 }
