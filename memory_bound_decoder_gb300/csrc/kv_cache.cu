@@ -27,133 +27,179 @@ namespace {
 constexpr int kAppendThreads = 256;
 constexpr int kAppendMaxTokens = 16;   // tokens of one CTA
 
-// The sequence that owns row t of the new tokens: the last b with cu[b] <= t.
+// The sequence that owns row t of the new tokens, the last b with cu[b] <= t, found by a whole warp: 32 places at a time.
 __device__ __forceinline__ int64_t owner_of(const int32_t* cu, int64_t n_seqs, int64_t t) {
-    int64_t lo = 0, hi = n_seqs;
+    const int lane = threadIdx.x & 31;
+    int64_t lo = 0, hi = n_seqs;   // cu[lo] <= t (or lo == 0), cu[hi] > t (or hi == n_seqs)
     while (hi - lo > 1) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (cu[mid] <= t) lo = mid;
-        else hi = mid;
+        const int64_t step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
+        const unsigned above = __ballot_sync(0xffffffffu, at >= hi || cu[at] > t);   // the last lane's always is
+        const int64_t from = lo + (__ffs(above) - 1) * step;
+        hi = min(hi, from + step);
+        lo = from;
     }
     return lo;
 }
 
-struct Quad {
-    float v[8];
+// A scale to divide by. A correctly rounded quotient from the correctly rounded reciprocal r and the remainder of v r
+// (Markstein's theorem, "IA-64 and Elementary Functions", 2000; it excludes divisors whose significand is all ones):
+// three instructions for two elements. It needs a remainder that does not underflow, so scales below 2^-60 (or above
+// 2^60) are divided by.
+struct Divisor {
+    float scale, r;
+    uint32_t most, least;   // +-1024 scales as pairs of bf16: codes saturate at 448, and the quotient has to stay finite
+    bool fast;
 };
 
-__device__ __forceinline__ Quad unpack(const uint4& w) {
-    Quad q;
-    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        q.v[2 * i] = bf16_lo(x[i]);
-        q.v[2 * i + 1] = bf16_hi(x[i]);
-    }
-    return q;
+__device__ __forceinline__ Divisor divisor(float scale) {
+    Divisor d;
+    d.scale = scale;
+    d.r = __frcp_rn(scale);
+    d.most = pack_bf16x2(1024.0f * scale, 1024.0f * scale);
+    d.least = d.most ^ 0x80008000u;
+    d.fast = scale >= 0x1p-60f && scale <= 0x1p60f && (__float_as_uint(scale) & 0x7fffffu) != 0x7fffffu;
+    return d;
 }
 
-// Eight values over one scale as E4M3 codes; a zero scale gives zero codes.
-__device__ __forceinline__ uint2 encode(const Quad& q, float scale) {
-    if (scale == 0.0f) return make_uint2(0u, 0u);
-    float d[8];
+__device__ __forceinline__ float2 quotient(float2 v, const Divisor& d) {
+    const float2 r = f2(d.r), q = __fmul2_rn(v, r);
+    return __ffma2_rn(__ffma2_rn(q, f2(-d.scale), v), r, q);
+}
+
+__device__ __forceinline__ uint32_t clamp_bf16x2(uint32_t w, const Divisor& d) {
+    uint32_t x;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(w), "r"(d.most));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(x), "r"(d.least));
+    return x;
+}
+
+// Eight bf16 values over one scale as E4M3 codes; a zero scale gives zero codes. CLAMP: the values may exceed 1024
+// scales (they do not where the scale is the row's own).
+template <bool CLAMP>
+__device__ __forceinline__ uint2 encode(const uint4& x, const Divisor& s) {
+    if (s.scale == 0.0f) return make_uint2(0u, 0u);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float2 d[4];
+    if (s.fast) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) d[i] = __fdiv_rn(q.v[i], scale);
-    return make_uint2(pack_e4m3x4(d[0], d[1], d[2], d[3]), pack_e4m3x4(d[4], d[5], d[6], d[7]));
+        for (int i = 0; i < 4; ++i) d[i] = quotient(bf16x2_to_float2(CLAMP ? clamp_bf16x2(w[i], s) : w[i]), s);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = make_float2(__fdiv_rn(bf16_lo(w[i]), s.scale), __fdiv_rn(bf16_hi(w[i]), s.scale));
+    }
+    return make_uint2(pack_e4m3x4(d[0], d[1]), pack_e4m3x4(d[2], d[3]));
+}
+
+// Largest magnitude of eight bf16 values.
+__device__ __forceinline__ float amax(const uint4& x) {
+    uint32_t m = max_bf16x2_bits(max_bf16x2_bits(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                 max_bf16x2_bits(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+    return fmaxf(bf16_lo(m), bf16_hi(m));
 }
 
 template <int STORE, int LANES>   // LANES = head_dim / 8: the lanes that own one head's row
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ AppendParams p,
-                                                                   int tokens_per_cta) {
-    __shared__ int64_t s_page[kAppendMaxTokens], s_slot[kAppendMaxTokens];
+                                                                   int tokens_per_cta, unsigned inverse) {
+    // Of each token: the byte offset of head 0's row in the pools (-1: no slot), the index of its scale, the slot.
+    __shared__ int64_t s_row[kAppendMaxTokens], s_meta[kAppendMaxTokens];
+    __shared__ int s_slot[kAppendMaxTokens];
+    constexpr int kRow = LANES * (STORE == kKvBf16 ? 16 : 8);
     pdl_trigger();
     pdl_wait();
     const int64_t first = static_cast<int64_t>(blockIdx.x) * tokens_per_cta;
     const int tid = threadIdx.x;
-    if (tid < tokens_per_cta) {
-        const int64_t t = first + tid;
-        int64_t page = -1, slot = 0;
-        if (t < p.n_tokens) {
-            const int64_t seq = p.cu_tokens ? owner_of(p.cu_tokens, p.n_seqs, t) : t;
+    const int tokens = static_cast<int>(min(static_cast<int64_t>(tokens_per_cta), p.n_tokens - first));
+    const int per_token = p.c.n_kv_heads * LANES;   // 16-byte vectors of one token's keys
+    const int total = tokens * per_token, lane = tid % LANES;
+    constexpr int kBatch = 2;                       // vectors of k and of v that a thread has in flight
+    // i / per_token: `inverse` is 2^32 / per_token rounded up, exact while i * per_token < 2^32 (launch_kv_append).
+    auto token_of = [&](int i) { return tokens_per_cta == 1 ? 0 : static_cast<int>(__umulhi(i, inverse)); };
+    uint4 k[kBatch], v[kBatch];
+    auto load = [&](int base) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int i = base + u * kAppendThreads + tid, local = token_of(i);
+            k[u] = v[u] = make_uint4(0, 0, 0, 0);
+            if (i >= total) continue;
+            const int64_t at = (first + local) * p.row_bytes + static_cast<int64_t>(i - local * per_token) * 16;
+            k[u] = load_stream(reinterpret_cast<const uint4*>(static_cast<const char*>(p.k) + at));
+            v[u] = load_stream(reinterpret_cast<const uint4*>(static_cast<const char*>(p.v) + at));
+        }
+    };
+    load(0);   // rows need no slot to be read: their loads are under way while the slots are looked up
+    for (int j = tid >> 5; j < tokens; j += kAppendThreads / 32) {
+        const int64_t t = first + j;
+        const int64_t seq = p.cu_tokens ? owner_of(p.cu_tokens, p.n_seqs, t) : t;
+        if ((tid & 31) == 0) {
             const int64_t begin = p.cu_tokens ? p.cu_tokens[seq] : t, end = p.cu_tokens ? p.cu_tokens[seq + 1] : t + 1;
+            int64_t page = -1, slot = 0;
             if (t >= begin && t < end) {   // rows behind the last sequence's are padding
                 slot = static_cast<int64_t>(p.seq_lens[seq]) - end + t;
                 if (slot >= 0 && slot < p.c.capacity) page = kv_page(p.c, seq, slot);
                 else kv_bad_index();
             }
+            s_row[j] = page >= 0 ? kv_row(p.c, page, 0, slot, kRow) : -1;
+            s_meta[j] = page >= 0 ? kv_meta(p.c, page, 0, slot) : 0;
+            s_slot[j] = static_cast<int>(slot);
         }
-        s_page[tid] = page;
-        s_slot[tid] = slot;
     }
     __syncthreads();
-    float ks = 0.0f, vs = 0.0f;
+    Divisor ks{}, vs{};
     if constexpr (STORE == kKvFp8Static) {
-        ks = *p.c.k_scale;
-        vs = *p.c.v_scale;
+        ks = divisor(*p.c.k_scale);
+        vs = divisor(*p.c.v_scale);
     }
-    const int per_token = p.c.n_kv_heads * LANES;      // 16-byte vectors of one token's keys
-    const int total = tokens_per_cta * per_token;
-    const int lane = tid % LANES;
-    // Every lane of a warp stays in the loop as long as one of them has a row: the dynamic scale shuffles.
-    for (int base = tid - (tid & 31); base < total; base += kAppendThreads) {
-        const int i = base + (tid & 31);
-        const int local = i / per_token, head = (i - local * per_token) / LANES;
-        const int64_t page = i < total ? s_page[local] : -1, slot = i < total ? s_slot[local] : 0;
-        const bool live = page >= 0;
-        uint4 k = make_uint4(0, 0, 0, 0), v = k;
-        const int64_t t = first + local;
-        if (live) {
-            const int64_t at = t * p.row_bytes + (static_cast<int64_t>(head) * LANES + lane) * 16;
-            k = load_stream(reinterpret_cast<const uint4*>(static_cast<const char*>(p.k) + at));
-            v = load_stream(reinterpret_cast<const uint4*>(static_cast<const char*>(p.v) + at));
-        }
-        const int64_t meta = live ? kv_meta(p.c, page, head, slot) : 0;
-        if constexpr (STORE == kKvBf16) {
-            if (live) {
-                const int64_t to = kv_row(p.c, page, head, slot, LANES * 16) + lane * 16;
-                *reinterpret_cast<uint4*>(static_cast<char*>(p.c.k) + to) = k;
-                *reinterpret_cast<uint4*>(static_cast<char*>(p.c.v) + to) = v;
-            }
-        } else {
-            const Quad a = unpack(k), b = unpack(v);
-            if constexpr (STORE == kKvFp8Dynamic) {
-                float ka = 0.0f, va = 0.0f;
+    // Every thread stays in the loop until all are done: the dynamic scale shuffles.
+    for (int base = 0; base < total; base += kAppendThreads * kBatch) {
+        if (base > 0) load(base);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    ka = fmaxf(ka, fabsf(a.v[e]));
-                    va = fmaxf(va, fabsf(b.v[e]));
+        for (int u = 0; u < kBatch; ++u) {
+            const int i = base + u * kAppendThreads + tid, local = min(token_of(i), tokens - 1);
+            const int head = (i - local * per_token) / LANES;
+            const int64_t row = s_row[local];
+            const bool live = i < total && row >= 0;
+            const int64_t to = row + (static_cast<int64_t>(head) << p.c.page_shift) * kRow + lane * (kRow / LANES);
+            const int64_t meta = s_meta[local] + (static_cast<int64_t>(head) << p.c.page_shift);
+            if constexpr (STORE == kKvBf16) {
+                if (live) {
+                    *reinterpret_cast<uint4*>(static_cast<char*>(p.c.k) + to) = k[u];
+                    *reinterpret_cast<uint4*>(static_cast<char*>(p.c.v) + to) = v[u];
                 }
+            } else {
+                if constexpr (STORE == kKvFp8Dynamic) {
+                    float ka = amax(k[u]), va = amax(v[u]);
 #pragma unroll
-                for (int o = LANES / 2; o > 0; o >>= 1) {
-                    ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, o));
-                    va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, o));
+                    for (int o = LANES / 2; o > 0; o >>= 1) {
+                        ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, o));
+                        va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, o));
+                    }
+                    ks = divisor(__fdiv_rn(ka, 448.0f));
+                    vs = divisor(__fdiv_rn(va, 448.0f));
+                    if (live && lane == 0) {
+                        p.c.k_scale[meta] = ks.scale;
+                        p.c.v_scale[meta] = vs.scale;
+                    }
                 }
-                ks = __fdiv_rn(ka, 448.0f);
-                vs = __fdiv_rn(va, 448.0f);
-                if (live && lane == 0) {
-                    p.c.k_scale[meta] = ks;
-                    p.c.v_scale[meta] = vs;
+                if (live) {
+                    constexpr bool kClamp = STORE == kKvFp8Static;
+                    *reinterpret_cast<uint2*>(static_cast<char*>(p.c.k) + to) = encode<kClamp>(k[u], ks);
+                    *reinterpret_cast<uint2*>(static_cast<char*>(p.c.v) + to) = encode<kClamp>(v[u], vs);
                 }
             }
-            if (live) {
-                const int64_t to = kv_row(p.c, page, head, slot, LANES * 8) + lane * 8;
-                *reinterpret_cast<uint2*>(static_cast<char*>(p.c.k) + to) = encode(a, ks);
-                *reinterpret_cast<uint2*>(static_cast<char*>(p.c.v) + to) = encode(b, vs);
+            if (live && lane == 0) {
+                if (p.c.weight) p.c.weight[meta] = 0.0f;
+                if (p.c.position) p.c.position[meta] = p.positions ? p.positions[first + local] : s_slot[local];
             }
-        }
-        if (live && lane == 0) {
-            if (p.c.weight) p.c.weight[meta] = 0.0f;
-            if (p.c.position) p.c.position[meta] = p.positions ? p.positions[t] : static_cast<int32_t>(slot);
         }
     }
 }
 
 template <int STORE>
-cudaError_t launch_append(const AppendParams& p, unsigned grid, int tokens, cudaStream_t s) {
+cudaError_t launch_append(const AppendParams& p, unsigned grid, int tokens, unsigned inverse, cudaStream_t s) {
     switch (p.c.head_dim) {
-        case 64: return kv_launch(kv_append_kernel<STORE, 8>, grid, kAppendThreads, 0, 1, s, p, tokens);
-        case 128: return kv_launch(kv_append_kernel<STORE, 16>, grid, kAppendThreads, 0, 1, s, p, tokens);
-        case 256: return kv_launch(kv_append_kernel<STORE, 32>, grid, kAppendThreads, 0, 1, s, p, tokens);
+        case 64: return kv_launch(kv_append_kernel<STORE, 8>, grid, kAppendThreads, 0, 1, s, p, tokens, inverse);
+        case 128: return kv_launch(kv_append_kernel<STORE, 16>, grid, kAppendThreads, 0, 1, s, p, tokens, inverse);
+        case 256: return kv_launch(kv_append_kernel<STORE, 32>, grid, kAppendThreads, 0, 1, s, p, tokens, inverse);
     }
     return cudaErrorInvalidValue;
 }
@@ -437,16 +483,17 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const __grid
 }  // namespace
 
 cudaError_t launch_kv_append(const AppendParams& p, int sms, cudaStream_t s) {
-    // Few tokens: one to a CTA, as many SMs as there are. Many: up to 16, so that a CTA has several rows to load
-    // at once.
-    int64_t tokens = p.n_tokens / (4 * int64_t{sms});
-    tokens = tokens < 1 ? 1 : (tokens > kAppendMaxTokens ? kAppendMaxTokens : tokens);
+    // Few tokens: one to a CTA, as many SMs as there are. Many: as many as give each thread two vectors of k and of v.
+    const int64_t per_token = static_cast<int64_t>(p.c.n_kv_heads) * (p.c.head_dim / 8);
+    int64_t tokens = p.n_tokens < 4 * int64_t{sms} ? 1 : 2 * kAppendThreads / per_token;
+    tokens = tokens < 1 ? 1 : (tokens > kAppendMaxTokens ? kAppendMaxTokens : tokens);   // (per_token is at most 512 here)
+    const unsigned inverse = static_cast<unsigned>(((uint64_t{1} << 32) + per_token - 1) / per_token);
     const unsigned grid = static_cast<unsigned>((p.n_tokens + tokens - 1) / tokens);
     const int t = static_cast<int>(tokens);
     switch (p.c.store) {
-        case kKvBf16: return launch_append<kKvBf16>(p, grid, t, s);
-        case kKvFp8Static: return launch_append<kKvFp8Static>(p, grid, t, s);
-        case kKvFp8Dynamic: return launch_append<kKvFp8Dynamic>(p, grid, t, s);
+        case kKvBf16: return launch_append<kKvBf16>(p, grid, t, inverse, s);
+        case kKvFp8Static: return launch_append<kKvFp8Static>(p, grid, t, inverse, s);
+        case kKvFp8Dynamic: return launch_append<kKvFp8Dynamic>(p, grid, t, inverse, s);
     }
     return cudaErrorInvalidValue;
 }
