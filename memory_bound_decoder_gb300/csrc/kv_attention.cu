@@ -6,8 +6,11 @@ namespace mbd {
 
 namespace {
 
-// weight[slot] += sum over the group's query heads of exp2(logit - lse2): a thread per slot.
-__global__ void __launch_bounds__(256) kv_weights_kernel(const __grid_constant__ AttendParams p, int blocks_per_row) {
+constexpr int kWeighThreads = 256, kWeighSlots = 4;   // slots of a thread: their loads are in flight together
+
+// weight[slot] += sum over the group's query heads of exp2(logit - lse2), with the logits that the attention left. Reads 4
+// bytes a query head and slot (from L2, where short caches are concerned) besides the 8 of the weight.
+__global__ void __launch_bounds__(kWeighThreads) kv_weights_kernel(const __grid_constant__ AttendParams p, int blocks_per_row) {
     pdl_trigger();
     pdl_wait();
     const int64_t row = blockIdx.x / blocks_per_row, seq = row / p.c.n_kv_heads;
@@ -16,13 +19,37 @@ __global__ void __launch_bounds__(256) kv_weights_kernel(const __grid_constant__
     const int64_t len = kv_len(p.c, p.seq_lens[seq]);
     const int64_t first = p.window > 0 && p.window < len ? len - p.window : 0;
     const float* lse2 = p.lse2 + seq * p.n_q_heads + head * p.group;
-    for (int64_t j = first + static_cast<int64_t>(block) * 256 + threadIdx.x; j < len; j += int64_t{256} * blocks_per_row) {
-        const int64_t page = kv_page(p.c, seq, j);
-        if (page < 0) continue;
-        const float* x = p.logits + (row * p.c.capacity + j) * p.logit_heads;
-        float w = 0.0f;
-        for (int h = 0; h < p.group; ++h) w += ex2(x[h] - lse2[h]);
-        p.c.weight[kv_meta(p.c, page, head, j)] += w;
+    const int32_t* table = p.c.table + seq * p.c.pages_per_seq;
+    for (int64_t base = first + static_cast<int64_t>(block) * kWeighThreads * kWeighSlots; base < len;
+         base += int64_t{kWeighThreads} * kWeighSlots * blocks_per_row) {
+        // Loads without a branch between them: a thread behind the end repeats the last slot, a page outside the pool
+        // counts as page 0, and neither stores.
+        int page[kWeighSlots];
+        float w[kWeighSlots], old[kWeighSlots];
+        auto slot = [&](int u) { return min(base + u * kWeighThreads + threadIdx.x, len - 1); };
+#pragma unroll
+        for (int u = 0; u < kWeighSlots; ++u) {
+            page[u] = table[slot(u) >> p.c.page_shift];
+            w[u] = 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < kWeighSlots; ++u) {
+            const bool good = static_cast<uint32_t>(page[u]) < static_cast<uint32_t>(p.c.n_pages);
+            old[u] = p.c.weight[kv_meta(p.c, good ? page[u] : 0, head, slot(u))];
+        }
+        for (int h = 0; h < p.group; h += 2) {
+            const float a = lse2[h], b = h + 1 < p.group ? lse2[h + 1] : 0.0f;
+#pragma unroll
+            for (int u = 0; u < kWeighSlots; ++u) {
+                const float2 x = *reinterpret_cast<const float2*>(p.logits + (row * p.c.capacity + slot(u)) * p.logit_heads + h);
+                w[u] += ex2(x.x - a) + (h + 1 < p.group ? ex2(x.y - b) : 0.0f);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kWeighSlots; ++u)
+            if (base + u * kWeighThreads + threadIdx.x < len &&
+                static_cast<uint32_t>(page[u]) < static_cast<uint32_t>(p.c.n_pages))
+                p.c.weight[kv_meta(p.c, page[u], head, slot(u))] = old[u] + w[u];
     }
 }
 
@@ -52,9 +79,10 @@ cudaError_t launch_kv_attend(const AttendParams& p, cudaStream_t s) {
 }
 
 cudaError_t launch_kv_weights(const AttendParams& p, cudaStream_t s) {
-    const int64_t rows = p.n_seqs * p.c.n_kv_heads, blocks = (p.c.capacity + 255) / 256;
+    const int64_t rows = p.n_seqs * p.c.n_kv_heads, most = p.window > 0 && p.window < p.c.capacity ? p.window : p.c.capacity;
+    const int64_t blocks = (most + kWeighThreads * kWeighSlots - 1) / (kWeighThreads * kWeighSlots);
     const int per_row = static_cast<int>(blocks < 64 ? blocks : 64);
-    return kv_launch(kv_weights_kernel, static_cast<unsigned>(rows * per_row), 256, 0, 1, s, p, per_row);
+    return kv_launch(kv_weights_kernel, static_cast<unsigned>(rows * per_row), kWeighThreads, 0, 1, s, p, per_row);
 }
 
 cudaError_t device_error_flags_kv_attention(unsigned int* flags, bool clear) { return kv_error_flags(flags, clear); }
