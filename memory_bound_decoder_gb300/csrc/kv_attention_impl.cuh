@@ -188,6 +188,29 @@ __device__ __forceinline__ bool arrive(unsigned long long* words, unsigned long 
     return true;
 }
 
+// The same for an addition whose result does not depend on who does it, or on whether two do: each part leaves its flag and
+// looks for the others' (by warp 0). One round trip instead of one a level; two parts that deliver at the same time may
+// both find all of them. Whoever adds up clears the flags. Part i's is word `first` for i == 0, rest[i] else.
+__device__ __forceinline__ bool all_there(unsigned long long* first, unsigned long long* rest, unsigned long long call,
+                                          int me, int parts) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) {
+        __threadfence();
+        asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(me == 0 ? first : rest + me), "l"(call) : "memory");
+        asm volatile("fence.sc.gpu;" ::: "memory");
+    }
+    __syncwarp();
+    bool there = true;
+    for (int i = lane; i < parts; i += 32) {
+        unsigned long long seen;
+        asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(seen) : "l"(i == 0 ? first : rest + i) : "memory");
+        there &= seen == call;
+    }
+    there = __all_sync(0xffffffffu, there);
+    if (there) __threadfence();
+    return there;
+}
+
 // Sums of one item (or of a part of it) over the warps of a CTA, per query head of the chunk.
 template <int D, int HT>
 struct MergeSmem {
@@ -309,6 +332,9 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
     if (begin >= end) return;
     if (threadIdx.x < 2) sm.cut[threadIdx.x].last = 0;
 
+    // Words where parts meet, by share: of the item that began before it, and of the one that begins in it. (An item of
+    // several runs has the latter of its inner shares, in which no item begins, for the runs.)
+    unsigned long long *const words_in = p.arrived, *const words_from = p.arrived + p.grid;
     // The share's first tile.
     Cursor cur{};
     int64_t unit = begin;   // the tile's
@@ -838,12 +864,16 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
                 }
             }
             __syncthreads();
-            if (!whole && threadIdx.x == 0) {
+            if (!whole && warp == 0) {
                 const int head = static_cast<int>(((first_unit + 1) * grid - 1) / total);
                 const int tail = static_cast<int>(((last_unit + 1) * grid - 1) / total);
                 const int run = (static_cast<int>(cta) - head) / kJoinParts * kJoinParts + head;
-                const bool last = arrive(p.arrived + run, p.call, static_cast<int>(cta) - run, min(tail - run + 1, kJoinParts));
-                sm.cut[slot] = Cut{out_head, n, head, tail, last};
+                bool last = false;
+                if (tail - head < kJoinParts)
+                    last = all_there(words_from + head, words_in + head, p.call, static_cast<int>(cta) - head, tail - head + 1);
+                else if (lane == 0)
+                    last = arrive(words_in + run, p.call, static_cast<int>(cta) - run, min(tail - run + 1, kJoinParts));
+                if (lane == 0) sm.cut[slot] = Cut{out_head, n, head, tail, last};
             }
         }
         if (!more) break;
@@ -858,11 +888,19 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
         const int runs = (cut.tail - cut.head) / kJoinParts + 1, mine = (static_cast<int>(cta) - cut.head) / kJoinParts;
         const int run = cut.head + mine * kJoinParts;
         join<D, STORE, HT>(p, cut, run, min(cut.tail, run + kJoinParts - 1), 1, runs == 1);
-        if (runs == 1) continue;
-        __syncthreads();
-        if (threadIdx.x == 0) sm.last = arrive(p.arrived + p.grid + cut.head, p.call, mine, runs);
-        __syncthreads();
-        if (sm.last) join<D, STORE, HT>(p, cut, cut.head, cut.tail, kJoinParts, true);
+        if (runs > 1) {
+            __syncthreads();
+            if (warp == 0) {
+                const bool last = all_there(words_from + cut.head, words_from + cut.head, p.call, mine, runs);
+                if (lane == 0) sm.last = last;
+            }
+            __syncthreads();
+            if (!sm.last) continue;
+            join<D, STORE, HT>(p, cut, cut.head, cut.tail, kJoinParts, true);
+        }
+        const int flags = runs == 1 ? cut.tail - cut.head + 1 : runs;
+        for (int i = threadIdx.x; i < flags; i += kThreads)
+            (i == 0 || runs > 1 ? words_from : words_in)[cut.head + i] = 0;
     }
 }
 
