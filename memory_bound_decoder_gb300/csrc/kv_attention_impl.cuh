@@ -91,8 +91,8 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 
 // Keys of a warp's step.
 constexpr int step_keys(int d, int store) {
-    const int row = d * (store == kKvBf16 ? 2 : 1), bytes = store == kKvBf16 ? 256 : 128;
-    return row >= bytes ? 16 : 16 * bytes / row;
+    const int row = d * (store == kKvBf16 ? 2 : 1);
+    return row >= 256 ? 16 : 16 * 256 / row;
 }
 
 // What a (D, STORE) variant loads and holds. A step is 16 NG keys of one warp, 4 KB of K and of V where rows are at
@@ -113,7 +113,7 @@ struct Shape {
 };
 
 // CTAs that share an SM, by the registers that their loads in flight and accumulators take.
-constexpr int resident_ctas(int d, int store, int nt) { return nt == 1 && d < 256 ? (store == kKvBf16 ? 3 : 4) : 2; }
+constexpr int resident_ctas(int d, int store, int nt) { return nt == 1 && d == 64 && store == kKvBf16 ? 3 : 2; }
 
 // One (sequence, key-value head, chunk of query heads), at one of its tiles.
 struct Cursor {
@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
         for (int i = threadIdx.x; p.lse && i < p.n_q_heads; i += kThreads) p.lse[b * p.n_q_heads + i] = -INFINITY;
     }
     if (begin >= end) return;
-    if (threadIdx.x < 2) sm.cut[threadIdx.x].last = 0;
+    if (threadIdx.x < 2) sm.cut[threadIdx.x].n = sm.cut[threadIdx.x].last = 0;
 
     // Words where parts meet, by share: of the item that began before it, and of the one that begins in it. (An item of
     // several runs has the latter of its inner shares, in which no item begins, for the runs.)
@@ -864,23 +864,29 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
                 }
             }
             __syncthreads();
-            if (!whole && warp == 0) {
-                const int head = static_cast<int>(((first_unit + 1) * grid - 1) / total);
-                const int tail = static_cast<int>(((last_unit + 1) * grid - 1) / total);
-                const int run = (static_cast<int>(cta) - head) / kJoinParts * kJoinParts + head;
-                bool last = false;
-                if (tail - head < kJoinParts)
-                    last = all_there(words_from + head, words_in + head, p.call, static_cast<int>(cta) - head, tail - head + 1);
-                else if (lane == 0)
-                    last = arrive(words_in + run, p.call, static_cast<int>(cta) - run, min(tail - run + 1, kJoinParts));
-                if (lane == 0) sm.cut[slot] = Cut{out_head, n, head, tail, last};
-            }
+            if (!whole && threadIdx.x == 0)
+                sm.cut[slot] = Cut{out_head, n, static_cast<int>(((first_unit + 1) * grid - 1) / total),
+                                   static_cast<int>(((last_unit + 1) * grid - 1) / total), 0};
         }
         if (!more) break;
     }
 
-    // The cut items whose parts are complete.
+    // Both parts are delivered at the end, each by a warp: a fence and a round trip in the middle of the share would hold
+    // back a warp for two microseconds, and with it the others where the next item ends.
     __syncthreads();
+    if (warp < 2 && sm.cut[warp].n > 0) {
+        const Cut cut = sm.cut[warp];
+        const int me = static_cast<int>(cta) - cut.head, parts = cut.tail - cut.head + 1;
+        const int run = me / kJoinParts * kJoinParts;
+        bool last = false;
+        if (parts > 2 && parts <= kJoinParts)
+            last = all_there(words_from + cut.head, words_in + cut.head, p.call, me, parts);
+        else if (lane == 0)
+            last = arrive(words_in + cut.head + run, p.call, me - run, min(parts - run, kJoinParts));
+        if (lane == 0) sm.cut[warp].last = last;
+    }
+    __syncthreads();
+    // The cut items whose parts are complete.
 #pragma unroll 1
     for (int slot = 0; slot < 2; ++slot) {
         const Cut cut = sm.cut[slot];
