@@ -551,7 +551,8 @@ mbd_status mbd_paged_attention_decode(void* out, const void* q, int64_t q_stride
  *   new_lens : int32 [n_seqs], written: min(seq_lens[b], budget). Must not overlap seq_lens (heads read it while others
  *              are done already).
  *   budget   : 0 .. MBD_KV_MAX_CAPACITY;   recent : 0 .. budget.
- * The cache must have `weight` and `position`. Limit: pages_per_seq * page_size <= MBD_KV_MAX_EVICT_CAPACITY.
+ * The cache must have `weight` and `position`. Limits: pages_per_seq * page_size <= MBD_KV_MAX_EVICT_CAPACITY, n_pages *
+ * page_size <= 2^31.
  */
 #define MBD_KV_MAX_EVICT_CAPACITY 425984
 mbd_status mbd_kv_cache_evict(const mbd_kv_cache* cache, int32_t* new_lens, const int32_t* seq_lens,

@@ -303,6 +303,7 @@ mbd_status mbd_kv_cache_evict(const mbd_kv_cache* cache, int32_t* new_lens, cons
     if (budget < 0 || recent < 0 || recent > budget) return MBD_ERR_INVALID_ARG;
     const int64_t capacity = pages_per_seq * cache->page_size;
     if (capacity > MBD_KV_MAX_EVICT_CAPACITY || budget > MBD_KV_MAX_CAPACITY ||
+        cache->n_pages > (int64_t{1} << 31) / cache->page_size ||
         n_seqs > MBD_KV_MAX_ROWS / cache->n_kv_heads)
         return MBD_ERR_UNSUPPORTED;
     if (n_seqs == 0) return MBD_OK;

@@ -311,8 +311,8 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const __grid
     if (lane == 0) atomicMax(&sm.max_position, newest);
     if (p.recent > 0) {   // protected slots come before every weight
         cluster.sync();
-        int all = INT32_MIN;
-        for (int r = 0; r < ctas; ++r) all = max(all, *cluster.map_shared_rank(&sm.max_position, r));
+        // (Here and below a lane reads a peer's word: one round trip, where a loop over the peers would wait for each.)
+        const int all = __reduce_max_sync(0xffffffffu, lane < ctas ? *cluster.map_shared_rank(&sm.max_position, lane) : INT32_MIN);
         const int64_t from = static_cast<int64_t>(all) - p.recent;
         for (int i = tid; i < n; i += kEvictThreads)
             if (aux[i] > from) key[i] = 0xffffffffu;
@@ -326,6 +326,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const __grid
     for (int pass = 0; pass < 4; ++pass) {
         const int shift = 24 - 8 * pass;
         unsigned* hist = sm.hist[pass & 1];
+#pragma unroll 4
         for (int i = tid; i < n; i += kEvictThreads)
             if ((key[i] & mask) == value) atomicAdd(&hist[(key[i] >> shift) & 255u], 1u);
         cluster.sync();
@@ -373,11 +374,12 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const __grid
     unsigned equal_before = 0;
     if (need != count) {
         unsigned equal = 0;
+#pragma unroll 4
         for (int i = lo; i < hi; i += 32)
             equal += __popc(__ballot_sync(0xffffffffu, i + lane < hi && (key[i + lane] & mask) == value));
         equal_before = scan_warps(sm, equal, 0, 0).x;
         cluster.sync();
-        for (int r = 0; r < rank; ++r) equal_before += cluster.map_shared_rank(&sm.total[0][0], r)[0];
+        equal_before += __reduce_add_sync(0xffffffffu, lane < rank ? cluster.map_shared_rank(&sm.total[0][0], lane)[0] : 0u);
     }
     // kept(): whether lane's slot i + lane stays; `equal` counts the equal slots before i.
     auto kept = [&](int i, unsigned& equal) {
@@ -392,6 +394,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const __grid
         return keep;
     };
     unsigned holes = 0, movers = 0, equal = equal_before;
+#pragma unroll 4
     for (int i = lo; i < hi; i += 32) {
         const bool in = i + lane < hi, low = first + i + lane < p.budget, keep = kept(i, equal);
         holes += __popc(__ballot_sync(0xffffffffu, in && low && !keep));
@@ -399,19 +402,27 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const __grid
     }
     uint2 at = scan_warps(sm, holes, movers, 1);
     cluster.sync();
-    unsigned moves = 0;
-    for (int r = 0; r < ctas; ++r) {
-        const unsigned* t = cluster.map_shared_rank(&sm.total[1][0], r);
-        if (r < rank) at = make_uint2(at.x + t[0], at.y + t[1]);
-        moves += t[1];
+    uint2 peer = make_uint2(0, 0);
+    if (lane < ctas) {
+        const unsigned* t = cluster.map_shared_rank(&sm.total[1][0], lane);
+        peer = make_uint2(t[0], t[1]);
     }
+    const unsigned moves = __reduce_add_sync(0xffffffffu, peer.y);
+    at.x += __reduce_add_sync(0xffffffffu, lane < rank ? peer.x : 0u);
+    at.y += __reduce_add_sync(0xffffffffu, lane < rank ? peer.y : 0u);
     // The lists, entry i with CTA i / chunk of the cluster: slots given up, then the rows that take their places.
     const unsigned chunk = (moves + ctas - 1) / ctas;
+    // An entry is a slot's place in the pool, page * page_size + place (it fits: the host checks), or -1.
+    auto token_at = [&](int64_t slot) {
+        const int page = table[slot >> p.c.page_shift];
+        return on_pool(page, p.c) ? (page << p.c.page_shift) + static_cast<int>(slot & ((1 << p.c.page_shift) - 1)) : -1;
+    };
     if (moves > 0) {
         // e / chunk by a product: exact while e * chunk < 2^32, and 425984 slots give at most 212992 * 13312.
         const unsigned inverse = chunk > 1 ? 0xffffffffu / chunk + 1 : 0;
         const unsigned below = (1u << lane) - 1u;
         equal = equal_before;
+#pragma unroll 2
         for (int i = lo; i < hi; i += 32) {
             const bool in = i + lane < hi, low = first + i + lane < p.budget, keep = kept(i, equal);
             const unsigned h = __ballot_sync(0xffffffffu, in && low && !keep);
@@ -421,7 +432,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const __grid
                 const unsigned e = hole ? at.x + __popc(h & below) : at.y + __popc(m & below);
                 const unsigned owner = chunk > 1 ? __umulhi(e, inverse) : e;
                 int* list = cluster.map_shared_rank(aux, owner);
-                list[(e - owner * chunk) * 2 + (mover ? 1 : 0)] = static_cast<int>(first) + i + lane;
+                list[(e - owner * chunk) * 2 + (mover ? 1 : 0)] = token_at(first + i + lane);
             }
             at = make_uint2(at.x + __popc(h), at.y + __popc(m));
         }
@@ -436,9 +447,8 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const __grid
     // 1546 rows of 128 bytes a CTA.)
     for (int i = tid; i < mine; i += kEvictThreads) {
         const int2 move = reinterpret_cast<const int2*>(aux)[i];
-        const int page_to = table[move.x >> p.c.page_shift], page_from = table[move.y >> p.c.page_shift];
-        if (!on_pool(page_to, p.c) || !on_pool(page_from, p.c)) continue;
-        const int64_t a = kv_meta(p.c, page_from, head, move.y), b = kv_meta(p.c, page_to, head, move.x);
+        if (move.x < 0 || move.y < 0) continue;
+        const int64_t a = kv_meta(p.c, move.y >> p.c.page_shift, head, move.y), b = kv_meta(p.c, move.x >> p.c.page_shift, head, move.x);
         const float w = p.c.weight[a];
         const int32_t at_position = p.c.position[a];
         float ks = 0.0f, vs = 0.0f;
@@ -454,26 +464,20 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const __grid
         }
     }
     for (int i0 = tid / lanes; i0 < mine; i0 += groups * kMoves) {   // loads without a branch between them, as above
-        int page_to[kMoves], page_from[kMoves];
+        int2 move[kMoves];
         uint4 k[kMoves], v[kMoves];
 #pragma unroll
         for (int u = 0; u < kMoves; ++u) {
-            const int2 move = reinterpret_cast<const int2*>(aux)[min(i0 + u * groups, mine - 1)];
-            page_to[u] = table[move.x >> p.c.page_shift];
-            page_from[u] = table[move.y >> p.c.page_shift];
-        }
-#pragma unroll
-        for (int u = 0; u < kMoves; ++u) {
-            const int from = aux[2 * min(i0 + u * groups, mine - 1) + 1], page = on_pool(page_from[u], p.c) ? page_from[u] : 0;
-            const int64_t a = kv_row(p.c, page, head, from, row_bytes) + part * 16;
+            move[u] = reinterpret_cast<const int2*>(aux)[min(i0 + u * groups, mine - 1)];
+            const int from = max(move[u].y, 0);
+            const int64_t a = kv_row(p.c, from >> p.c.page_shift, head, from, row_bytes) + part * 16;
             k[u] = load_stream(reinterpret_cast<const uint4*>(static_cast<const char*>(p.c.k) + a));
             v[u] = load_stream(reinterpret_cast<const uint4*>(static_cast<const char*>(p.c.v) + a));
         }
 #pragma unroll
         for (int u = 0; u < kMoves; ++u) {
-            if (i0 + u * groups >= mine || !on_pool(page_from[u], p.c) || !on_pool(page_to[u], p.c)) continue;
-            const int to = aux[2 * (i0 + u * groups)];
-            const int64_t b = kv_row(p.c, page_to[u], head, to, row_bytes) + part * 16;
+            if (i0 + u * groups >= mine || move[u].x < 0 || move[u].y < 0) continue;
+            const int64_t b = kv_row(p.c, move[u].x >> p.c.page_shift, head, move[u].x, row_bytes) + part * 16;
             *reinterpret_cast<uint4*>(static_cast<char*>(p.c.k) + b) = k[u];
             *reinterpret_cast<uint4*>(static_cast<char*>(p.c.v) + b) = v[u];
         }

@@ -167,6 +167,7 @@ def test_evict_arguments(lib):
     assert _rc(evict(cache(position=None))) == mbd.ERR_INVALID_ARG
     assert _rc(evict(c, pages_per_seq=425984 // 16 + 1)) == mbd.ERR_UNSUPPORTED
     assert _rc(evict(c, budget=(1 << 30) + 1)) == mbd.ERR_UNSUPPORTED
+    assert _rc(evict(cache(n_pages=(1 << 27) + 1, k=1 << 40, v=1 << 42, weight=1 << 44, position=1 << 45))) == mbd.ERR_UNSUPPORTED
     assert _rc(evict(c, n_seqs=(1 << 23) + 1)) == mbd.ERR_UNSUPPORTED
     mbd.kv_cache_evict(c, None, None, None, 4, 0, 16, 4)
 
