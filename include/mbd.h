@@ -39,7 +39,8 @@
  *     context where they belong to one, and the static schedule buffer's address) and is safe to call from
  *     several host threads.
  *   - Work is enqueued on `stream` (a cudaStream_t; NULL is the legacy default stream) and runs in stream
- *     order. Each successful call of an entry point launches exactly one kernel (a batch: one per op).
+ *     order. Each successful call of an entry point launches exactly one kernel (a batch: one per op; an attention that
+ *     accumulates weights: two).
  *   - Arithmetic is fp32 in registers; every intermediate stays unrounded until the single final rounding
  *     to bf16 or to E4M3 (round to nearest even, saturating finite overflow to +-448).
  *   - Scale convention (both FP8 entry points): `scale` is the DEQUANTISATION multiplier, value ~ code * scale.
@@ -524,13 +525,15 @@ mbd_status mbd_kv_cache_append(const mbd_kv_cache* cache, const void* k, const v
  * A sequence with nothing in view gives zeros and lse = -inf; what lies in masked slots is not read.
  *   out        : [n_seqs, n_q_heads * head_dim] bf16, 16-byte aligned, written.
  *   q          : n_seqs rows of n_q_heads * head_dim bf16, q_stride elements apart (0: dense).
- *   scale      : finite, usually 1 / sqrt(head_dim).   window : 0 (none) or the number of slots in view.
+ *   scale      : finite (also times log2(e)), usually 1 / sqrt(head_dim).   window : 0 (none) or the number of slots in view.
  *   lse        : fp32 [n_seqs, n_q_heads], written, or null.
  *   accumulate : != 0 adds to weight[j] of each slot in view the sum of exp(x_j - lse) over the query heads that read
  *                it (the cache must have `weight`; sequences must not share pages then).
  *   workspace  : device memory of the caller, 256-byte aligned, mbd_paged_attention_workspace_bytes() long for the
- *                same arguments on the same device (0 for arguments that the call refuses). It holds nothing between
- *                calls and need not be set; calls that may run at the same time need one each.
+ *                same arguments on the same device (0 for arguments that the call refuses). Calls hand nothing to one
+ *                another through it, and it need not be set before the first; calls that may run at the same time need
+ *                one each. (CTAs that share a sequence find each other there by a 64-bit number that each call draws anew:
+ *                memory that holds this number by chance would mislead them.)
  * Sums are fp32; the result does not depend on what else runs, and equal calls give equal bits.
  */
 size_t mbd_paged_attention_workspace_bytes(const mbd_kv_cache* cache, int64_t pages_per_seq, int64_t n_seqs,

@@ -241,7 +241,7 @@ mbd_status mbd_paged_attention_decode(void* out, const void* q, int64_t q_stride
     mbd_status st = check_attend(cache, pages_per_seq, n_seqs, n_q_heads);
     if (st != MBD_OK) return st;
     const int64_t width = n_q_heads * cache->head_dim;
-    if (!std::isfinite(scale) || window < 0) return MBD_ERR_INVALID_ARG;
+    if (!std::isfinite(scale * 1.44269504088896341f) || window < 0) return MBD_ERR_INVALID_ARG;
     st = check_stride(&q_stride, width);
     if (st != MBD_OK) return st;
     if (n_seqs == 0) return MBD_OK;

@@ -1,5 +1,6 @@
-"""The paged key-value cache in NumPy, from the definitions and in 64 bits: what the GPU tests compare with. Also the
-caches they run on, with every byte that no call may read (or write) poisoned.
+"""The paged key-value cache in NumPy, from the definitions and in 64 bits -- TEST INFRASTRUCTURE ONLY, as the C oracle: what
+the tests and the smoke check compare with. Also the caches they run on, with every byte that no call may read (or write)
+poisoned. It shares no code with the CUDA library.
 
 Tolerances, derived before the kernels ran:
   * appended rows, scales, positions, evicted caches, lengths: bit for bit (values are copied, or come from IEEE
@@ -202,35 +203,6 @@ class Cache:
                     for x in pools:
                         x[p[to], h, s[to]] = x[p[src], h, s[src]]
         return np.minimum(self.lens, budget).astype(np.int32)
-
-    # -------------------------------------------------------------------------------------------- on the GPU
-
-    def device(self, torch, mbd):
-        from tests.parity import Guarded
-        it = {"bf16": torch.int16, "fp8": torch.uint8}[self.fmt]
-        as_np = lambda a: a.view(np.int16) if a.dtype == np.uint16 else a
-        put = lambda a, dt: None if a is None else Guarded(torch, a.size, dt, fill=as_np(a))
-        self.g = dict(k=put(self.k_raw, it), v=put(self.v_raw, it), ks=put(self.ks, torch.float32),
-                      vs=put(self.vs, torch.float32), weight=put(self.weight, torch.float32),
-                      position=put(self.position, torch.int32), table=put(self.table, torch.int32),
-                      lens=put(self.lens, torch.int32))
-        w = {n: (None if g is None else g.view) for n, g in self.g.items()}
-        self.table_d, self.lens_d = w["table"], w["lens"]
-        self.c = mbd.kv_cache(w["k"], w["v"], self.n_pages, self.page, self.hkv, self.d, self.fmt, self.mode, w["ks"],
-                              w["vs"], w["weight"], w["position"], self.stride if self.gap else 0)
-        return self.c
-
-    def check_equal(self, what="", skip=()):
-        """Every byte of the GPU's copy, guard bands included, is what the host's says."""
-        host = dict(k=self.k_raw, v=self.v_raw, ks=self.ks, vs=self.vs, weight=self.weight, position=self.position,
-                    table=self.table, lens=self.lens)
-        for name, g in self.g.items():
-            if g is None:
-                continue
-            g.check_guards(f"{what} {name}")
-            if name not in skip:
-                bits = {1: np.uint8, 2: np.uint16, 4: np.uint32}[host[name].dtype.itemsize]
-                np.testing.assert_array_equal(g.numpy(bits), host[name].reshape(-1).view(bits), f"{what}: {name}")
 
 
 def check_close(got, want, tol, what):

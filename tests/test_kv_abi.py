@@ -9,7 +9,7 @@ import pytest
 import memory_bound_decoder_gb300 as mbd
 import workloads as wl
 from memory_bound_decoder_gb300 import build as mbd_build
-from tests import kv_reference as ref
+from oracle import kv_cache as ref
 
 A = 1 << 24   # fake device pointers, A apart: never dereferenced
 
@@ -131,6 +131,7 @@ def test_attention_arguments(lib):
     assert _rc(attend(c, n_q_heads=0)) == mbd.ERR_INVALID_ARG
     assert _rc(attend(c, scale=float("nan"))) == mbd.ERR_INVALID_ARG
     assert _rc(attend(c, scale=float("inf"))) == mbd.ERR_INVALID_ARG
+    assert _rc(attend(c, scale=3e38)) == mbd.ERR_INVALID_ARG            # not finite in units of log2
     assert _rc(attend(c, window=-1)) == mbd.ERR_INVALID_ARG
     assert _rc(attend(c, out=None)) == mbd.ERR_INVALID_ARG
     assert _rc(attend(c, q=None)) == mbd.ERR_INVALID_ARG

@@ -1,12 +1,12 @@
 """The key-value cache on the GPU against the 64-bit reference: appended and evicted caches byte for byte, attention
-within the tolerances that tests/kv_reference.py derives. Everything a call must not touch or use is poisoned: slots
+within the tolerances that oracle/kv_cache.py derives. Everything a call must not touch or use is poisoned: slots
 without a token hold NaN, guard bands lie around every tensor, the page table's unused entries name no page."""
 import numpy as np
 import pytest
 
 import workloads as wl
-from tests import kv_reference as ref
-from tests.kv_reference import check_close
+from oracle import kv_cache as ref
+from oracle.kv_cache import check_close
 from tests.parity import Guarded
 
 torch = pytest.importorskip("torch")
@@ -32,6 +32,36 @@ def bits(rng, *shape, sigma=1.0):
 
 def up(a):
     return torch.from_numpy(np.ascontiguousarray(a).view(np.int16 if a.dtype == np.uint16 else a.dtype)).cuda()
+
+
+class Cache(ref.Cache):
+    """With a copy on the GPU between guard bands."""
+
+    def device(self, mbd):
+        it = {"bf16": torch.int16, "fp8": torch.uint8}[self.fmt]
+        as_np = lambda a: a.view(np.int16) if a.dtype == np.uint16 else a
+        put = lambda a, dt: None if a is None else Guarded(torch, a.size, dt, fill=as_np(a))
+        self.g = dict(k=put(self.k_raw, it), v=put(self.v_raw, it), ks=put(self.ks, torch.float32),
+                      vs=put(self.vs, torch.float32), weight=put(self.weight, torch.float32),
+                      position=put(self.position, torch.int32), table=put(self.table, torch.int32),
+                      lens=put(self.lens, torch.int32))
+        w = {n: (None if g is None else g.view) for n, g in self.g.items()}
+        self.table_d, self.lens_d = w["table"], w["lens"]
+        self.c = mbd.kv_cache(w["k"], w["v"], self.n_pages, self.page, self.hkv, self.d, self.fmt, self.mode, w["ks"],
+                              w["vs"], w["weight"], w["position"], self.stride if self.gap else 0)
+        return self.c
+
+    def check_equal(self, what="", skip=()):
+        """Every byte of the GPU's copy, guard bands included, is what the host's says."""
+        host = dict(k=self.k_raw, v=self.v_raw, ks=self.ks, vs=self.vs, weight=self.weight, position=self.position,
+                    table=self.table, lens=self.lens)
+        for name, g in self.g.items():
+            if g is None:
+                continue
+            g.check_guards(f"{what} {name}")
+            if name not in skip:
+                bits = {1: np.uint8, 2: np.uint16, 4: np.uint32}[host[name].dtype.itemsize]
+                np.testing.assert_array_equal(g.numpy(bits), host[name].reshape(-1).view(bits), f"{what}: {name}")
 
 
 STORES = [("bf16", "static"), ("fp8", "static"), ("fp8", "dynamic")]
@@ -84,8 +114,8 @@ HEADS = [(12, 2, 128), (32, 8, 128), (8, 1, 128), (16, 1, 128), (5, 5, 64), (16,
 @pytest.mark.parametrize("hq,hkv,d", HEADS)
 def test_attention_head_layouts(mbd, hq, hkv, d, fmt, mode):
     rng = np.random.default_rng(hash((hq, hkv, d)) % 1000)
-    c = ref.Cache(rng, [37, 0, 1, 200, 129], hkv, d, 16, fmt, mode)
-    c.device(torch, mbd)
+    c = Cache(rng, [37, 0, 1, 200, 129], hkv, d, 16, fmt, mode)
+    c.device(mbd)
     check_attend(mbd, c, rng, hq)
     check_attend(mbd, c, rng, hq, accumulate=True)
 
@@ -96,8 +126,8 @@ def test_attention_lengths_and_pages(mbd, page, fmt, mode):
     """Lengths around the sizes that the work is cut into, in every order, pages that end inside a step."""
     rng = np.random.default_rng(page)
     lens = [0, 1, 2, 7, 8, 9, 15, 16, 17, 31, 32, 33, 63, 64, 65, 0, 127, 128, 129, 255, 256, 257, 511, 513, 1000]
-    c = ref.Cache(rng, rng.permutation(lens), 2, 128, page, fmt, mode)
-    c.device(torch, mbd)
+    c = Cache(rng, rng.permutation(lens), 2, 128, page, fmt, mode)
+    c.device(mbd)
     check_attend(mbd, c, rng, 6, accumulate=True, q_gap=64)
 
 
@@ -105,8 +135,8 @@ def test_attention_lengths_and_pages(mbd, page, fmt, mode):
 @pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 64, 100, 1000, 5000])
 def test_attention_window(mbd, window, fmt, mode):
     rng = np.random.default_rng(window)
-    c = ref.Cache(rng, [0, 1, 5, 16, 99, 100, 101, 640, 1500], 1, 64, 32, fmt, mode)
-    c.device(torch, mbd)
+    c = Cache(rng, [0, 1, 5, 16, 99, 100, 101, 640, 1500], 1, 64, 32, fmt, mode)
+    c.device(mbd)
     check_attend(mbd, c, rng, 4, window=window, accumulate=True)
 
 
@@ -117,17 +147,78 @@ def test_attention_shapes(mbd, n, length, hq, hkv, d, fmt, mode):
     """One long sequence split over the card; more sequences than a block scans at once."""
     rng = np.random.default_rng(n)
     lens = np.full(n, length) if n == 1 else rng.integers(0, length + 1, n)
-    c = ref.Cache(rng, lens, hkv, d, 16, fmt, mode)
-    c.device(torch, mbd)
+    c = Cache(rng, lens, hkv, d, 16, fmt, mode)
+    c.device(mbd)
     check_attend(mbd, c, rng, hq, accumulate=n < 500)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_attention_of_an_empty_batch(mbd, n):
+    """Nothing cached at all: zeros and -inf, weights as they were."""
+    rng = np.random.default_rng(n)
+    c = Cache(rng, [0] * n, 2, 64, 16, "bf16")
+    c.device(mbd)
+    check_attend(mbd, c, rng, 4, accumulate=True)
+
+
+def test_attention_offsets_beyond_32_bits(mbd):
+    """Pages 2 GiB apart in a pool: byte offsets past 2^32, in the attention and in the append."""
+    rng = np.random.default_rng(13)
+    c = Cache(rng, [40], 1, 64, 16, "bf16", spare=1, meta=False)
+    stride = 1 << 30
+    pools = [torch.zeros((c.n_pages - 1) * stride + 16 * 64, dtype=torch.int16, device="cuda") for _ in range(2)]
+    for pool, raw in zip(pools, (c.k_raw, c.v_raw)):
+        for i in range(c.n_pages):
+            pool[i * stride:i * stride + 1024] = up(raw.reshape(c.n_pages, -1)[i])
+    c.device(mbd)
+    c.c = mbd.kv_cache(pools[0], pools[1], c.n_pages, 16, 1, 64, page_stride=stride)
+    assert c.table[0, :3].max() >= 2
+    check_attend(mbd, c, rng, 2)
+    k, v = bits(rng, 1, 64), bits(rng, 1, 64)
+    mbd.kv_cache_append(c.c, up(k), up(v), 0, c.table_d, c.width, c.lens_d, 1, 1)
+    c.store(0, [39], k.reshape(1, 1, 64), v.reshape(1, 1, 64))
+    for pool, raw in zip(pools, (c.k_raw, c.v_raw)):
+        for i in range(c.n_pages):
+            got = pool[i * stride:i * stride + 1024].cpu().numpy().view(np.uint16)
+            np.testing.assert_array_equal(got, raw.reshape(c.n_pages, -1)[i])
+
+
+@pytest.mark.parametrize("fmt,mode", STORES)
+def test_attention_replayed_with_many_parts(mbd, fmt, mode):
+    """A captured call over one long sequence, whose head is cut into parts of parts, replayed over a workspace that
+    other calls use between the replays: the same bits every time."""
+    rng = np.random.default_rng(14)
+    c = Cache(rng, [30011], 1, 128, 64, fmt, mode)
+    other = Cache(rng, [5000, 7], 2, 128, 64, fmt, mode)
+    c.device(mbd)
+    other.device(mbd)
+    q, q2 = up(bits(rng, 1, 8 * 128)), up(bits(rng, 2, 4 * 128))
+    nb = max(mbd.paged_attention_workspace_bytes(c.c, c.width, 1, 8),
+             mbd.paged_attention_workspace_bytes(other.c, other.width, 2, 4))
+    ws = torch.full((nb,), 0xAB, dtype=torch.uint8, device="cuda")
+    out, out2 = torch.empty(1, 1024, dtype=torch.bfloat16, device="cuda"), torch.empty(2, 512, dtype=torch.bfloat16, device="cuda")
+    call = lambda: mbd.paged_attention_decode(out, q, 0, c.c, c.table_d, c.width, c.lens_d, 1, 8, 0.09, 0, None, False, ws, nb)
+    call()
+    torch.cuda.synchronize()
+    want = out.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for i in range(6):
+        if i % 2:
+            mbd.paged_attention_decode(out2, q2, 0, other.c, other.table_d, other.width, other.lens_d, 2, 4, 0.09, 0, None,
+                                       False, ws, nb)
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, want), f"replay {i}"
 
 
 @pytest.mark.parametrize("fmt,mode", STORES)
 def test_attention_strides_and_width(mbd, fmt, mode):
     """Pages apart in the pool, a page table wider than any sequence, and no lse."""
     rng = np.random.default_rng(5)
-    c = ref.Cache(rng, [70, 3, 200], 2, 128, 16, fmt, mode, width=50, gap=48)
-    c.device(torch, mbd)
+    c = Cache(rng, [70, 3, 200], 2, 128, 16, fmt, mode, width=50, gap=48)
+    c.device(mbd)
     check_attend(mbd, c, rng, 8, accumulate=True)
     check_attend(mbd, c, rng, 8, lse=False)
 
@@ -136,8 +227,8 @@ def test_attention_interleaved_pool(mbd):
     """k and v as the halves of one pool's pages."""
     rng = np.random.default_rng(6)
     hkv, d, page, hq = 2, 64, 8, 4
-    c = ref.Cache(rng, [33, 7], hkv, d, page, "bf16", gap=hkv * page * d)
-    c.device(torch, mbd)
+    c = Cache(rng, [33, 7], hkv, d, page, "bf16", gap=hkv * page * d)
+    c.device(mbd)
     pool = np.zeros((c.n_pages, 2, hkv, page, d), np.uint16)
     pool[:, 0], pool[:, 1] = c.view(c.k_raw), c.view(c.v_raw)
     p = up(pool)
@@ -151,14 +242,14 @@ def test_attention_peaked_and_rising_logits(mbd, fmt, mode):
     values that differ by many powers of two (dynamic)."""
     rng = np.random.default_rng(7)
     hkv, d, L = 2, 128, 1200
-    c = ref.Cache(rng, [L, L], hkv, d, 16, fmt, mode)
+    c = Cache(rng, [L, L], hkv, d, 16, fmt, mode)
     for b, slope in ((0, 1.0), (1, -1.0)):
         ramp = np.exp2(slope * np.linspace(-6, 6, L)).astype(np.float32)[:, None, None]
         k = np.abs(rng.standard_normal((L, hkv, d))).astype(np.float32) * ramp
         v = rng.standard_normal((L, hkv, d)).astype(np.float32) * (2.0 ** rng.integers(-20, 20, (L, hkv, 1))
                                                                    if mode == "dynamic" else 1.0)
         c.store(b, np.arange(L), wl.f32_to_bf16_bits(k), wl.f32_to_bf16_bits(v.astype(np.float32)))
-    c.device(torch, mbd)
+    c.device(mbd)
     check_attend(mbd, c, rng, 8, accumulate=True)
     check_attend(mbd, c, rng, 8, scale=-0.01)
 
@@ -167,7 +258,7 @@ def test_attention_extremes_propagate(mbd):
     """A NaN in view reaches its own sequence and head only; +-inf values follow the definition; a key of the type's
     lowest values is given no weight."""
     rng = np.random.default_rng(8)
-    c = ref.Cache(rng, [100, 100, 100], 2, 64, 16, "bf16")
+    c = Cache(rng, [100, 100, 100], 2, 64, 16, "bf16")
     kv, vv = c.view(c.k_raw), c.view(c.v_raw)
     p, _, s = c.at(0, [50])
     vv[p[0], 1, s[0], 3] = 0x7FC0                     # one NaN value: one output element of each of 2 heads
@@ -175,7 +266,7 @@ def test_attention_extremes_propagate(mbd):
     vv[p[0], 0, s[0], 5] = 0x7F80                     # an infinite value
     p, _, s = c.at(2, [20])
     kv[p[0], 0, s[0], :] = 0xFF7F                     # the lowest finite key; queries positive: logit about -3e38
-    c.device(torch, mbd)
+    c.device(mbd)
     q = np.abs(wl.bf16_bits_to_f32(bits(rng, 3, 4 * 64)))
     qb = wl.f32_to_bf16_bits(q)
     out = torch.empty(3 * 4 * 64, dtype=torch.bfloat16, device="cuda")
@@ -204,8 +295,8 @@ def test_attention_bad_indices_are_reported_and_masked(mbd):
     """Page numbers outside the pool and lengths outside the table: the error bit, no access, and the rest as if those
     slots were masked."""
     rng = np.random.default_rng(9)
-    c = ref.Cache(rng, [64, 50, 30], 2, 64, 16, "bf16")
-    c.device(torch, mbd)
+    c = Cache(rng, [64, 50, 30], 2, 64, 16, "bf16")
+    c.device(mbd)
     keep = c.table.copy()
     c.table_d.view(3, -1)[0, 1] = c.n_pages            # slots 16..31 of sequence 0
     c.table_d.view(3, -1)[1, 0] = -7                   # slots 0..15 of sequence 1
@@ -230,10 +321,10 @@ def test_attention_bad_indices_are_reported_and_masked(mbd):
 def test_attention_is_deterministic_and_leaves_no_state(mbd):
     """Equal calls give equal bits, also after the workspace was used by another shape and on another stream."""
     rng = np.random.default_rng(10)
-    a = ref.Cache(rng, [3000, 10, 700], 2, 128, 16, "bf16")
-    b = ref.Cache(rng, [100] * 40, 4, 64, 8, "fp8", "dynamic")
-    a.device(torch, mbd)
-    b.device(torch, mbd)
+    a = Cache(rng, [3000, 10, 700], 2, 128, 16, "bf16")
+    b = Cache(rng, [100] * 40, 4, 64, 8, "fp8", "dynamic")
+    a.device(mbd)
+    b.device(mbd)
     qa, qb = up(bits(rng, 3, 8 * 128)), up(bits(rng, 40, 4 * 64))
     nb = max(mbd.paged_attention_workspace_bytes(a.c, a.width, 3, 8), mbd.paged_attention_workspace_bytes(b.c, b.width, 40, 4))
     ws = torch.empty(nb + 1, dtype=torch.uint8, device="cuda")
@@ -260,8 +351,8 @@ def test_attention_is_deterministic_and_leaves_no_state(mbd):
 @pytest.mark.parametrize("hkv,d,page", [(8, 128, 16), (1, 64, 1), (3, 256, 8), (5, 64, 64)])
 def test_append_one_token_each(mbd, hkv, d, page, fmt, mode):
     rng = np.random.default_rng(d + page)
-    c = ref.Cache(rng, [1, 2, 17, 16, 64, 65, 100], hkv, d, page, fmt, mode, gap=16)
-    c.device(torch, mbd)
+    c = Cache(rng, [1, 2, 17, 16, 64, 65, 100], hkv, d, page, fmt, mode, gap=16)
+    c.device(mbd)
     n, wide = 7, 2 * hkv * d + 24
     rows = bits(rng, n, wide)
     rows[2, :hkv * d] = 0                                 # an all-zero key row; the largest finite values
@@ -288,8 +379,8 @@ def test_append_prompts(mbd, counts, padding, fmt, mode):
     rng = np.random.default_rng(sum(counts))
     n, hkv, d = len(counts), 2, 128
     lens = [x + int(rng.integers(0, 40)) for x in counts]
-    c = ref.Cache(rng, lens, hkv, d, 16, fmt, mode)
-    c.device(torch, mbd)
+    c = Cache(rng, lens, hkv, d, 16, fmt, mode)
+    c.device(mbd)
     cu = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
     total = int(cu[-1]) + padding
     k, v = bits(rng, total, hkv * d), bits(rng, total, hkv * d)
@@ -310,8 +401,8 @@ def test_append_prompts(mbd, counts, padding, fmt, mode):
 
 def test_append_without_weight_and_position(mbd):
     rng = np.random.default_rng(3)
-    c = ref.Cache(rng, [4, 9], 2, 64, 4, "bf16", meta=False)
-    c.device(torch, mbd)
+    c = Cache(rng, [4, 9], 2, 64, 4, "bf16", meta=False)
+    c.device(mbd)
     k, v = bits(rng, 2, 128), bits(rng, 2, 128)
     mbd.kv_cache_append(c.c, up(k), up(v), 0, c.table_d, c.width, c.lens_d, 2, 2)
     torch.cuda.synchronize()
@@ -323,8 +414,8 @@ def test_append_without_weight_and_position(mbd):
 def test_append_bad_indices_are_reported_and_dropped(mbd):
     """A page outside the pool, a length past the table or of 0 with a new token: the error bit, and nothing stored."""
     rng = np.random.default_rng(4)
-    c = ref.Cache(rng, [20, 20, 20, 20], 2, 64, 16, "bf16")
-    c.device(torch, mbd)
+    c = Cache(rng, [20, 20, 20, 20], 2, 64, 16, "bf16")
+    c.device(mbd)
     c.table_d.view(4, -1)[0, 1] = c.n_pages
     c.lens_d[1], c.lens_d[2] = 0, c.width * 16 + 1
     k, v = bits(rng, 4, 128), bits(rng, 4, 128)
@@ -351,7 +442,7 @@ def run_evict(mbd, c, budget, recent):
 @pytest.mark.parametrize("budget,recent", [(0, 0), (1, 0), (1, 1), (17, 5), (64, 64), (100, 0), (333, 32), (1000, 10)])
 def test_evict(mbd, budget, recent, fmt, mode):
     rng = np.random.default_rng(budget)
-    c = ref.Cache(rng, [0, 1, 18, 64, 65, 101, 334, 700], 2, 64, 16, fmt, mode, gap=32)
+    c = Cache(rng, [0, 1, 18, 64, 65, 101, 334, 700], 2, 64, 16, fmt, mode, gap=32)
     for b, length in enumerate(c.lens):                   # positions in any order; weights with ties, NaN, zeros of both
         if length:                                        # signs, infinities
             p, _, s = c.at(b, np.arange(length))
@@ -362,7 +453,7 @@ def test_evict(mbd, budget, recent, fmt, mode):
                 w[rng.random(length) < 0.05] = -0.0
                 w[rng.random(length) < 0.02] = np.inf
                 c.weight[p, h, s] = w
-    c.device(torch, mbd)
+    c.device(mbd)
     mbd.device_error_flags(clear=True)
     got = run_evict(mbd, c, budget, recent)
     np.testing.assert_array_equal(got, c.evict(budget, recent))
@@ -377,19 +468,29 @@ def test_evict_shapes(mbd, n, length, hkv, d, page, budget, ties):
     """Rows over clusters of every size; all weights equal, where the lowest slots stay."""
     rng = np.random.default_rng(length)
     lens = np.full(n, length) if n == 1 else rng.integers(length // 2, length + 1, n)
-    c = ref.Cache(rng, lens, hkv, d, page, "fp8", "dynamic")
+    c = Cache(rng, lens, hkv, d, page, "fp8", "dynamic")
     if ties:
         c.weight[~np.isnan(c.weight)] = 0.25
-    c.device(torch, mbd)
+    c.device(mbd)
     np.testing.assert_array_equal(run_evict(mbd, c, budget, budget // 8), c.evict(budget, budget // 8))
+    c.check_equal("evict")
+
+
+def test_evict_the_longest(mbd):
+    """As many slots as the entry point takes: the largest shares of the largest cluster."""
+    rng = np.random.default_rng(15)
+    length = 425984
+    c = Cache(rng, [length], 1, 64, 4096, "fp8")
+    c.device(mbd)
+    np.testing.assert_array_equal(run_evict(mbd, c, 200001, 777), c.evict(200001, 777))
     c.check_equal("evict")
 
 
 def test_evict_bad_pages_are_reported(mbd):
     """Slots on a page outside the pool go first, and nothing is read or written there."""
     rng = np.random.default_rng(12)
-    c = ref.Cache(rng, [96, 96], 1, 64, 16, "bf16")
-    c.device(torch, mbd)
+    c = Cache(rng, [96, 96], 1, 64, 16, "bf16")
+    c.device(mbd)
     c.table_d.view(2, -1)[0, 2] = 1 << 29
     before = {n: g.view.clone() for n, g in c.g.items() if g is not None}
     mbd.device_error_flags(clear=True)
@@ -413,10 +514,10 @@ def test_decode_with_eviction(mbd, fmt, mode):
     GPU's cache follows the reference step by step, on one stream without a synchronisation inside a step."""
     rng = np.random.default_rng(20)
     n, hkv, hq, d, page, budget, full = 3, 2, 8, 64, 8, 24, 40
-    c = ref.Cache(rng, [full] * n, hkv, d, page, fmt, mode, fill=False)
+    c = Cache(rng, [full] * n, hkv, d, page, fmt, mode, fill=False)
     prompts = np.array([30, 12, 33], np.int32)
     c.lens = prompts.copy()
-    c.device(torch, mbd)
+    c.device(mbd)
     cu = np.concatenate([[0], np.cumsum(prompts)]).astype(np.int32)
     k, v = bits(rng, cu[-1], hkv * d), bits(rng, cu[-1], hkv * d)
     mbd.kv_cache_append(c.c, up(k), up(v), 0, c.table_d, c.width, c.lens_d, n, int(cu[-1]), up(cu))
@@ -474,13 +575,13 @@ def test_captured_steps_share_a_workspace(mbd):
 
     def fresh():
         r = np.random.default_rng(seed)
-        c = ref.Cache(r, [100, 1, 64, 333], hkv, d, page, "fp8", "dynamic", width=25, spare=30)
+        c = Cache(r, [100, 1, 64, 333], hkv, d, page, "fp8", "dynamic", width=25, spare=30)
         for b in range(n):                                # pages for the tokens to come
             used = -(-int(c.lens[b]) // page)
             free = [p for p in range(c.n_pages) if p not in set(c.table[c.table >= 0]) and p < c.n_pages]
             c.table[b, used:used + 1] = free[0]
         c.table[(c.table < 0) | (c.table >= c.n_pages)] = -1
-        c.device(torch, mbd)
+        c.device(mbd)
         return c
 
     def call(c, x, out, ws, nb):
