@@ -162,13 +162,11 @@ def header_functions() -> List[str]:
 
 
 def _ptr(a: Any) -> Optional[int]:
-    if a is None:
-        return None
-    if isinstance(a, int):
+    if a is None or isinstance(a, int):
         return a
     dp = getattr(a, "data_ptr", None)
     if dp is not None:
-        return int(dp())
+        return dp()
     raise TypeError(f"expected a tensor or an integer device pointer, got {type(a).__name__}")
 
 

@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kJoinParts = 16;   // parts of a cut item that are added up at once
+constexpr int kJoinParts = 40;   // parts of a cut item that are added up at once
 constexpr float kLazy = 8.0f;    // units of log2 that a logit may exceed the kept maximum by (p <= 2^8)
 constexpr float kShift = 6.0f;   // E4M3: p is multiplied by 2^kShift (p <= 2^14 in f16)
 constexpr float kLn2 = 0.693147180559945309f;
@@ -240,7 +240,8 @@ __device__ __forceinline__ void write_out(const AttendParams& p, int64_t head, i
 template <int D, int STORE, int HT>
 __device__ __forceinline__ void join(const AttendParams& p, const Cut& cut, int a, int b, int step, bool to_output) {
     constexpr int kLanes = kThreads / HT, kVecs = D / 4 / kLanes;   // threads of a query head, vectors of each
-    constexpr int kBatch = 16 / (kVecs + 1);                        // parts loaded at once
+    // Parts loaded at once, as the registers of the variant allow.
+    constexpr int kBatch = (resident_ctas(D, STORE, HT / 8) == 3 ? 16 : 24) / (kVecs + 1);
     const int h = threadIdx.x / kLanes, dim = threadIdx.x % kLanes * 4, parts = (b - a) / step + 1;
     if (h >= cut.n) return;
     auto part_of = [&](int i) {
@@ -295,6 +296,31 @@ __device__ __forceinline__ void join(const AttendParams& p, const Cut& cut, int 
     if (dim == 0) p.part_ml[part_of(0)] = make_float4(m, t, mo, 0.0f);
 }
 
+// The same for an item of two parts, by half a CTA (`thread` of it): a share can have two of them to join at once.
+template <int D, int STORE, int HT>
+__device__ __forceinline__ void join_two(const AttendParams& p, const Cut& cut, int thread) {
+    constexpr int kLanes = kThreads / 2 / HT, kVecs = D / 4 / kLanes;
+    const int h = thread / kLanes, dim = thread % kLanes * 4;
+    if (h >= cut.n) return;
+    const int64_t a = static_cast<int64_t>(cut.head * 2 + 1) * HT + h, b = static_cast<int64_t>(cut.tail * 2) * HT + h;
+    const float4 ra = __ldcg(p.part_ml + a), rb = __ldcg(p.part_ml + b);
+    float4 xa[kVecs], xb[kVecs];
+#pragma unroll
+    for (int e = 0; e < kVecs; ++e) {
+        xa[e] = __ldcg(reinterpret_cast<const float4*>(p.part_o + a * D + dim + e * kLanes * 4));
+        xb[e] = __ldcg(reinterpret_cast<const float4*>(p.part_o + b * D + dim + e * kLanes * 4));
+    }
+    const float m = fmaxf(ra.x, rb.x), mo = fmaxf(ra.z, rb.z);
+    const float t = (ra.x != -INFINITY ? ra.y * ex2(ra.x - m) : 0.0f) + (rb.x != -INFINITY ? rb.y * ex2(rb.x - m) : 0.0f);
+    const float f = ra.z != -INFINITY ? ex2(ra.z - mo) : 0.0f, g = rb.z != -INFINITY ? ex2(rb.z - mo) : 0.0f;
+#pragma unroll
+    for (int e = 0; e < kVecs; ++e)
+        write_out<D, STORE>(p, cut.out_head + h, dim + e * kLanes * 4,
+                            make_float4(xa[e].x * f + xb[e].x * g, xa[e].y * f + xb[e].y * g, xa[e].z * f + xb[e].z * g,
+                                        xa[e].w * f + xb[e].w * g),
+                            m, t, mo);
+}
+
 template <int D, int STORE, int NT, bool SMALL>   // SMALL: pages of fewer than 16 slots, looked up for each key
 __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
     kv_attend_kernel(const __grid_constant__ AttendParams p) {
@@ -320,7 +346,12 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
     total *= heads;
     // Shares of at least two units: every share between those of an item's first and last tile has a tile of it.
     const int64_t cta = blockIdx.x, grid = min(static_cast<int64_t>(gridDim.x), total / 2);
-    const int64_t begin = cta < grid ? cta * total / grid : 0, end = cta < grid ? (cta + 1) * total / grid : 0;
+    // (32-bit divisions where the numbers allow it: they stand on the way to the first load.)
+    const bool narrow = total * grid + total < (int64_t{1} << 32);
+    auto divide = [&](int64_t a, int64_t b) {
+        return narrow ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+    };
+    const int64_t begin = cta < grid ? divide(cta * total, grid) : 0, end = cta < grid ? divide((cta + 1) * total, grid) : 0;
     // Sequences with nothing in view: zeros, shared out over the CTAs.
     for (int64_t b = cta; b < p.n_seqs; b += gridDim.x) {
         int first, len;
@@ -353,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
             if (hit) {
                 const int src = __ffs(hit) - 1;
                 const int64_t off = begin - (before + __shfl_sync(0xffffffffu, upto - t, src)) * heads;
-                const int units = __shfl_sync(0xffffffffu, t, src), item = static_cast<int>(off / units);
+                const int units = __shfl_sync(0xffffffffu, t, src), item = static_cast<int>(divide(off, units));
                 const int at = static_cast<int>(off - static_cast<int64_t>(item) * units);
                 cur.first = __shfl_sync(0xffffffffu, first, src);
                 cur.len = __shfl_sync(0xffffffffu, len, src);
@@ -589,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
         const char* pool = static_cast<const char*>(lane < 16 ? p.c.k : p.c.v);
         prefetch_l2_bulk(pool + kv_row(p.c, pg, at.head, key, S::kRow), (SMALL ? 1 : 16) * S::kRow);
     };
-    constexpr int kAhead = NT == 2 ? 2 : 0;
+    constexpr int kAhead = NT == 2 ? 1 : 0;
 
     // Starts on the part of an item that begins at cur.key: `tiles` of the `left` tiles that the item has from there.
     int left, tiles;
@@ -887,10 +918,15 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
     }
     __syncthreads();
     // The cut items whose parts are complete.
+    {
+        const int slot = threadIdx.x / (kThreads / 2);
+        if (sm.cut[slot].last && sm.cut[slot].tail - sm.cut[slot].head == 1)
+            join_two<D, STORE, HT>(p, sm.cut[slot], threadIdx.x % (kThreads / 2));
+    }
 #pragma unroll 1
     for (int slot = 0; slot < 2; ++slot) {
         const Cut cut = sm.cut[slot];
-        if (!cut.last) continue;
+        if (!cut.last || cut.tail - cut.head == 1) continue;
         const int runs = (cut.tail - cut.head) / kJoinParts + 1, mine = (static_cast<int>(cta) - cut.head) / kJoinParts;
         const int run = cut.head + mine * kJoinParts;
         join<D, STORE, HT>(p, cut, run, min(cut.tail, run + kJoinParts - 1), 1, runs == 1);
