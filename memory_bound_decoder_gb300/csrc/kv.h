@@ -63,6 +63,7 @@ struct AttendParams {
     int chunk_heads;            // query heads that a CTA takes at once: 8 or 16
     int chunks;                 // of a group
     int grid;                   // CTAs: the shares that the work is cut into
+    int sms;
     float* part_o;              // workspace: [grid, 2, chunk_heads, head_dim], sums of the items that are cut
     float4* part_ml;            // workspace: [grid, 2, chunk_heads], their maxima, sums and exponents
     unsigned long long* arrived;   // workspace: [2, grid], where the deliveries of parts meet

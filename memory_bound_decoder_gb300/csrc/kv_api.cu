@@ -146,7 +146,7 @@ AttendLayout attend_layout(const mbd_kv_cache* c, int64_t pages_per_seq, int64_t
     const int group = static_cast<int>(n_q_heads / c->n_kv_heads);
     const int64_t capacity = pages_per_seq * c->page_size;
     mbd::plan_kv_attend(c->head_dim, store_of(c), group, mbd::kv_sm_count(), capacity, n_seqs * c->n_kv_heads, &w.plan);
-    w.logit_heads = (group + 1) / 2 * 2;   // pairs of heads are stored together
+    w.logit_heads = group <= 2 ? 2 : (group + 3) / 4 * 4;   // read in whole vectors
     const uint64_t parts = uint64_t(w.plan.grid) * 2 * w.plan.chunk_heads;
     w.part_ml = round_up(parts * c->head_dim * 4);
     w.arrived = w.part_ml + round_up(parts * 16);
@@ -280,6 +280,7 @@ mbd_status mbd_paged_attention_decode(void* out, const void* q, int64_t q_stride
     p.chunk_heads = ws.plan.chunk_heads;
     p.chunks = ws.plan.chunks;
     p.grid = ws.plan.grid;
+    p.sms = mbd::kv_sm_count();
     p.logit_heads = ws.logit_heads;
     p.accumulate = accumulate != 0;
     char* base = static_cast<char*>(workspace);

@@ -6,50 +6,75 @@ namespace mbd {
 
 namespace {
 
-constexpr int kWeighThreads = 256, kWeighSlots = 4;   // slots of a thread: their loads are in flight together
+constexpr int kWeighThreads = 256, kWeighSlots = 4;   // slots of a lane group whose loads are in flight together
+
+template <int V>
+struct Logits {
+    float v[V];
+};
+__device__ __forceinline__ void load_logits(Logits<4>& l, const float* p) {
+    const float4 x = __ldcs(reinterpret_cast<const float4*>(p));
+    l = Logits<4>{{x.x, x.y, x.z, x.w}};
+}
+__device__ __forceinline__ void load_logits(Logits<2>& l, const float* p) {
+    const float2 x = __ldcs(reinterpret_cast<const float2*>(p));
+    l = Logits<2>{{x.x, x.y}};
+}
 
 // weight[slot] += sum over the group's query heads of exp2(logit - lse2), with the logits that the attention left. Reads 4
-// bytes a query head and slot (from L2, where short caches are concerned) besides the 8 of the weight.
-__global__ void __launch_bounds__(kWeighThreads) kv_weights_kernel(const __grid_constant__ AttendParams p, int blocks_per_row) {
+// bytes a query head and slot (from L2, where they fit) besides the 8 of the weight. 2^shift lanes own a slot, V query
+// heads each at a time, so that a warp reads whole lines of logits. The sum goes to its weight as a reduction in L2 (the
+// only one for it in the call), which spares the round trip of reading the weight.
+template <int V>
+__global__ void __launch_bounds__(kWeighThreads) kv_weights_kernel(const __grid_constant__ AttendParams p, int blocks_per_row,
+                                                                   int shift) {
     pdl_trigger();
     pdl_wait();
-    const int64_t row = blockIdx.x / blocks_per_row, seq = row / p.c.n_kv_heads;
-    const int block = static_cast<int>(blockIdx.x - row * blocks_per_row);
-    const int head = static_cast<int>(row - seq * p.c.n_kv_heads);
-    const int64_t len = kv_len(p.c, p.seq_lens[seq]);
-    const int64_t first = p.window > 0 && p.window < len ? len - p.window : 0;
-    const float* lse2 = p.lse2 + seq * p.n_q_heads + head * p.group;
-    const int32_t* table = p.c.table + seq * p.c.pages_per_seq;
-    for (int64_t base = first + static_cast<int64_t>(block) * kWeighThreads * kWeighSlots; base < len;
-         base += int64_t{kWeighThreads} * kWeighSlots * blocks_per_row) {
-        // Loads without a branch between them: a thread behind the end repeats the last slot, a page outside the pool
-        // counts as page 0, and neither stores.
-        int page[kWeighSlots];
-        float w[kWeighSlots], old[kWeighSlots];
-        auto slot = [&](int u) { return min(base + u * kWeighThreads + threadIdx.x, len - 1); };
+    const unsigned row = blockIdx.x / blocks_per_row, seq = row / p.c.n_kv_heads;
+    const int block = static_cast<int>(blockIdx.x - row * blocks_per_row), head = static_cast<int>(row - seq * p.c.n_kv_heads);
+    const int lanes = 1 << shift, part = threadIdx.x & (lanes - 1), place_mask = (1 << p.c.page_shift) - 1;
+    const int len = static_cast<int>(kv_len(p.c, p.seq_lens[seq]));
+    const int first = p.window > 0 && p.window < len ? len - static_cast<int>(p.window) : 0;
+    const float* lse2 = p.lse2 + static_cast<int64_t>(seq) * p.n_q_heads + head * p.group;
+    const float* logits = p.logits + static_cast<int64_t>(row) * p.c.capacity * p.logit_heads;
+    const int32_t* table = p.c.table + static_cast<int64_t>(seq) * p.c.pages_per_seq;
+    float* weight = p.c.weight + (static_cast<int64_t>(head) << p.c.page_shift);   // of page 0, this head
+    const int64_t page_weights = static_cast<int64_t>(p.c.n_kv_heads) << p.c.page_shift;
+    const int step = kWeighThreads >> shift;   // slots that the CTA reads at once
+    float l[V];
+    auto load_lse = [&](int h) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) l[i] = h + i < p.group ? lse2[h + i] : 0.0f;
+    };
+    load_lse(part * V);
+    for (int base = first + block * step * kWeighSlots; base < len; base += step * kWeighSlots * blocks_per_row) {
+        // Loads without a branch between them: a thread behind the end repeats the last slot.
+        int page[kWeighSlots], slot[kWeighSlots];
+        float w[kWeighSlots];
 #pragma unroll
         for (int u = 0; u < kWeighSlots; ++u) {
-            page[u] = table[slot(u) >> p.c.page_shift];
+            slot[u] = min(base + u * step + static_cast<int>(threadIdx.x >> shift), len - 1);
+            page[u] = table[slot[u] >> p.c.page_shift];
             w[u] = 0.0f;
         }
+        for (int h = part * V; h < p.group; h += lanes * V) {   // once, up to 128 query heads
+            if (h >= lanes * V) load_lse(h);
+            Logits<V> x[kWeighSlots];
+#pragma unroll
+            for (int u = 0; u < kWeighSlots; ++u) load_logits(x[u], logits + static_cast<int64_t>(slot[u]) * p.logit_heads + h);
+#pragma unroll
+            for (int u = 0; u < kWeighSlots; ++u)
+#pragma unroll
+                for (int i = 0; i < V; ++i) w[u] += h + i < p.group ? ex2(x[u].v[i] - l[i]) : 0.0f;   // (padding holds anything)
+            if (p.group > lanes * V) load_lse(part * V);
+        }
 #pragma unroll
         for (int u = 0; u < kWeighSlots; ++u) {
-            const bool good = static_cast<uint32_t>(page[u]) < static_cast<uint32_t>(p.c.n_pages);
-            old[u] = p.c.weight[kv_meta(p.c, good ? page[u] : 0, head, slot(u))];
-        }
-        for (int h = 0; h < p.group; h += 2) {
-            const float a = lse2[h], b = h + 1 < p.group ? lse2[h + 1] : 0.0f;
-#pragma unroll
-            for (int u = 0; u < kWeighSlots; ++u) {
-                const float2 x = *reinterpret_cast<const float2*>(p.logits + (row * p.c.capacity + slot(u)) * p.logit_heads + h);
-                w[u] += ex2(x.x - a) + (h + 1 < p.group ? ex2(x.y - b) : 0.0f);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kWeighSlots; ++u)
-            if (base + u * kWeighThreads + threadIdx.x < len &&
+            for (int o = lanes >> 1; o > 0; o >>= 1) w[u] += __shfl_xor_sync(0xffffffffu, w[u], o);
+            if (part == 0 && base + u * step + static_cast<int>(threadIdx.x >> shift) < len &&
                 static_cast<uint32_t>(page[u]) < static_cast<uint32_t>(p.c.n_pages))
-                p.c.weight[kv_meta(p.c, page[u], head, slot(u))] = old[u] + w[u];
+                atomicAdd(weight + page[u] * page_weights + (slot[u] & place_mask), w[u]);
+        }
     }
 }
 
@@ -80,9 +105,15 @@ cudaError_t launch_kv_attend(const AttendParams& p, cudaStream_t s) {
 
 cudaError_t launch_kv_weights(const AttendParams& p, cudaStream_t s) {
     const int64_t rows = p.n_seqs * p.c.n_kv_heads, most = p.window > 0 && p.window < p.c.capacity ? p.window : p.c.capacity;
-    const int64_t blocks = (most + kWeighThreads * kWeighSlots - 1) / (kWeighThreads * kWeighSlots);
-    const int per_row = static_cast<int>(blocks < 64 ? blocks : 64);
-    return kv_launch(kv_weights_kernel, static_cast<unsigned>(rows * per_row), kWeighThreads, 0, 1, s, p, per_row);
+    int shift = 0;
+    while (shift < 5 && (4 << shift) < p.group) ++shift;
+    const int64_t slots = int64_t{kWeighThreads >> shift} * kWeighSlots, blocks = (most + slots - 1) / slots;
+    // A few waves of CTAs at most: each first waits for its sequence's length.
+    const int64_t want = (int64_t{16} * p.sms + rows - 1) / rows;
+    const int per_row = static_cast<int>(blocks < want ? blocks : want);
+    const unsigned grid = static_cast<unsigned>(rows * per_row);
+    return p.logit_heads < 4 ? kv_launch(kv_weights_kernel<2>, grid, kWeighThreads, 0, 1, s, p, per_row, 0)
+                             : kv_launch(kv_weights_kernel<4>, grid, kWeighThreads, 0, 1, s, p, per_row, shift);
 }
 
 cudaError_t device_error_flags_kv_attention(unsigned int* flags, bool clear) { return kv_error_flags(flags, clear); }
