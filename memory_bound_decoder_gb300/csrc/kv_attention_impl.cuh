@@ -321,11 +321,15 @@ __device__ __forceinline__ void join_two(const AttendParams& p, const Cut& cut, 
                             m, t, mo);
 }
 
-template <int D, int STORE, int NT, bool SMALL>   // SMALL: pages of fewer than 16 slots, looked up for each key
+// GRAN: keys that share a lookup in the page table: 16 (a group), 8 (half of one), or 1 for pages of fewer than 8 slots
+// (SMALL), whose rows' places lanes look up and hand to one another.
+template <int D, int STORE, int NT, int GRAN>
 __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
     kv_attend_kernel(const __grid_constant__ AttendParams p) {
     using S = Shape<D, STORE>;
     constexpr bool kF8 = S::kF8, kDyn = STORE == kKvFp8Dynamic;
+    constexpr bool SMALL = GRAN == 1;
+    constexpr int H = GRAN == 8 ? 2 : 1;   // lookups of a group
     constexpr int HT = 8 * NT, NG = S::kGroups, KV = S::kKv, VV = S::kVv, VW = S::kVw, KK = S::kK;
     __shared__ MergeSmem<D, HT> sm;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
@@ -419,43 +423,50 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
     uint32_t q[NT][KK][2];
     float ks[NG][2], vs[NG][2];            // dynamic scales of the keys r and r + 8: k's, and log2 of v's
     float ks_next[NG][2], vs_next[NG][2];
-    int64_t row[NG];                       // byte offset of the group's first row (SMALL: of row lane % 16)
+    int64_t row[NG][H];                    // byte offset of the group's (half's) first row (SMALL: of row lane % 16)
     bool full, full_next;                  // every key of the step is in view
     unsigned live[NG], live_next[NG];      // bit i: key i of the group is in view
-    int page[NG];                          // of the step after the next
+    int page[NG][H];                       // of the step after the next
 
     // Page numbers of this warp's step in the tile at `tile`; -1 behind the sequence.
     auto load_pages = [&](int tile) {
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const int key = tile + warp * S::kStep + g * 16 + (SMALL ? lane & 15 : 0);
-            page[g] = key < cur.len ? cur.table[key >> p.c.page_shift] : -1;
-        }
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const int key = tile + warp * S::kStep + g * 16 + h * 8 + (SMALL ? lane & 15 : 0);
+                page[g][h] = key < cur.len ? cur.table[key >> p.c.page_shift] : -1;
+            }
     };
+    auto on_pool = [&](int pg) { return static_cast<uint32_t>(pg) < static_cast<uint32_t>(p.c.n_pages); };
     // Rows and view of the step, whose page numbers were loaded.
     auto place = [&](int tile) {
         const int step = tile + warp * S::kStep;
         full_next = step >= cur.first && step + S::kStep <= cur.len;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const int key = step + g * 16, mine = key + (SMALL ? lane & 15 : 0);
-            const bool good = static_cast<uint32_t>(page[g]) < static_cast<uint32_t>(p.c.n_pages);
-            full_next &= SMALL ? __all_sync(0xffffffffu, good) : good;
-            row[g] = kv_row(p.c, good ? page[g] : 0, cur.head, mine, S::kRow);
-        }
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const bool good = on_pool(page[g][h]);
+                full_next &= SMALL ? __all_sync(0xffffffffu, good) : good;
+                row[g][h] = kv_row(p.c, good ? page[g][h] : 0, cur.head, step + g * 16 + h * 8 + (SMALL ? lane & 15 : 0), S::kRow);
+            }
 #pragma unroll
         for (int g = 0; g < NG; ++g) live_next[g] = 0xffffu;
         if (!full_next) {
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 const int key = step + g * 16, left = cur.len - key, skip = cur.first - key;
-                const bool good = static_cast<uint32_t>(page[g]) < static_cast<uint32_t>(p.c.n_pages);
                 unsigned m = left >= 16 ? 0xffffu : (left <= 0 ? 0u : (1u << left) - 1u);
                 if (skip > 0) m &= skip >= 16 ? 0u : ~((1u << skip) - 1u);
-                if (!good && (SMALL ? (m >> (lane & 15)) & 1u : m)) kv_bad_index();
-                if (SMALL) m &= __ballot_sync(0xffffffffu, good);
-                else if (!good) m = 0u;
-                live_next[g] = m;
+                unsigned missing = 0;   // keys of the group whose page is none of the pool's
+                if (SMALL) missing = ~__ballot_sync(0xffffffffu, on_pool(page[g][0])) & 0xffffu;
+                else
+#pragma unroll
+                    for (int h = 0; h < H; ++h)
+                        if (!on_pool(page[g][h])) missing |= H == 1 ? 0xffffu : 0xffu << (8 * h);
+                if (m & missing) kv_bad_index();
+                live_next[g] = m & ~missing;
             }
         }
         if constexpr (kDyn) {
@@ -465,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
                 for (int i = 0; i < 2; ++i) {
                     ks_next[g][i] = vs_next[g][i] = 0.0f;
                     const int at = r + 8 * i;
-                    const int pg = SMALL ? __shfl_sync(0xffffffffu, page[g], at) : page[g];
+                    const int pg = SMALL ? __shfl_sync(0xffffffffu, page[g][0], at) : page[g][H == 2 ? i : 0];
                     if ((live_next[g] >> at) & 1u) {
                         const int64_t meta = kv_meta(p.c, pg, cur.head, step + g * 16 + at);
                         ks_next[g][i] = p.c.k_scale[meta];
@@ -474,9 +485,11 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
                 }
         }
     };
-    // Offset of row `at` of group g from k_lane or v_lane; `rows` of it are the lane's own, and in there unless SMALL.
+    // Offset of row `at` of group g from k_lane or v_lane, which have the lane's own rows in them unless SMALL; `rows` come on
+    // top of those.
     auto offset = [&](int g, int at, int rows) {
-        return SMALL ? __shfl_sync(0xffffffffu, row[g], at) : row[g] + rows * S::kRow;
+        if (SMALL) return __shfl_sync(0xffffffffu, row[g][0], at);
+        return row[g][H == 2 ? rows / 8 : 0] + (H == 2 ? rows % 8 : rows) * S::kRow;
     };
     auto load_k = [&] {
         if (full_next) {
@@ -610,15 +623,15 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
         }
     };
 
-    // Warms L2 with this warp's rows of the tile at `tile`: a bulk prefetch for each 16 rows (SMALL: each row) of K, by
-    // lanes 0 .., and of V, by lanes 16 .. .
+    // Warms L2 with this warp's rows of the tile at `tile`: a bulk prefetch for each GRAN rows of K, by lanes 0 .., and of V,
+    // by lanes 16 .. .
     auto warm = [&](const Cursor& at, int tile) {
-        const int key = tile + warp * S::kStep + (SMALL ? lane & 15 : (lane & 15) * 16);
-        if (key >= at.len || !(SMALL || (lane & 15) < NG)) return;
+        const int key = tile + warp * S::kStep + (lane & 15) * GRAN;
+        if (key >= at.len || (lane & 15) * GRAN >= S::kStep) return;
         const int pg = at.table[key >> p.c.page_shift];
         if (static_cast<uint32_t>(pg) >= static_cast<uint32_t>(p.c.n_pages)) return;
         const char* pool = static_cast<const char*>(lane < 16 ? p.c.k : p.c.v);
-        prefetch_l2_bulk(pool + kv_row(p.c, pg, at.head, key, S::kRow), (SMALL ? 1 : 16) * S::kRow);
+        prefetch_l2_bulk(pool + kv_row(p.c, pg, at.head, key, S::kRow), GRAN * S::kRow);
     };
     constexpr int kAhead = NT == 2 ? 1 : 0;
 
@@ -948,8 +961,9 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
 
 template <int D, int STORE, int NT>
 cudaError_t launch_nt(const AttendParams& p, cudaStream_t s) {
-    return p.c.page_shift < 4 ? kv_launch(kv_attend_kernel<D, STORE, NT, true>, p.grid, kThreads, 0, 1, s, p)
-                              : kv_launch(kv_attend_kernel<D, STORE, NT, false>, p.grid, kThreads, 0, 1, s, p);
+    if (p.c.page_shift >= 4) return kv_launch(kv_attend_kernel<D, STORE, NT, 16>, p.grid, kThreads, 0, 1, s, p);
+    if (p.c.page_shift == 3) return kv_launch(kv_attend_kernel<D, STORE, NT, 8>, p.grid, kThreads, 0, 1, s, p);
+    return kv_launch(kv_attend_kernel<D, STORE, NT, 1>, p.grid, kThreads, 0, 1, s, p);
 }
 
 template <int D, int STORE>
