@@ -338,9 +338,17 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
     pdl_wait();
 
     // The total of units, then this CTA's share of them, which has the tiles that begin in it: every warp scans the
-    // lengths for itself.
-    int64_t total = 0;
-    for (int64_t b0 = 0; b0 < p.n_seqs; b0 += 32) {
+    // lengths for itself, and keeps the first 32 sequences' (all of this stands on the way to the first load).
+    int first0 = 0, len0 = 0;
+    const int units0 = lane < p.n_seqs ? units_of(view_of<S>(p, lane, &first0, &len0)) : 0;
+    int upto0 = units0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, upto0, o);
+        if (lane >= o) upto0 += x;
+    }
+    int64_t total = __shfl_sync(0xffffffffu, upto0, 31);
+    for (int64_t b0 = 32; b0 < p.n_seqs; b0 += 32) {
         int first, len;
         int64_t t = b0 + lane < p.n_seqs ? units_of(view_of<S>(p, b0 + lane, &first, &len)) : 0;
 #pragma unroll
@@ -357,7 +365,8 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
     };
     const int64_t begin = cta < grid ? divide(cta * total, grid) : 0, end = cta < grid ? divide((cta + 1) * total, grid) : 0;
     // Sequences with nothing in view: zeros, shared out over the CTAs.
-    for (int64_t b = cta; b < p.n_seqs; b += gridDim.x) {
+    const bool some_empty = p.n_seqs > 32 || __any_sync(0xffffffffu, lane < p.n_seqs && units0 == 0);
+    for (int64_t b = some_empty ? cta : p.n_seqs; b < p.n_seqs; b += gridDim.x) {
         int first, len;
         if (view_of<S>(p, b, &first, &len) > 0) continue;
         for (int i = threadIdx.x; i < p.n_q_heads * D / 8; i += kThreads)
@@ -376,13 +385,16 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
     {
         int64_t before = 0;
         for (int64_t b0 = 0; b0 < p.n_seqs; b0 += 32) {
-            int first = 0, len = 0;
-            const int t = b0 + lane < p.n_seqs ? units_of(view_of<S>(p, b0 + lane, &first, &len)) : 0;
-            int64_t upto = t;
+            int first = first0, len = len0, t = units0;
+            int64_t upto = upto0;
+            if (b0 > 0) {
+                t = b0 + lane < p.n_seqs ? units_of(view_of<S>(p, b0 + lane, &first, &len)) : 0;
+                upto = t;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += x;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += x;
+                }
             }
             const unsigned hit = __ballot_sync(0xffffffffu, (before + upto) * heads > begin);
             if (hit) {
