@@ -16,12 +16,26 @@
 // E4M3 codes become f16 by the hardware conversion (exact), so the FP8 path multiplies in f16, with q scaled by a power of
 // two per head so that its elements are normal f16 numbers (bf16's 8 bits fit) and p by 2^6 (flushing below 2^-30).
 // In the bf16 path p goes in as the sum of two bf16 terms (2^-16): rounding it once would cost as much accuracy as
-// rounding the output does, and the tensor cores idle anyway.
+// rounding the output does, and the second product costs nothing measurable (64 sequences of up to 2047 tokens, 32 query
+// and 8 key-value heads: 48.4 us without it, 48.6 with it). The running maximum is kept until a logit exceeds it by 2^8:
+// one vote a step instead of three shuffles a head (one FP8 sequence of 131071 tokens: 61.1 us, 62.3 with it kept exact).
 //
 // Work is cut by keys, not by sequences: all tiles (4 warps' steps) of all sequences and heads in a row, the CTAs of a
 // resident grid take equal shares, wherever they begin and end. A share covers whole (sequence, head) items, written
 // at once, and at most two cut ones, whose sums go to the workspace; whichever CTA delivers the last part of an item adds
-// them up, in the order of the parts, behind its share. A warp keeps a step of K and of V in flight at all times.
+// them up, in the order of the parts, behind its share. (As a second launch the joins took 6 us of such a call, where
+// now 4 go by between the end of the last share and the end of the kernel.) A warp keeps a step of K and of V in flight
+// at all times: the next step's keys are loaded when this one's have been multiplied, its values after this one's, and
+// the next item's first step before an item's end is dealt with.
+//
+// Measured on one GB300 (bytes of the operation over time; 6766 GB/s is the measured copy rate):
+//   bf16, 16 sequences of 9001..32768 tokens, 128 query and 8 key-value heads     206 us, 6650 GB/s
+//   bf16, 64 sequences of 0..2047 tokens, 32 and 8 heads, pages of 16              48.5 us, 5550 GB/s
+//   FP8 static, 32 sequences of 100..8192 tokens, 64 and 8 heads, pages of 32      53 us, 5130 GB/s
+//   FP8 dynamic, one sequence of 131071 tokens, 64 and 8 heads                     60 us, 4600 GB/s
+//   bf16, 24 windows of 1024 tokens, 16 and 16 heads of 64                         23.4 us, 4230 GB/s
+// About ten microseconds of each do not depend on the bytes: launch, lengths, page table and first rows on the way in (each
+// a round trip of half a microsecond), shares that end up to 8% apart, and the joins.
 #pragma once
 
 #include "kv_common.cuh"
@@ -32,7 +46,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kJoinParts = 40;   // parts of a cut item that are added up at once
+constexpr int kJoinParts = 40;   // parts of a cut item that are added up at once (one long sequence: 59.8 us; in two stages of 16: 61.0)
 constexpr float kLazy = 8.0f;    // units of log2 that a logit may exceed the kept maximum by (p <= 2^8)
 constexpr float kShift = 6.0f;   // E4M3: p is multiplied by 2^kShift (p <= 2^14 in f16)
 constexpr float kLn2 = 0.693147180559945309f;
@@ -112,7 +126,10 @@ struct Shape {
     static constexpr int kK = D / 16;                        // k-steps of S^T, m-tiles of O^T
 };
 
-// CTAs that share an SM, by the registers that their loads in flight and accumulators take.
+// CTAs that share an SM, by the registers that their loads in flight and accumulators take. Two keep as much in flight as
+// HBM needs, and more make more cuts to join: bf16 at head_dim 128 takes 48.6 us either way (64 sequences of up to 2047
+// tokens), FP8 61 us with two CTAs of 32-key steps and 70 with four of 16-key ones (one sequence of 131071). At head_dim
+// 64 in bf16 a third pays: 37.4 against 39.1 us (16 sequences of up to 6000 tokens, 16 heads).
 constexpr int resident_ctas(int d, int store, int nt) { return nt == 1 && d == 64 && store == kKvBf16 ? 3 : 2; }
 
 // One (sequence, key-value head, chunk of query heads), at one of its tiles.
@@ -363,7 +380,8 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
     auto divide = [&](int64_t a, int64_t b) {
         return narrow ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
     };
-    const int64_t begin = cta < grid ? divide(cta * total, grid) : 0, end = cta < grid ? divide((cta + 1) * total, grid) : 0;
+    const int64_t begin = cta < grid ? divide(cta * total, grid) : 0;
+    const int64_t end = cta < grid ? divide((cta + 1) * total, grid) : 0;
     // Sequences with nothing in view: zeros, shared out over the CTAs.
     const bool some_empty = p.n_seqs > 32 || __any_sync(0xffffffffu, lane < p.n_seqs && units0 == 0);
     for (int64_t b = some_empty ? cta : p.n_seqs; b < p.n_seqs; b += gridDim.x) {
@@ -645,6 +663,9 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
         const char* pool = static_cast<const char*>(lane < 16 ? p.c.k : p.c.v);
         prefetch_l2_bulk(pool + kv_row(p.c, pg, at.head, key, S::kRow), GRAN * S::kRow);
     };
+    // Only where two 8-column operands leave few registers for loads: 206.9 against 219.7 us without it (16 sequences of up
+    // to 32768 tokens, groups of 16); elsewhere a tile ahead costs more than it gives (64 sequences of up to 2047 tokens,
+    // groups of 4: 50.5 against 48.5 us; FP8, 32 of up to 8192: 57.7 against 53.2).
     constexpr int kAhead = NT == 2 ? 1 : 0;
 
     // Starts on the part of an item that begins at cur.key: `tiles` of the `left` tiles that the item has from there.

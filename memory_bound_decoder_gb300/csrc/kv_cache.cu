@@ -2,9 +2,13 @@
 //
 // Append. Row (token t, head h) of the stacked projection goes to slot lens[seq] - (new tokens of seq) + i of its
 // sequence, as it is (bf16) or as E4M3 codes of value / scale; the dynamic scale is amax / 448 of the head's row.
-// Both divisions are IEEE divisions, so codes and scales are those of the definition, ties included. Bound by
-// bytes (2 D in, D or 2 D out for each of k and v) and, for a decode step's few rows, by latency. head_dim / 8
-// lanes own a row, 16 bytes of k and of v each, so the maximum of a row is a few shuffles and nothing is staged.
+// Both divisions are rounded to nearest, so codes and scales are those of the definition, ties included. Bound by bytes (2 D
+// in, D or 2 D out for each of k and v) and, for a decode step's few rows, by latency: the rows need no slot to be read,
+// so their loads are under way while the slots are looked up. head_dim / 8 lanes own a row, 16 bytes of k and of v
+// each, so the maximum of a row is a few shuffles and nothing is staged. Measured on one GB300: 8190 prompt tokens of 8
+// heads of 128 in bf16 7.4 us (5180 GB/s of the operation's bytes, part of them from L2), 8700 into E4M3 with a static
+// scale 13.8 us (3870 GB/s; the conversion's instructions, two per element, are half of that), 128 single tokens 5.3 us (the
+// host's call).
 //
 // Eviction. Of the `len` slots of one sequence and head the `budget` best stay: first those whose position is
 // among the newest `recent`, then those of the largest weight, equal ones by the lowest slot. A kept row behind
@@ -13,7 +17,10 @@
 // the order of the moves is free. One cluster owns a sequence's head: each CTA keeps its share of the slots as
 // order-preserving 32-bit keys in shared memory (read from HBM once), the budget-th largest key is found by a
 // radix selection of 8 bits a pass whose histograms are added up through distributed shared memory, and the
-// ranks of the moving rows come from ballots and one scan in slot order.
+// ranks of the moving rows come from ballots and one scan in slot order. The moves run near HBM's rate; what surrounds them
+// is latency: eight cluster barriers of about a microsecond and the passes between them. Measured on one GB300: 16
+// sequences of 1500..4099 tokens to 2048, 8 heads of 128 in bf16, 33 us (12 of them moves), one of 131072 to 32768 in FP8 60 us
+// (16 of them moves; a cluster of 16 for each of 8 heads is all that the card's GPCs hold at once).
 #include <cooperative_groups.h>
 
 #include "kv_common.cuh"
