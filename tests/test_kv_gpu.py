@@ -345,6 +345,40 @@ def test_attention_is_deterministic_and_leaves_no_state(mbd):
             assert torch.equal(x, y)
 
 
+def test_attention_on_two_streams_at_once(mbd):
+    """Calls on two streams over one cache, each with a workspace of its own, and torch's current stream taken up where
+    none is given: the bits of the calls made alone."""
+    rng = np.random.default_rng(17)
+    c = Cache(rng, [6000, 3, 900], 2, 128, 16, "bf16")
+    c.device(mbd)
+    qs = [up(bits(rng, 3, 8 * 128)) for _ in range(2)]
+    nb = mbd.paged_attention_workspace_bytes(c.c, c.width, 3, 8)
+    spaces = [torch.empty(nb, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    outs = [torch.empty(3, 1024, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    call = lambda i: mbd.paged_attention_decode(outs[i], qs[i], 0, c.c, c.table_d, c.width, c.lens_d, 3, 8, 0.09, 0, None,
+                                                False, spaces[i], nb)
+    want = []
+    for i in range(2):
+        call(i)
+        torch.cuda.synchronize()
+        want.append(outs[i].clone())
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for i in range(2):
+        assert mbd._stream(streams[i]) == streams[i].cuda_stream
+        with torch.cuda.stream(streams[i]):
+            assert mbd._stream(None) == streams[i].cuda_stream
+    for _ in range(20):
+        for i in range(2):
+            outs[i].zero_()
+        torch.cuda.synchronize()
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                call(i)
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert torch.equal(outs[i], want[i])
+
+
 # ------------------------------------------------------------------------------------------------ append
 
 @pytest.mark.parametrize("fmt,mode", STORES)
@@ -484,6 +518,28 @@ def test_evict_the_longest(mbd):
     c.device(mbd)
     np.testing.assert_array_equal(run_evict(mbd, c, 200001, 777), c.evict(200001, 777))
     c.check_equal("evict")
+
+
+def test_evict_captured(mbd):
+    """A captured eviction over a cluster of the largest size, replayed on a fresh cache each time."""
+    rng = np.random.default_rng(16)
+    c = Cache(rng, [40000], 1, 64, 64, "fp8", "dynamic")
+    c.device(mbd)
+    start = {n: g.raw.clone() for n, g in c.g.items() if g is not None}
+    new = torch.empty(1, dtype=torch.int32, device="cuda")
+    call = lambda: mbd.kv_cache_evict(c.c, new, c.lens_d, c.table_d, c.width, 1, 9000, 100)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    c.evict(9000, 100)
+    for _ in range(2):
+        for n, raw in start.items():
+            c.g[n].raw.copy_(raw)
+        new.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert int(new) == 9000
+        c.check_equal("evict")
 
 
 def test_evict_bad_pages_are_reported(mbd):
