@@ -80,7 +80,7 @@ struct EvictParams {
     int64_t budget;
     int64_t recent;
     int ctas_per_row;           // cluster size: the CTAs that share one sequence's head
-    int slots_per_cta;          // slots of the longest row that one of them holds
+    int slots_per_cta;          // slots of the longest row that one of them holds, even
 };
 
 // How the attention covers a call: chunk_heads, chunks and grid of AttendParams; `rows`: n_seqs * n_kv_heads.

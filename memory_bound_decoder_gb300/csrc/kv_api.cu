@@ -335,7 +335,7 @@ mbd_status mbd_kv_cache_evict(const mbd_kv_cache* cache, int32_t* new_lens, cons
     while (ctas < 16 && (capacity > kMaxSlots * ctas || (2 * rows * ctas <= 2 * sms && capacity >= int64_t{2048} * ctas)))
         ctas *= 2;
     p.ctas_per_row = ctas;
-    p.slots_per_cta = static_cast<int>((capacity + ctas - 1) / ctas);
+    p.slots_per_cta = static_cast<int>((capacity + ctas - 1) / ctas + 1) / 2 * 2;   // even: pairs of words follow
     return static_cast<mbd_status>(
         mbd::kv_finish_launch(mbd::launch_kv_evict(p, reinterpret_cast<cudaStream_t>(stream))));
 }

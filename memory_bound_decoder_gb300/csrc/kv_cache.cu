@@ -261,7 +261,7 @@ __device__ __forceinline__ bool on_pool(int page, const KvView& c) {
 __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const __grid_constant__ EvictParams p) {
     constexpr int kLoads = 8;   // slots of a thread whose weight and position are in flight
     constexpr int kMoves = 4;   // rows of a lane group in flight
-    extern __shared__ uint32_t slots[];   // keys [slots_per_cta], then positions, later the lists of moves
+    extern __shared__ __align__(16) uint32_t slots[];   // keys [slots_per_cta], then positions, later the lists of moves
     __shared__ EvictSmem sm;
     cg::cluster_group cluster = cg::this_cluster();
     const int ctas = p.ctas_per_row, rank = static_cast<int>(blockIdx.x) % ctas;
@@ -418,6 +418,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const __grid
     at.x += __reduce_add_sync(0xffffffffu, lane < rank ? peer.x : 0u);
     at.y += __reduce_add_sync(0xffffffffu, lane < rank ? peer.y : 0u);
     // The lists, entry i with CTA i / chunk of the cluster: slots given up, then the rows that take their places.
+    // (At most half of the slots move, and slots_per_cta is even: a CTA's entries fit it, and begin on eight bytes.)
     const unsigned chunk = (moves + ctas - 1) / ctas;
     // An entry is a slot's place in the pool, page * page_size + place (it fits: the host checks), or -1.
     auto token_at = [&](int64_t slot) {

@@ -510,6 +510,18 @@ def test_evict_shapes(mbd, n, length, hkv, d, page, budget, ties):
     c.check_equal("evict")
 
 
+@pytest.mark.parametrize("page", [1, 2, 4, 8])
+@pytest.mark.parametrize("length", [1, 3, 33, 4501])
+def test_evict_small_pages_and_odd_capacities(mbd, page, length):
+    """Tables of any width over the smallest pages: a row's capacity may be odd."""
+    rng = np.random.default_rng(page + length)
+    c = Cache(rng, [length, length // 2], 3, 64, page, "bf16", width=-(-length // page) | 1)
+    c.device(mbd)
+    budget = length // 3
+    np.testing.assert_array_equal(run_evict(mbd, c, budget, budget // 2), c.evict(budget, budget // 2))
+    c.check_equal("evict")
+
+
 def test_evict_the_longest(mbd):
     """As many slots as the entry point takes: the largest shares of the largest cluster."""
     rng = np.random.default_rng(15)
