@@ -38,6 +38,8 @@
 // a round trip of half a microsecond), shares that end up to 8% apart, and the joins.
 #pragma once
 
+#include <cfloat>
+
 #include "kv_common.cuh"
 
 namespace mbd {
@@ -899,11 +901,22 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
                         *reinterpret_cast<float4*>(&sm.o[warp][head][dim]) =
                             make_float4(o[nt][k][h], o[nt][k][2 + h], o[nt][k + 1][h], o[nt][k + 1][2 + h]);
                     }
-                    float t = sum[nt][h];
+                    // No maximum was kept: nothing in view (the sums are 0), or NaN alone, which fmaxf passes over and
+                    // the sums hold. Such sums stay, under the least exponent: in a join no factor makes them
+                    // finite, and what another warp or part has in the same row's other elements is not scaled away.
+                    float t = sum[nt][h], nan = 0.0f;
+                    if constexpr (kDyn) {   // (a scale of the values that is NaN shows in o only)
 #pragma unroll
-                    for (int x = 4; x < 32; x <<= 1) t += __shfl_xor_sync(0xffffffffu, t, x);
-                    const float m = lim[nt][h] == -INFINITY ? -INFINITY : ref[nt][h];
-                    const float mo = !kDyn ? m : (limo[nt][h] == -INFINITY ? -INFINITY : refo[nt][h]);
+                        for (int k = 0; k < KK; ++k) nan += 0.0f * o[nt][k][h] + 0.0f * o[nt][k][2 + h];
+                    }
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) {
+                        t += __shfl_xor_sync(0xffffffffu, t, x);
+                        if constexpr (kDyn) nan += __shfl_xor_sync(0xffffffffu, nan, x);
+                    }
+                    const float m = lim[nt][h] != -INFINITY ? ref[nt][h] : (t == 0.0f ? -INFINITY : -FLT_MAX);
+                    const float mo = !kDyn ? m
+                                           : (limo[nt][h] != -INFINITY ? refo[nt][h] : (nan == 0.0f ? -INFINITY : -FLT_MAX));
                     if (r == 0) sm.ml[warp][head] = make_float4(m, t, mo, 0.0f);
                 }
             __syncthreads();

@@ -1,0 +1,105 @@
+"""The key-value cache's entry points on the GPU at the edges of what their documentation allows: values that are not
+finite, calls from several host threads, pages outside the pool, the largest sizes. Tolerances are those that
+oracle/kv_cache.py derives, on the inputs without the planted values."""
+import numpy as np
+import pytest
+
+import workloads as wl
+from oracle.kv_cache import check_close
+from tests.test_kv_gpu import STORES, Cache, bits, mbd, up  # noqa: F401  (mbd is the fixture)
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+NAN16, INF16 = 0x7FC0, 0x7F80
+
+
+def attend(mbd, c, q, hq, scale, accumulate=True):
+    """out [n, hq, d], lse [n, hq] and the weights after the call."""
+    n = len(c.lens)
+    nb = mbd.paged_attention_workspace_bytes(c.c, c.width, n, hq, accumulate)
+    ws = torch.full((nb,), 0xFF, dtype=torch.uint8, device="cuda")
+    out = torch.zeros(n, hq * c.d, dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(n, hq, device="cuda")
+    mbd.device_error_flags(clear=True)
+    mbd.paged_attention_decode(out, up(q), 0, c.c, c.table_d, c.width, c.lens_d, n, hq, scale, 0, lse, accumulate, ws, nb)
+    torch.cuda.synchronize()
+    assert mbd.device_error_flags() == 0
+    w = c.g["weight"].numpy(np.float32).reshape(c.weight.shape)
+    return out.float().cpu().numpy().reshape(n, hq, c.d), lse.cpu().numpy(), w
+
+
+# Lengths whose last key is alone in its warp's step, whatever the step (16, 32 or 64 keys); a single key; a sequence
+# that is cut into many parts.
+LONELY = [1, 49, 65, 129, 20033]
+
+
+def check_planted(c, want, got, heads, hq, nan_lse=True):
+    """The query heads in `heads` are NaN in out (and lse); the rest is as the reference without the plant."""
+    out, lse, w = got
+    sick = np.zeros(hq, bool)
+    sick[heads] = True
+    assert np.isnan(out[:, sick]).all()
+    check_close(out[:, ~sick], want[0][:, ~sick], want[2][:, ~sick], "out of the other heads")
+    if nan_lse:
+        assert np.isnan(lse[:, sick]).all()
+    whole = ~sick if nan_lse else np.ones(hq, bool)
+    check_close(lse[:, whole], want[1][:, whole], want[3][:, whole], "lse")
+    group = hq // c.hkv
+    for h in range(c.hkv):
+        live = ~np.isnan(c.weight[:, h])
+        if sick[h * group:(h + 1) * group].any():
+            if nan_lse:
+                assert np.isnan(w[:, h]).all()
+                continue
+        check_close(w[:, h][live], want[4][:, h][live], want[5][:, h][live], "weights")
+
+
+@pytest.mark.parametrize("fmt,mode", STORES)
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (4, 2, 128), (18, 2, 128), (2, 2, 256)])
+@pytest.mark.parametrize("where", ["query", "key", "k_scale", "v_scale"])
+def test_attention_nan_reaches_its_heads(mbd, fmt, mode, hq, hkv, d, where):
+    """A NaN in one head's query, in the last key, or in a scale of the last token gives NaN to the query heads that read
+    it, wherever that key lies, and to no others."""
+    if "scale" in where and mode != "dynamic":
+        pytest.skip("scales of a token")
+    rng = np.random.default_rng(d + hq)
+    c = Cache(rng, LONELY, hkv, d, 16, fmt, mode)
+    q = bits(rng, len(LONELY), hq * d)
+    want = c.attend(q, hq, d ** -0.5, 0, True)
+    group, bad = hq // hkv, hkv - 1
+    heads = list(range(bad * group, hq))
+    for b, length in enumerate(c.lens):
+        p, _, s = c.at(b, [length - 1])
+        if where == "query":
+            heads = [hq - 1]
+            q[b, (hq - 1) * d + 5] = NAN16
+        elif where == "key":
+            c.view(c.k_raw)[p[0], bad, s[0], 7] = NAN16 if fmt == "bf16" else 0x7F
+        else:
+            (c.ks if where == "k_scale" else c.vs)[p[0], bad, s[0]] = np.nan
+    c.device(mbd)
+    check_planted(c, want, attend(mbd, c, q, hq, d ** -0.5), heads, hq, nan_lse=where != "v_scale")
+
+
+def test_attention_nan_value_under_a_scale_of_zero(mbd):
+    """A NaN code whose token has a zero scale: NaN in that element of the output, nothing in the others."""
+    rng = np.random.default_rng(3)
+    hq = hkv = 2
+    c = Cache(rng, LONELY, hkv, 64, 16, "fp8", "dynamic")
+    for b, length in enumerate(c.lens):
+        p, _, s = c.at(b, [length - 1])
+        c.vs[p[0], :, s[0]] = 0
+        c.view(c.v_raw)[p[0], :, s[0]] = 0
+    q = bits(rng, len(LONELY), hq * 64)
+    want = c.attend(q, hq, 0.125, 0, True)
+    for b, length in enumerate(c.lens):
+        p, _, s = c.at(b, [length - 1])
+        c.view(c.v_raw)[p[0], 1, s[0], 9] = 0x7F
+    c.device(mbd)
+    out, lse, _ = attend(mbd, c, q, hq, 0.125)
+    nan = np.zeros(out.shape, bool)
+    nan[:, 1, 9] = True
+    np.testing.assert_array_equal(np.isnan(out), nan)
+    check_close(np.where(nan, 0, out), np.where(nan, 0, want[0]), want[2], "out")
+    check_close(lse, want[1], want[3], "lse")
