@@ -17,7 +17,8 @@
 // two per head so that its elements are normal f16 numbers (bf16's 8 bits fit) and p by 2^6 (flushing below 2^-30).
 // In the bf16 path p goes in as the sum of two bf16 terms (2^-16): rounding it once would cost as much accuracy as
 // rounding the output does, and the second product costs nothing measurable (64 sequences of up to 2047 tokens, 32 query
-// and 8 key-value heads: 48.4 us without it, 48.6 with it). The running maximum is kept until a logit exceeds it by 2^8:
+// and 8 key-value heads: 48.4 us without it, 48.6 with it). Both terms are positive (of p above 2^-110), or an infinite value would
+// meet a second term that is zero or negative and come out as NaN. The running maximum is kept until a logit exceeds it by 2^8:
 // one vote a step instead of three shuffles a head (one FP8 sequence of 131071 tokens: 61.1 us, 62.3 with it kept exact).
 //
 // Work is cut by keys, not by sequences: all tiles (4 warps' steps) of all sequences and heads in a row, the CTAs of a
@@ -839,9 +840,10 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
                     if constexpr (kF8) {
                         hi[nt][i] = transpose8x8(pack_f16x2(w[2 * i], w[2 * i + 1]));
                     } else {
-                        const uint32_t a = pack_bf16x2(w[2 * i], w[2 * i + 1]);
-                        hi[nt][i] = transpose8x8(a);
-                        lo[nt][i] = transpose8x8(pack_bf16x2(w[2 * i] - bf16_lo(a), w[2 * i + 1] - bf16_hi(a)));
+                        // The first term is cut off and the last bit set, so that the second is positive where p is.
+                        const uint32_t a = __float_as_uint(w[2 * i]) | 1u, b = __float_as_uint(w[2 * i + 1]) | 1u;
+                        hi[nt][i] = transpose8x8(__byte_perm(a, b, 0x7632));
+                        lo[nt][i] = transpose8x8(pack_bf16x2(__uint_as_float(a) - bf16_hi(a), __uint_as_float(b) - bf16_hi(b)));
                     }
                 }
             }

@@ -103,3 +103,33 @@ def test_attention_nan_value_under_a_scale_of_zero(mbd):
     np.testing.assert_array_equal(np.isnan(out), nan)
     check_close(np.where(nan, 0, out), np.where(nan, 0, want[0]), want[2], "out")
     check_close(lse, want[1], want[3], "lse")
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (4, 2, 128), (18, 2, 128), (2, 2, 256)])
+def test_attention_infinite_values(mbd, hq, hkv, d, accumulate):
+    """An infinite value comes out as the infinity of its sign, whatever its probability (of a single key: exactly 1, of
+    equal keys: a power of two), and leaves the other elements alone."""
+    rng = np.random.default_rng(d)
+    c = Cache(rng, [1, 2, 64, 100, 4096, 20033], hkv, d, 16, "bf16")
+    for b in (1, 2, 4):                                   # equal keys: probabilities 1/2, 1/64, 1/4096
+        p, _, s = c.at(b, np.arange(c.lens[b]))
+        c.view(c.k_raw)[p, :, s] = wl.f32_to_bf16_bits(np.ones(d, np.float32))
+    at = [(b, int(rng.integers(0, n))) for b, n in enumerate(c.lens)]
+    for b, slot in at:                                    # (the reference sees zeros there)
+        p, _, s = c.at(b, [slot])
+        c.view(c.v_raw)[p[0], :, s[0], 3] = c.view(c.v_raw)[p[0], :, s[0], d - 2] = 0
+    q = bits(rng, len(c.lens), hq * d)
+    want = c.attend(q, hq, d ** -0.5, 0, True)
+    for b, slot in at:
+        p, _, s = c.at(b, [slot])
+        c.view(c.v_raw)[p[0], :, s[0], 3], c.view(c.v_raw)[p[0], :, s[0], d - 2] = INF16, INF16 | 0x8000
+    c.device(mbd)
+    out, lse, w = attend(mbd, c, q, hq, d ** -0.5, accumulate)
+    assert np.isposinf(out[..., 3]).all() and np.isneginf(out[..., d - 2]).all()
+    keep = np.delete(np.arange(d), [3, d - 2])
+    check_close(out[..., keep], want[0][..., keep], want[2][..., keep], "out")
+    check_close(lse, want[1], want[3], "lse")
+    if accumulate:
+        live = ~np.isnan(c.weight)
+        check_close(w[live], want[4][live], want[5][live], "weights")
