@@ -44,7 +44,10 @@ __global__ void __launch_bounds__(kWeighThreads) kv_weights_kernel(const __grid_
     float l[V];
     auto load_lse = [&](int h) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) l[i] = h + i < p.group ? lse2[h + i] : 0.0f;
+        for (int i = 0; i < V; ++i) {
+            l[i] = h + i < p.group ? lse2[h + i] : 0.0f;
+            if (l[i] == -INFINITY) l[i] = INFINITY;   // every logit is -inf: nothing to add (-inf - -inf would be NaN)
+        }
     };
     load_lse(part * V);
     for (int base = first + block * step * kWeighSlots; base < len; base += step * kWeighSlots * blocks_per_row) {

@@ -133,3 +133,41 @@ def test_attention_infinite_values(mbd, hq, hkv, d, accumulate):
     if accumulate:
         live = ~np.isnan(c.weight)
         check_close(w[live], want[4][live], want[5][live], "weights")
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (18, 2, 128), (2, 2, 256), (260, 2, 64)])
+def test_attention_with_logits_of_minus_infinity(mbd, hq, hkv, d):
+    """Keys of -inf under positive queries have no weight; where all of a head's keys are such, it gives zeros and -inf
+    and adds nothing to the weights."""
+    rng = np.random.default_rng(d)
+    c = Cache(rng, [1, 50, 20033, 300], hkv, d, 16, "bf16")
+    q = wl.f32_to_bf16_bits(np.abs(wl.bf16_bits_to_f32(bits(rng, 4, hq * d))) + np.float32(2 ** -10))
+    want = [x.copy() for x in c.attend(q, hq, d ** -0.5, 0, True)]
+    group = hq // hkv
+    for b in range(3):                                    # key-value head 0 of the first three
+        p, _, s = c.at(b, np.arange(c.lens[b]))
+        c.view(c.k_raw)[p, 0, s, 11] = INF16 | 0x8000
+        want[0][b, :group], want[1][b, :group] = 0, -np.inf
+        want[4][p, 0, s] = c.weight[p, 0, s]
+    half = Cache.at(c, 3, np.arange(0, 300, 2))           # every other key of the last: the reference on the others
+    c.view(c.k_raw)[half[0], 0, half[2], 11] = INF16 | 0x8000
+    k, v = (x[0] for x in c.rows(3, np.arange(1, 300, 2)))
+    qd = wl.bf16_bits_to_f32(q[3]).astype(np.float64).reshape(hq, d)[:group]
+    x = qd @ k.T * d ** -0.5
+    m = x.max(-1, keepdims=True)
+    pr = np.exp(x - m) / np.exp(x - m).sum(-1, keepdims=True)
+    want[0][3, :group], want[1][3, :group] = pr @ v, (m + np.log(np.exp(x - m).sum(-1, keepdims=True)))[:, 0]
+    dx = (d * 2.0 ** -23 + 2.0 ** -22) * (np.abs(qd) @ np.abs(k).T * d ** -0.5).max()
+    dp = 2 * dx + (150 / 32 + 8) * 2.0 ** -23             # as oracle/kv_cache.py derives them, over all of the group
+    want[2][3, :group] = pr @ np.abs(v) * (dp + 2.0 ** -16 + (150 / 32 + 64) * 2.0 ** -23) + 2.0 ** -8 * np.abs(pr @ v)
+    want[3][3, :group] = dp + 2.0 ** -22 * np.abs(want[1][3, :group])
+    p, _, s = c.at(3, np.arange(1, 300, 2))
+    want[4][p, 0, s] = c.weight[p, 0, s] + pr.sum(0)
+    want[5][p, 0, s] = pr.sum(0) * dp + 2.0 ** -23 * want[4][p, 0, s]
+    want[4][half[0], 0, half[2]] = c.weight[half[0], 0, half[2]]
+    c.device(mbd)
+    out, lse, w = attend(mbd, c, q, hq, d ** -0.5)
+    check_close(out, want[0], want[2], "out")
+    check_close(lse, want[1], want[3], "lse")
+    live = ~np.isnan(c.weight)
+    check_close(w[live], want[4][live], want[5][live], "weights")
