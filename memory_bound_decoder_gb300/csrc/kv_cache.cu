@@ -24,6 +24,7 @@
 #include <cooperative_groups.h>
 
 #include "kv_common.cuh"
+#include "mbd.h"
 
 namespace mbd {
 
@@ -215,6 +216,10 @@ cudaError_t launch_append(const AppendParams& p, unsigned grid, int tokens, unsi
 
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
+
+// Dynamic shared memory for a share of `slots` slots: a key and a position each, and the lists' last entry.
+constexpr size_t evict_shared(int slots) { return (static_cast<size_t>(slots) * 2 + 4) * sizeof(uint32_t); }
+constexpr int kEvictMaxShared = static_cast<int>(evict_shared(MBD_KV_MAX_EVICT_CAPACITY / 16));
 
 struct EvictSmem {
     unsigned hist[2][256];   // alternate: peers may still read one while the next is cleared
@@ -511,10 +516,12 @@ cudaError_t launch_kv_append(const AppendParams& p, int sms, cudaStream_t s) {
 }
 
 cudaError_t launch_kv_evict(const EvictParams& p, cudaStream_t s) {
-    const size_t smem = (static_cast<size_t>(p.slots_per_cta) * 2 + 4) * sizeof(uint32_t);
+    const size_t smem = evict_shared(p.slots_per_cta);
     cudaError_t e = cudaSuccess;
+    // The limit is the kernel's, not the launch's: always the largest share's, or a smaller call of another thread could
+    // lower it between this call's two steps. (What a launch takes is its own size.)
     if (smem > 40 * 1024)
-        e = cudaFuncSetAttribute(kv_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        e = cudaFuncSetAttribute(kv_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictMaxShared);
     if (e == cudaSuccess && p.ctas_per_row > 8)
         e = cudaFuncSetAttribute(kv_evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;

@@ -1,0 +1,57 @@
+"""Entry points called from several host threads at once, where a launch depends on an attribute of the kernel: every
+call succeeds, and its results are those of the call made alone."""
+import threading
+
+import numpy as np
+import pytest
+
+import workloads as wl
+from tests.test_kv_gpu import Cache, mbd, up  # noqa: F401  (mbd is the fixture)
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def in_threads(*jobs):
+    """Run the jobs at the same time, each on a host thread of its own; the first exception of any is raised here."""
+    gate, failed = threading.Barrier(len(jobs)), []
+
+    def body(job):
+        try:
+            gate.wait()
+            job()
+        except Exception as e:                            # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=body, args=(job,)) for job in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    if failed:
+        raise failed[0]
+
+
+def test_evict_from_two_host_threads(mbd):
+    """Evictions of two caches of very different width from two threads, on a stream each: every launch is accepted."""
+    rng = np.random.default_rng(40)
+    calls, caches = [], []
+    for page, width in ((1024, 100), (1, 425984)):        # 50 KB and 208 KB of shared memory a CTA
+        c = Cache(rng, [90] * 2, 1, 64, page, "bf16", width=width)
+        c.device(mbd)
+        new = torch.zeros(2, dtype=torch.int32, device="cuda")
+        stream = torch.cuda.Stream()
+        caches.append((c, new))
+
+        def run(c=c, new=new, stream=stream):
+            for i in range(4000):
+                mbd.kv_cache_evict(c.c, new, c.lens_d, c.table_d, c.width, 2, 40, 8, stream)
+                if i % 500 == 499:
+                    stream.synchronize()
+        calls.append(run)
+    torch.cuda.synchronize()
+    in_threads(*calls)
+    torch.cuda.synchronize()
+    assert mbd.device_error_flags() == 0
+    for c, new in caches:                                 # each further call on the same lengths does the first's again
+        assert new.tolist() == [40, 40]
