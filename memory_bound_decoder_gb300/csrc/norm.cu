@@ -176,8 +176,10 @@ NormKernel norm_kernel(const NormParams& p, const RowPlan& plan) {
 cudaError_t prepare_partials_kernel(NormKernel kern, int variant, size_t smem) {
     const cudaError_t ce = prefer_shared_carveout(reinterpret_cast<const void*>(kern), variant);
     if (ce != cudaSuccess) return ce;
-    if (smem > 48 * 1024)
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // The limit is the kernel's, not the launch's: always the largest call's, or a smaller call of another thread
+    // could lower it between this call's two steps. (What a launch takes is its own size.)
+    constexpr int kMost = kMaxPartials * 512 * 16;   // 512 threads, one vector of 16 bytes each
+    if (smem > 48 * 1024) return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     return cudaSuccess;
 }
 

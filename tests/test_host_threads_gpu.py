@@ -55,3 +55,38 @@ def test_evict_from_two_host_threads(mbd):
     assert mbd.device_error_flags() == 0
     for c, new in caches:                                 # each further call on the same lengths does the first's again
         assert new.tolist() == [40, 40]
+
+
+def test_partial_norms_from_two_host_threads(mbd):
+    """Norms over eight partials in rows of different width, which take 52 and 64 KB of shared memory a CTA."""
+    calls, checks = [], []
+    for hidden in (26000, 32768):
+        parts = [up(wl.normal_bf16((2, hidden), 7, "x", salt=j)) for j in range(8)]
+        start, weight = up(wl.normal_bf16((2, hidden), 8, "residual")), up(wl.weight_bf16(hidden, 9))
+        residual, stream = torch.empty_like(start), torch.cuda.Stream()
+        out = torch.empty(2, hidden, dtype=torch.bfloat16, device="cuda")
+
+        def norm(out=out, residual=residual, parts=parts, weight=weight, hidden=hidden, stream=stream):
+            mbd.fused_allreduce_add_rmsnorm(out, residual, parts, weight, 2, hidden, 1e-6, stream)
+
+        def once(norm=norm, residual=residual, start=start, stream=stream):
+            with torch.cuda.stream(stream):
+                residual.copy_(start)
+            norm()
+
+        torch.cuda.synchronize()
+        once()
+        torch.cuda.synchronize()
+        checks.append((out, out.clone(), residual, residual.clone()))
+
+        def run(norm=norm, once=once, stream=stream):
+            for i in range(60000):
+                norm()
+                if i % 500 == 499:
+                    stream.synchronize()
+            once()
+        calls.append(run)
+    in_threads(*calls)
+    torch.cuda.synchronize()
+    for out, want, residual, sums in checks:
+        assert torch.equal(out, want) and torch.equal(residual, sums)
