@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
     for (int64_t b = some_empty ? cta : p.n_seqs; b < p.n_seqs; b += gridDim.x) {
         int first, len;
         if (view_of<S>(p, b, &first, &len) > 0) continue;
-        for (int i = threadIdx.x; i < p.n_q_heads * D / 8; i += kThreads)
+        for (int i = threadIdx.x; i < p.n_q_heads * (D / 8); i += kThreads)   // (at most 2^29)
             reinterpret_cast<uint4*>(p.out)[b * p.n_q_heads * (D / 8) + i] = make_uint4(0, 0, 0, 0);
         for (int i = threadIdx.x; p.lse && i < p.n_q_heads; i += kThreads) p.lse[b * p.n_q_heads + i] = -INFINITY;
     }

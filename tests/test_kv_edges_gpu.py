@@ -171,3 +171,17 @@ def test_attention_with_logits_of_minus_infinity(mbd, hq, hkv, d):
     check_close(lse, want[1], want[3], "lse")
     live = ~np.isnan(c.weight)
     check_close(w[live], want[4][live], want[5][live], "weights")
+
+
+@pytest.mark.parametrize("hq,d", [(1 << 23, 256), (1 << 24, 128), ((1 << 23) + 8, 256)])
+def test_attention_of_an_empty_sequence_with_the_most_heads(mbd, hq, d):
+    """Rows of 2^31 elements and more, all of which have to become zero."""
+    rng = np.random.default_rng(1)
+    c = Cache(rng, [0], 1, d, 16, "bf16")
+    c.device(mbd)
+    out = torch.full((hq * d,), 0x3F80, dtype=torch.int16, device="cuda")
+    q, lse = torch.empty(hq * d, dtype=torch.int16, device="cuda"), torch.zeros(hq, device="cuda")
+    nb = mbd.paged_attention_workspace_bytes(c.c, c.width, 1, hq)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    mbd.paged_attention_decode(out, q, 0, c.c, c.table_d, c.width, c.lens_d, 1, hq, 0.1, 0, lse, False, ws, nb)
+    assert not bool(out.view(torch.int64).any()) and bool(torch.isneginf(lse).all())
