@@ -551,7 +551,8 @@ mbd_status mbd_paged_attention_decode(void* out, const void* q, int64_t q_stride
  * least weight). A slot that stays and lies before `budget` is not moved; the others that stay go, in ascending order,
  * to the slots given up, in ascending order, with their scales, weight and position. Attention does not depend on
  * the order of the slots; `position` keeps that of the tokens. Slots from `budget` on keep their old contents, and their
- * pages may be freed.
+ * pages may be freed. Slots on a page outside the pool (MBD_DEVERR_BAD_INDEX) hold nothing and have no room: those before
+ * `budget` count as staying, so that many rows fewer are kept, still the best ones, and none is lost on the way.
  *   new_lens : int32 [n_seqs], written: min(seq_lens[b], budget). Must not overlap seq_lens (heads read it while others
  *              are done already).
  *   budget   : 0 .. MBD_KV_MAX_CAPACITY;   recent : 0 .. budget.

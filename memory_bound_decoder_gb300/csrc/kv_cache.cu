@@ -309,7 +309,9 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const __grid
             const bool good = on_pool(page[u], p.c);
             bad |= !good;
             if (i < n) {
-                key[i] = good ? order_key(w[u]) : 0u;
+                // A bad page's slot has no row to keep and no room for one: before the budget it stays, and takes up its place;
+                // behind it it comes last, and `budget` slots are found without it.
+                key[i] = good ? order_key(w[u]) : (first + i < p.budget ? 0xffffffffu : 0u);
                 aux[i] = good ? at[u] : INT32_MIN;
             }
             newest = max(newest, good ? at[u] : INT32_MIN);

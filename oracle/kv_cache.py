@@ -188,11 +188,16 @@ class Cache:
             if length <= budget:
                 continue
             p, _, s = self.at(b, np.arange(length))
+            bad = (p < 0) | (p >= self.n_pages)               # no page of the pool: no row, and no room for one
+            p = np.where(bad, 0, p)
+            stuck = bad & (np.arange(length) < budget)
             for h in range(self.hkv):
                 w, pos = self.weight[p, h, s], self.position[p, h, s].astype(np.int64)
+                w[bad], pos[bad] = np.nan, -(1 << 40)
                 safe = pos > pos.max() - recent if recent > 0 else np.zeros(length, bool)
+                safe |= stuck
+                worst = np.isnan(w)
                 w = np.where(np.isnan(w), -np.inf, w) + 0.0
-                worst = np.isnan(self.weight[p, h, s])
                 order = np.lexsort((np.arange(length), -w, worst & ~safe, ~safe)) if not safe.any() else \
                     np.lexsort((np.arange(length), np.where(safe, 0, -w), worst & ~safe, ~safe))
                 kept = np.zeros(length, bool)

@@ -185,3 +185,28 @@ def test_attention_of_an_empty_sequence_with_the_most_heads(mbd, hq, d):
     ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
     mbd.paged_attention_decode(out, q, 0, c.c, c.table_d, c.width, c.lens_d, 1, hq, 0.1, 0, lse, False, ws, nb)
     assert not bool(out.view(torch.int64).any()) and bool(torch.isneginf(lse).all())
+
+
+@pytest.mark.parametrize("fmt,mode", STORES)
+@pytest.mark.parametrize("budget,recent,bad", [(40, 8, {2}), (40, 8, {0, 1, 2}), (40, 40, {1}), (70, 5, {1, 3, 5}),
+                                               (40, 0, {3, 4, 5}), (20, 3, {0, 1, 2, 3, 4, 5}), (90, 0, {0, 2, 4, 5})])
+def test_evict_around_bad_pages(mbd, fmt, mode, budget, recent, bad):
+    """Slots on pages outside the pool take up their places before the budget; every row that is kept arrives, the best
+    ones, and the other sequence is evicted as ever."""
+    rng = np.random.default_rng(budget + len(bad))
+    c = Cache(rng, [96, 96], 2, 64, 16, fmt, mode)
+    for b in range(2):
+        p, _, s = c.at(b, np.arange(96))
+        for h in range(2):
+            c.position[p, h, s] = rng.permutation(96)
+            c.weight[p, h, s] = rng.integers(0, 8, 96).astype(np.float32) / 4
+            c.weight[p[rng.integers(0, 96)], h, s[3]] = np.nan
+    for i in bad:
+        c.table[0, i] = (-1, c.n_pages, 1 << 29)[i % 3]
+    c.device(mbd)
+    new = torch.zeros(2, dtype=torch.int32, device="cuda")
+    mbd.device_error_flags(clear=True)
+    mbd.kv_cache_evict(c.c, new, c.lens_d, c.table_d, c.width, 2, budget, recent)
+    assert mbd.device_error_flags(clear=True) == mbd.DEVERR_BAD_INDEX
+    np.testing.assert_array_equal(new.cpu().numpy(), c.evict(budget, recent))
+    c.check_equal("evict")
