@@ -509,7 +509,9 @@ typedef struct {
  *               == n_seqs and row b belongs to sequence b.
  *   seq_lens  : lengths WITH the new tokens: the last of them goes to slot seq_lens[b] - 1. So the call changes no
  *               length, and making it twice stores the same twice.
- *   positions : int32 [n_tokens] or null (a token's position is its slot); stored if the cache has `position`.
+ *   positions : int32 [n_tokens] or null (a token's position is its slot); stored if the cache has `position`. Once a
+ *               sequence was evicted from, its slots fall behind its positions, and they have to be given: by its slot the
+ *               newest token would count as older than those kept.
  * FP8: code = e4m3(value / scale), both divisions rounded to nearest; dynamic: scale = amax / 448 of the head's
  * head_dim values, zero codes where that is 0. If the cache has `weight`, the new slots' is set to 0.
  */

@@ -297,7 +297,8 @@ def kv_cache(k, v, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int,
 
 def kv_cache_append(cache: KVCache, k, v, row_stride: int, page_table, pages_per_seq: int, seq_lens, n_seqs: int,
                     n_tokens: int, cu_tokens=None, positions=None, stream=None) -> None:
-    """Store the new tokens' keys and values; seq_lens are the lengths with them (mbd_kv_cache_append)."""
+    """Store the new tokens' keys and values; seq_lens are the lengths with them, positions theirs in the sequences,
+    which a cache that was evicted from needs (mbd_kv_cache_append)."""
     _check(get_lib().mbd_kv_cache_append(cache, _ptr(k), _ptr(v), int(row_stride), _ptr(page_table), int(pages_per_seq),
                                          _ptr(seq_lens), int(n_seqs), int(n_tokens), _ptr(cu_tokens), _ptr(positions),
                                          _stream(stream)), "kv_cache_append")
