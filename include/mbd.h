@@ -529,6 +529,8 @@ mbd_status mbd_kv_cache_append(const mbd_kv_cache* cache, const void* k, const v
  *   out        : [n_seqs, n_q_heads * head_dim] bf16, 16-byte aligned, written.
  *   q          : n_seqs rows of n_q_heads * head_dim bf16, q_stride elements apart (0: dense).
  *   scale      : finite (also times log2(e)), usually 1 / sqrt(head_dim).   window : 0 (none) or the number of slots in view.
+ *                Slots, not positions: after an eviction the last slots are no longer the newest tokens, so a sequence
+ *                that was evicted from takes window 0 (the budget bounds its view).
  *   lse        : fp32 [n_seqs, n_q_heads], written, or null.
  *   accumulate : != 0 adds to weight[j] of each slot in view the sum of exp(x_j - lse) over the query heads that read
  *                it (the cache must have `weight`; sequences must not share pages then).
@@ -551,8 +553,8 @@ mbd_status mbd_paged_attention_decode(void* out, const void* q, int64_t q_stride
  * and become slots 0 .. budget - 1. Best are first the slots whose position is greater than (the largest position of
  * the head's slots) - recent, then those of the greatest weight; among equals the lowest slot (NaN counts as the
  * least weight). A slot that stays and lies before `budget` is not moved; the others that stay go, in ascending order,
- * to the slots given up, in ascending order, with their scales, weight and position. Attention does not depend on
- * the order of the slots; `position` keeps that of the tokens. Slots from `budget` on keep their old contents, and their
+ * to the slots given up, in ascending order, with their scales, weight and position. Attention without a window does not
+ * depend on the order of the slots; `position` keeps that of the tokens. Slots from `budget` on keep their old contents, and their
  * pages may be freed. Slots on a page outside the pool (MBD_DEVERR_BAD_INDEX) hold nothing and have no room: those before
  * `budget` count as staying, so that many rows fewer are kept, still the best ones, and none is lost on the way.
  *   new_lens : int32 [n_seqs], written: min(seq_lens[b], budget). Must not overlap seq_lens (heads read it while others

@@ -210,3 +210,31 @@ def test_evict_around_bad_pages(mbd, fmt, mode, budget, recent, bad):
     assert mbd.device_error_flags(clear=True) == mbd.DEVERR_BAD_INDEX
     np.testing.assert_array_equal(new.cpu().numpy(), c.evict(budget, recent))
     c.check_equal("evict")
+
+
+def test_window_counts_slots_also_after_an_eviction(mbd):
+    """The window is the last slots as they lie, whatever positions an eviction left there; without one, the order of
+    the slots decides nothing."""
+    rng = np.random.default_rng(21)
+    hq, hkv, d, n = 4, 2, 64, 3
+    c = Cache(rng, [300, 200, 64], hkv, d, 16, "bf16")
+    for b, length in enumerate(c.lens):
+        p, _, s = c.at(b, np.arange(length))
+        c.position[p, :, s] = np.arange(length)[:, None]
+    c.device(mbd)
+    new = torch.zeros(n, dtype=torch.int32, device="cuda")
+    mbd.kv_cache_evict(c.c, new, c.lens_d, c.table_d, c.width, n, 100, 20)
+    c.lens = c.evict(100, 20)
+    c.lens_d.copy_(new)
+    c.check_equal("evict")
+    p, _, s = c.at(0, np.arange(100))
+    assert (np.diff(c.position[p, 0, s].astype(np.int64)) < 0).any()
+    q = bits(rng, n, hq * d)
+    nb = mbd.paged_attention_workspace_bytes(c.c, c.width, n, hq)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    for window in (0, 20):
+        out, lse = torch.zeros(n, hq * d, dtype=torch.bfloat16, device="cuda"), torch.zeros(n, hq, device="cuda")
+        mbd.paged_attention_decode(out, up(q), 0, c.c, c.table_d, c.width, c.lens_d, n, hq, 0.125, window, lse, False, ws, nb)
+        want = c.attend(q, hq, 0.125, window)
+        check_close(out.float().cpu().numpy().reshape(n, hq, d), want[0], want[2], "out")
+        check_close(lse.cpu().numpy(), want[1], want[3], "lse")
