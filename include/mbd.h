@@ -471,7 +471,8 @@ mbd_status mbd_launch_shape(int kind, int mode, int64_t n_tokens, int64_t width,
  * that is not a multiple of 16 bytes MBD_ERR_MISALIGNED; a head_dim other than 64, 128 and 256, a page_size that is no
  * power of two or above 65536, or sizes beyond the limits below MBD_ERR_UNSUPPORTED. Page numbers and lengths live on
  * the device: the kernels check each before they use it (MBD_DEVERR_BAD_INDEX). What the entry points write must
- * not overlap what they read, their cache apart; that is checked for the tensors of a call.
+ * not overlap what they read, their cache apart, nor their results any array of the cache; that is checked for the
+ * tensors of a call.
  * n_seqs == 0 (append: n_tokens == 0) is a no-op; the cache's description and the sizes are checked even so.
  */
 #define MBD_KV_ABI_VERSION 1

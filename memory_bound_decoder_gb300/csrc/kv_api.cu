@@ -259,7 +259,7 @@ mbd_status mbd_paged_attention_decode(void* out, const void* q, int64_t q_stride
                             {lse, uint64_t(n_seqs) * n_q_heads * 4},
                             {workspace, ws.total},
                             accumulate ? c.weight : none};
-    for (const Range& r : {qr, table, lens, c.k, c.v, c.k_scale, c.v_scale})
+    for (const Range& r : {qr, table, lens, c.k, c.v, c.k_scale, c.v_scale, c.position, accumulate ? none : c.weight})
         if (overlaps_any(r, writes)) return MBD_ERR_INVALID_ARG;
     for (int i = 0; i < 4; ++i)
         for (int j = 0; j < i; ++j)
