@@ -65,8 +65,9 @@ mbd_status check_shape(const mbd_kv_cache* c, int64_t pages_per_seq, int64_t n_s
     if (c->page_stride != 0) {
         if (c->page_stride < dense) return MBD_ERR_INVALID_ARG;
         if (c->page_stride * size % 16 != 0) return MBD_ERR_MISALIGNED;
-        if (c->page_stride > (int64_t{1} << 40) / c->n_pages * 64) return MBD_ERR_UNSUPPORTED;   // 64 T elements in all
     }
+    // 64 T elements in all, so that no offset and no range of a check passes 64 bits.
+    if ((c->page_stride != 0 ? c->page_stride : dense) > (int64_t{1} << 40) / c->n_pages * 64) return MBD_ERR_UNSUPPORTED;
     return MBD_OK;
 }
 
