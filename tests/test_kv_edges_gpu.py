@@ -238,3 +238,27 @@ def test_window_counts_slots_also_after_an_eviction(mbd):
         want = c.attend(q, hq, 0.125, window)
         check_close(out.float().cpu().numpy().reshape(n, hq, d), want[0], want[2], "out")
         check_close(lse.cpu().numpy(), want[1], want[3], "lse")
+
+
+@pytest.mark.parametrize("fmt,mode", STORES)
+@pytest.mark.parametrize("hkv,d", [(3, 64), (5, 128), (7, 64), (3, 256), (1, 64), (11, 128), (17, 256)])
+def test_append_prompts_of_any_layout(mbd, hkv, d, fmt, mode):
+    """Many tokens of head layouts whose rows are no power of two of vectors, several tokens to a CTA, the last CTA with
+    fewer: the quotients that find a vector's token and head."""
+    rng = np.random.default_rng(hkv * d)
+    counts = [708, 0, 2, 40]
+    lens = [x + 5 * i for i, x in enumerate(counts)]
+    c = Cache(rng, lens, hkv, d, 8, fmt, mode)
+    c.device(mbd)
+    cu = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    total = int(cu[-1]) + 1                               # 751, a prime; one row is padding
+    k, v = bits(rng, total, hkv * d), bits(rng, total, hkv * d)
+    mbd.device_error_flags(clear=True)
+    mbd.kv_cache_append(c.c, up(k), up(v), 0, c.table_d, c.width, c.lens_d, len(counts), total, up(cu))
+    torch.cuda.synchronize()
+    for b, x in enumerate(counts):
+        if x:
+            at = slice(cu[b], cu[b + 1])
+            c.store(b, np.arange(lens[b] - x, lens[b]), k[at].reshape(x, hkv, d), v[at].reshape(x, hkv, d))
+    c.check_equal("append")
+    assert mbd.device_error_flags() == 0
