@@ -42,7 +42,8 @@
  *     order. Each successful call of an entry point launches exactly one kernel (a batch: one per op; an attention that
  *     accumulates weights: two).
  *   - Arithmetic is fp32 in registers; every intermediate stays unrounded until the single final rounding
- *     to bf16 or to E4M3 (round to nearest even, saturating finite overflow to +-448).
+ *     to bf16 or to E4M3 (round to nearest even, saturating finite overflow to +-448) (the attention's
+ *     probabilities apart: see there).
  *   - Scale convention (both FP8 entry points): `scale` is the DEQUANTISATION multiplier, value ~ code * scale.
  *       MBD_SCALE_STATIC_PER_TENSOR: scale points to ONE fp32 value, read on the device; it must be finite
  *         and > 0 (0 yields all-zero codes; other values give unspecified codes).
@@ -540,7 +541,11 @@ mbd_status mbd_kv_cache_append(const mbd_kv_cache* cache, const void* k, const v
  *                another through it, and it need not be set before the first; calls that may run at the same time need
  *                one each. (CTAs that share a sequence find each other there by a 64-bit number that each call draws anew:
  *                memory that holds this number by chance would mislead them.)
- * Sums are fp32; the result does not depend on what else runs, and equal calls give equal bits.
+ * Sums, maxima and lse are fp32. For the product with v_j, exp(x_j - lse) is rounded: to the sum of two bf16 terms in a bf16
+ * cache (off by 2^-16 of it), to one f16 term in an FP8 cache (off by 2^-11 of it, or by 2^-31 of the largest of the
+ * sequence where that is more; dynamic: of the largest product with the scale of v_j). So in an FP8 cache what L slots
+ * in view hold can be lost up to L 2^-31 of the largest |v|: 2^-9 of it, half a step of bf16, at four million slots. The
+ * result does not depend on what else runs, and equal calls give equal bits.
  */
 size_t mbd_paged_attention_workspace_bytes(const mbd_kv_cache* cache, int64_t pages_per_seq, int64_t n_seqs,
                                            int64_t n_q_heads, int accumulate);

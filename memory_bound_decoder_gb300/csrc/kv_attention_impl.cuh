@@ -14,7 +14,10 @@
 //   - V^T wants pairs of keys in one register: one byte permutation of two keys' vectors (E4M3: before conversion);
 //   - the probabilities change from accumulator to operand layout by one movmatrix per 8 keys.
 // E4M3 codes become f16 by the hardware conversion (exact), so the FP8 path multiplies in f16, with q scaled by a power of
-// two per head so that its elements are normal f16 numbers (bf16's 8 bits fit) and p by 2^6 (flushing below 2^-30).
+// two per head so that its elements are normal f16 numbers (bf16's 8 bits fit) and p by 2^6: one f16 term, off by 2^-11 of it,
+// or by 2^-31 of the largest p that the warp keeps where that is more, as subnormals end there. A warp's sums are relative
+// to its own maximum and joined in fp32, so what is lost that way is at most 2^-31 of the result's largest |v| for each key that
+// one warp takes of an item: 2^-16 at 32768 keys, a quarter of 131072.
 // In the bf16 path p goes in as the sum of two bf16 terms (2^-16): rounding it once would cost as much accuracy as
 // rounding the output does, and the second product costs nothing measurable (64 sequences of up to 2047 tokens, 32 query
 // and 8 key-value heads: 48.4 us without it, 48.6 with it). Both terms are positive (of p above 2^-110), or an infinite value would

@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 
 import workloads as wl
+from oracle import kv_cache as ref
 from oracle.kv_cache import check_close
 from tests.test_kv_gpu import STORES, Cache, bits, mbd, up  # noqa: F401  (mbd is the fixture)
 
@@ -262,3 +263,36 @@ def test_append_prompts_of_any_layout(mbd, hkv, d, fmt, mode):
             c.store(b, np.arange(lens[b] - x, lens[b]), k[at].reshape(x, hkv, d), v[at].reshape(x, hkv, d))
     c.check_equal("append")
     assert mbd.device_error_flags() == 0
+
+
+@pytest.mark.parametrize("fmt,mode", STORES)
+def test_attention_of_small_probabilities(mbd, fmt, mode):
+    """Probabilities of 2^-16 to 2^-36 beside one of 1, each with a value in an element of its own: off by half a bf16 step
+    (2^-8), by the rounding before the product (2^-16, 2^-11 in FP8) and by the fp32 sums and exponentials (a hundred times
+    2^-23), in FP8 besides by 2^-31 of the largest value."""
+    powers = np.array([0, 16, 18, 20, 22, 24, 26, 28, 30, 32, 36])
+    d, n = 64, len(powers)
+    c = Cache(np.random.default_rng(0), [n], 1, d, 16, fmt, mode, fill=False)
+    kx, vx = np.zeros((n, 1, d)), np.zeros((n, 1, d))
+    kx[:, 0, 0] = -powers                                 # exact in E4M3
+    vx[1:, 0, 1:n] = 448 * np.eye(n - 1)
+    p, _, s = c.at(0, np.arange(n))
+    for raw, scales, x in ((c.k_raw, c.ks, kx), (c.v_raw, c.vs, vx)):
+        if fmt == "fp8":
+            c.view(raw)[p, :, s] = ref.e4m3_codes(x)
+            scales[(p, slice(None), s) if mode == "dynamic" else 0] = 1
+        else:
+            c.view(raw)[p, :, s] = wl.f32_to_bf16_bits(x.astype(np.float32))
+    c.weight[p, :, s] = 0
+    q = np.zeros((1, d), np.uint16)
+    q[0, 0] = 0x3F80
+    scale = float(np.float32(np.log(2)))
+    c.device(mbd)
+    out, lse, w = attend(mbd, c, q, 1, scale)
+    pr = np.exp(-powers * scale)
+    pr /= pr.sum()
+    want = np.zeros(d)
+    want[1:n] = pr[1:] * 448
+    tol = want * (2.0 ** -8 + (2.0 ** -11 if fmt == "fp8" else 2.0 ** -16) + 100 * 2.0 ** -23)
+    check_close(out[0, 0], want, tol + (448 * 2.0 ** -31 if fmt == "fp8" else 0), "out")
+    check_close(w[p, 0, s], pr, pr * 100 * 2.0 ** -23, "weights")
