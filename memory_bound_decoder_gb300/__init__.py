@@ -166,7 +166,7 @@ def _ptr(a: Any) -> Optional[int]:
         return a
     dp = getattr(a, "data_ptr", None)
     if dp is not None:
-        return dp()
+        return int(dp())
     raise TypeError(f"expected a tensor or an integer device pointer, got {type(a).__name__}")
 
 
