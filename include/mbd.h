@@ -537,7 +537,8 @@ mbd_status mbd_kv_cache_append(const mbd_kv_cache* cache, const void* k, const v
  *   accumulate : != 0 adds to weight[j] of each slot in view the sum of exp(x_j - lse) over the query heads that read
  *                it (the cache must have `weight`; sequences must not share pages then).
  *   workspace  : device memory of the caller, 256-byte aligned, mbd_paged_attention_workspace_bytes() long for the
- *                same arguments on the same device (0 for arguments that the call refuses). Calls hand nothing to one
+ *                same arguments on the same device (0 for arguments that the call refuses; with accumulation about 4 bytes
+ *                for each query head and slot that the table can name, whatever the lengths). Calls hand nothing to one
  *                another through it, and it need not be set before the first; calls that may run at the same time need
  *                one each. (CTAs that share a sequence find each other there by a 64-bit number that each call draws anew:
  *                memory that holds this number by chance would mislead them.)
@@ -567,7 +568,7 @@ mbd_status mbd_paged_attention_decode(void* out, const void* q, int64_t q_stride
  *              are done already).
  *   budget   : 0 .. MBD_KV_MAX_CAPACITY;   recent : 0 .. budget.
  * The cache must have `weight` and `position`. Limits: pages_per_seq * page_size <= MBD_KV_MAX_EVICT_CAPACITY, n_pages *
- * page_size <= 2^31.
+ * page_size <= 2^31. The launch is sized by pages_per_seq, so a table no wider than the longest sequence needs is the fastest.
  */
 #define MBD_KV_MAX_EVICT_CAPACITY 425984
 mbd_status mbd_kv_cache_evict(const mbd_kv_cache* cache, int32_t* new_lens, const int32_t* seq_lens,

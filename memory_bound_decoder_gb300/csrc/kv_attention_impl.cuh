@@ -20,7 +20,7 @@
 // one warp takes of an item: 2^-16 at 32768 keys, a quarter of 131072.
 // In the bf16 path p goes in as the sum of two bf16 terms (2^-16): rounding it once would cost as much accuracy as
 // rounding the output does, and the second product costs nothing measurable (64 sequences of up to 2047 tokens, 32 query
-// and 8 key-value heads: 48.4 us without it, 48.6 with it). Both terms are positive (of p above 2^-110), or an infinite value would
+// and 8 key-value heads: 48.6 us without it, 48.7 with it). Both terms are positive (of p above 2^-110), or an infinite value would
 // meet a second term that is zero or negative and come out as NaN. The running maximum is kept until a logit exceeds it by 2^8:
 // one vote a step instead of three shuffles a head (one FP8 sequence of 131071 tokens: 61.1 us, 62.3 with it kept exact).
 //
@@ -36,7 +36,9 @@
 //   bf16, 16 sequences of 9001..32768 tokens, 128 query and 8 key-value heads     206 us, 6650 GB/s
 //   bf16, 64 sequences of 0..2047 tokens, 32 and 8 heads, pages of 16              48.5 us, 5550 GB/s
 //   FP8 static, 32 sequences of 100..8192 tokens, 64 and 8 heads, pages of 32      53 us, 5130 GB/s
-//   FP8 dynamic, one sequence of 131071 tokens, 64 and 8 heads                     60 us, 4600 GB/s
+//   FP8 dynamic, one sequence of 131071 tokens, 64 and 8 heads                     61 us, 4540 GB/s
+//   FP8 static, 4 sequences of 13240..17308 tokens, 128 and 8 heads, pages of 128  38.5 us, 3250 GB/s
+//   bf16, 32 sequences of 100..8192 tokens, 16 and 2 heads of 256, pages of 16     56 us, 4830 GB/s
 //   bf16, 24 windows of 1024 tokens, 16 and 16 heads of 64                         23.4 us, 4230 GB/s
 // About ten microseconds of each do not depend on the bytes: launch, lengths, page table and first rows on the way in (each
 // a round trip of half a microsecond), shares that end up to 8% apart, and the joins.
@@ -52,7 +54,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kJoinParts = 40;   // parts of a cut item that are added up at once (one long sequence: 59.8 us; in two stages of 16: 61.0)
+constexpr int kJoinParts = 40;   // parts of a cut item that are added up at once (one long sequence: 61.1 us; in two stages of 16: 61.4)
 constexpr float kLazy = 8.0f;    // units of log2 that a logit may exceed the kept maximum by (p <= 2^8)
 constexpr float kShift = 6.0f;   // E4M3: p is multiplied by 2^kShift (p <= 2^14 in f16)
 constexpr float kLn2 = 0.693147180559945309f;

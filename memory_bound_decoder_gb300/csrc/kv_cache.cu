@@ -7,8 +7,9 @@
 // so their loads are under way while the slots are looked up. head_dim / 8 lanes own a row, 16 bytes of k and of v
 // each, so the maximum of a row is a few shuffles and nothing is staged. Measured on one GB300: 8190 prompt tokens of 8
 // heads of 128 in bf16 7.4 us (5180 GB/s of the operation's bytes, part of them from L2), 8700 into E4M3 with a static
-// scale 13.8 us (3870 GB/s; the conversion's instructions, two per element, are half of that), 128 single tokens 5.3 us (the
-// host's call).
+// scale 13.8 us (3870 GB/s) and with a scale a row 14.9, 128 single tokens 6 us (the host's call). The E4M3 forms are short of
+// the bf16 one's rate for two reasons that a capture shows together: warps wait first of all at the block's barrier, for the
+// slots and then for the static scales loaded behind it, and issue is busy half of the time, the ALU pipe 46%.
 //
 // Eviction. Of the `len` slots of one sequence and head the `budget` best stay: first those whose position is
 // among the newest `recent`, then those of the largest weight, equal ones by the lowest slot. A kept row behind
@@ -17,10 +18,11 @@
 // the order of the moves is free. One cluster owns a sequence's head: each CTA keeps its share of the slots as
 // order-preserving 32-bit keys in shared memory (read from HBM once), the budget-th largest key is found by a
 // radix selection of 8 bits a pass whose histograms are added up through distributed shared memory, and the
-// ranks of the moving rows come from ballots and one scan in slot order. The moves run near HBM's rate; what surrounds them
-// is latency: eight cluster barriers of about a microsecond and the passes between them. Measured on one GB300: 16
-// sequences of 1500..4099 tokens to 2048, 8 heads of 128 in bf16, 33 us (12 of them moves), one of 131072 to 32768 in FP8 60 us
-// (16 of them moves; a cluster of 16 for each of 8 heads is all that the card's GPCs hold at once).
+// ranks of the moving rows come from ballots and one scan in slot order. Measured on one GB300, the selection by calls whose
+// best slots lie before the budget already: 16 sequences of 1500..4099 tokens to 2048, 8 heads of 128 in bf16, 27 us, 11 of
+// them launch and selection, 16 moves (their bytes take 10 at the copy rate; only the longer rows' CTAs have any); one of 131072
+// to 32768 in FP8 55 us, 25 of them launch and selection (up to eight cluster barriers and the passes between them), 31
+// moves (16 at the copy rate; a cluster of 16 for each of 8 heads is all that the card's GPCs hold at once).
 #include <cooperative_groups.h>
 
 #include "kv_common.cuh"
