@@ -527,7 +527,8 @@ mbd_status mbd_kv_cache_append(const mbd_kv_cache* cache, const void* k, const v
  * n_kv_heads). Over the slots j in view -- 0 .. seq_lens[b] - 1, with window > 0 the last `window` of them:
  *     x_j = scale * (q . k_j),   lse = log(sum_j exp(x_j)),   out = bf16(sum_j exp(x_j - lse) * v_j)
  * A sequence with nothing in view gives zeros and lse = -inf, and so does a query head whose logits are all -inf (it adds
- * nothing to the weights); what lies in masked slots is not read. A NaN logit gives NaN, an infinite value an infinity.
+ * nothing to the weights); what lies in masked slots is not read. A logit of NaN or +inf gives NaN, an infinite value an
+ * infinity (where its probability is above 2^-100: far below, the product with zero is NaN).
  *   out        : [n_seqs, n_q_heads * head_dim] bf16, 16-byte aligned, written.
  *   q          : n_seqs rows of n_q_heads * head_dim bf16, q_stride elements apart (0: dense).
  *   scale      : finite (also times log2(e)), usually 1 / sqrt(head_dim).   window : 0 (none) or the number of slots in view.

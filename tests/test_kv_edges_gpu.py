@@ -135,6 +135,20 @@ def test_attention_infinite_values(mbd, hq, hkv, d, accumulate):
         check_close(w[live], want[4][live], want[5][live], "weights")
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (18, 2, 128), (2, 2, 256)])
+def test_attention_with_a_logit_of_infinity(mbd, hq, hkv, d):
+    """An infinite key under positive queries leaves no softmax: NaN for the heads that read it, and no others."""
+    rng = np.random.default_rng(hq)
+    c = Cache(rng, LONELY, hkv, d, 16, "bf16")
+    q = wl.f32_to_bf16_bits(np.abs(wl.bf16_bits_to_f32(bits(rng, len(LONELY), hq * d))) + np.float32(2 ** -10))
+    want = c.attend(q, hq, d ** -0.5, 0, True)
+    for b, length in enumerate(c.lens):
+        p, _, s = c.at(b, [length // 2])
+        c.view(c.k_raw)[p[0], 1, s[0], 3] = INF16
+    c.device(mbd)
+    check_planted(c, want, attend(mbd, c, q, hq, d ** -0.5), list(range(hq // hkv, hq)), hq)
+
+
 @pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (18, 2, 128), (2, 2, 256), (260, 2, 64)])
 def test_attention_with_logits_of_minus_infinity(mbd, hq, hkv, d):
     """Keys of -inf under positive queries have no weight; where all of a head's keys are such, it gives zeros and -inf
