@@ -251,7 +251,7 @@ template <int D, int STORE>
 __device__ __forceinline__ void write_out(const AttendParams& p, int64_t head, int dim, const float4& acc, float m, float t,
                                           float mo) {
     const float one = STORE == kKvFp8Dynamic ? ex2(mo - m) : (STORE == kKvFp8Static ? *p.c.v_scale : 1.0f);
-    const float f = mo == -INFINITY ? 0.0f : one / t;
+    const float f = mo == -INFINITY || t == 0.0f ? 0.0f : one / t;   // (t == 0: every logit is -inf)
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + head * D + dim) =
         make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
     if (dim == 0) {
@@ -908,22 +908,22 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
                         *reinterpret_cast<float4*>(&sm.o[warp][head][dim]) =
                             make_float4(o[nt][k][h], o[nt][k][2 + h], o[nt][k + 1][h], o[nt][k + 1][2 + h]);
                     }
-                    // No maximum was kept: nothing in view (the sums are 0), or NaN alone, which fmaxf passes over and
-                    // the sums hold. Such sums stay, under the least exponent: in a join no factor makes them
-                    // finite, and what another warp or part has in the same row's other elements is not scaled away.
+                    // No maximum was kept: nothing in view (the sums are 0), or what fmaxf passes over and the sums hold: NaN
+                    // logits, NaN scales, NaN or infinite values under a weight of 0. Such sums stay, under the least exponent:
+                    // in a join no factor makes them finite, and what another warp or part has in the same row's
+                    // other elements is not scaled away.
+                    const float limv = kDyn ? limo[nt][h] : lim[nt][h], refv = kDyn ? refo[nt][h] : ref[nt][h];
                     float t = sum[nt][h], nan = 0.0f;
-                    if constexpr (kDyn) {   // (a scale of the values that is NaN shows in o only)
+                    if (__any_sync(0xffffffffu, limv == -INFINITY)) {
 #pragma unroll
                         for (int k = 0; k < KK; ++k) nan += 0.0f * o[nt][k][h] + 0.0f * o[nt][k][2 + h];
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) nan += __shfl_xor_sync(0xffffffffu, nan, x);
                     }
 #pragma unroll
-                    for (int x = 4; x < 32; x <<= 1) {
-                        t += __shfl_xor_sync(0xffffffffu, t, x);
-                        if constexpr (kDyn) nan += __shfl_xor_sync(0xffffffffu, nan, x);
-                    }
+                    for (int x = 4; x < 32; x <<= 1) t += __shfl_xor_sync(0xffffffffu, t, x);
                     const float m = lim[nt][h] != -INFINITY ? ref[nt][h] : (t == 0.0f ? -INFINITY : -FLT_MAX);
-                    const float mo = !kDyn ? m
-                                           : (limo[nt][h] != -INFINITY ? refo[nt][h] : (nan == 0.0f ? -INFINITY : -FLT_MAX));
+                    const float mo = limv != -INFINITY ? refv : (nan == 0.0f ? -INFINITY : -FLT_MAX);
                     if (r == 0) sm.ml[warp][head] = make_float4(m, t, mo, 0.0f);
                 }
             __syncthreads();

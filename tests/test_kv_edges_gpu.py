@@ -149,6 +149,38 @@ def test_attention_with_a_logit_of_infinity(mbd, hq, hkv, d):
     check_planted(c, want, attend(mbd, c, q, hq, d ** -0.5), list(range(hq // hkv, hq)), hq)
 
 
+@pytest.mark.parametrize("where", ["last", "first", "all"])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (18, 2, 128), (2, 2, 256)])
+def test_attention_infinite_values_without_weight(mbd, hq, hkv, d, where):
+    """An infinite value whose logit is -inf: zero times infinity, NaN in that element wherever the key lies (alone in
+    its warp, or with every logit -inf), and nothing in the others."""
+    rng = np.random.default_rng(hq)
+    c = Cache(rng, LONELY, hkv, d, 16, "bf16")
+    q = wl.f32_to_bf16_bits(np.abs(wl.bf16_bits_to_f32(bits(rng, len(LONELY), hq * d))) + np.float32(2 ** -10))
+    slots = [np.arange(n) if where == "all" else np.array([n - 1 if where == "last" else 0]) for n in c.lens]
+    alone = np.array([len(at) == n for at, n in zip(slots, c.lens)])
+    for b, at in enumerate(slots):
+        p, _, s = c.at(b, at)
+        c.view(c.k_raw)[p, :, s, 3] = INF16 | 0x8000
+        c.view(c.v_raw)[p[-1], :, s[-1], 5] = INF16
+    c.device(mbd)
+    out, lse, w = attend(mbd, c, q, hq, d ** -0.5)
+    assert np.isnan(out[..., 5]).all()
+    keep = np.delete(np.arange(d), 5)
+    assert not out[alone][..., keep].any() and np.isneginf(lse[alone]).all()
+    group = hq // hkv
+    for b in np.flatnonzero(~alone):
+        k, v = c.rows(b, np.setdiff1d(np.arange(c.lens[b]), slots[b]))
+        x = np.einsum("hgd,hld->hgl", wl.bf16_bits_to_f32(q[b]).astype(np.float64).reshape(hkv, group, d), k) * d ** -0.5
+        pr = np.exp(x - x.max(-1, keepdims=True))
+        pr /= pr.sum(-1, keepdims=True)
+        a = np.einsum("hgl,hld->hgd", pr, np.abs(v)).reshape(hq, d)
+        o = np.einsum("hgl,hld->hgd", pr, v).reshape(hq, d)
+        size = np.abs(wl.bf16_bits_to_f32(q[b])).reshape(hq, d).sum(-1).max() * np.abs(k).max() * d ** -0.5
+        tol = a * (2 * (d * 2.0 ** -23 + 2.0 ** -22) * size + 2.0 ** -16 + 2 * (k.shape[1] / 32 + 64) * 2.0 ** -23) + 2.0 ** -8 * np.abs(o)
+        check_close(out[b][:, keep], o[:, keep], tol[:, keep], "out")
+
+
 @pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (18, 2, 128), (2, 2, 256), (260, 2, 64)])
 def test_attention_with_logits_of_minus_infinity(mbd, hq, hkv, d):
     """Keys of -inf under positive queries have no weight; where all of a head's keys are such, it gives zeros and -inf
