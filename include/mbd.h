@@ -15,6 +15,7 @@
  *   mbd_kv_cache_append, mbd_paged_attention_decode, mbd_kv_cache_evict
  *                                    the decode step's paged key-value cache: new tokens in, the attention of
  *                                    one new token per sequence over it, eviction by accumulated weight
+ *   mbd_kv_cache_resize, mbd_rotary    the cache's pages and the new tokens' slots, handed out on the GPU; rotary positions
  *
  * Definitions (cited by page title and section):
  *   [TRT] "TensorRT-LLM: Compiling Inference Engines Ahead of Time", section "Fusing operations, measured":
@@ -575,6 +576,110 @@ mbd_status mbd_paged_attention_decode(void* out, const void* q, int64_t q_stride
 mbd_status mbd_kv_cache_evict(const mbd_kv_cache* cache, int32_t* new_lens, const int32_t* seq_lens,
                               const int32_t* page_table, int64_t pages_per_seq, int64_t n_seqs, int64_t budget,
                               int64_t recent, mbd_stream_t stream);
+
+/*
+ * What goes with the cache in a serving step: pages and slots for the tokens to come, rotary positions of their queries
+ * and keys, the attention of whole prompts. Their section has a version of its own.
+ */
+#define MBD_STEP_ABI_VERSION 1
+int mbd_step_abi_version(void);
+
+/*
+ * Give every sequence the length that is wanted: pages that it no longer needs go back to the free ones, pages that it
+ * needs come from them, and its new tokens get their places. One call serves a whole step of continuous batching:
+ * want_lens[b] is seq_lens[b] + 1 for a sequence that is decoded, the prompt's length for a row that was empty, what
+ * mbd_kv_cache_evict left (its new_lens) for one that was evicted from, 0 for one that has ended.
+ *   page_table   : int32 [n_seqs, pages_per_seq]; entries of pages given up become -1, those of pages taken are written.
+ *                  A page that several sequences name must not be given up by any of them.
+ *   free_pages   : int32 [n_pages], a ring of the pool's free pages; free_ends: int32 [2], the place of the first of them in the
+ *                  ring and their number. Pages given up go behind the last one, by sequence and then by slot; then
+ *                  pages are taken from the first one on, in the same order.
+ *   seq_lens     : int32 [n_seqs], read, and written where it changes.   want_lens: int32 [n_seqs], read.
+ *   tokens_seen  : int32 [n_seqs] or null: the tokens that a sequence has had, evicted ones among them; grows with its new
+ *                  tokens, and is set to 0 where the wanted length is 0.
+ *   cu_tokens    : int32 [n_seqs + 1], written: rows cu_tokens[b] .. cu_tokens[b + 1] - 1 of the step are sequence b's new
+ *                  tokens (as mbd_kv_cache_append and mbd_prompt_attention take them).
+ *   positions    : int32 [n_tokens] or null, written: the position of each row's token in its sequence (its slot, or counted on
+ *                  from tokens_seen), 0 for rows from cu_tokens[n_seqs] on.
+ *   slots        : int64 [n_tokens] or null, written: page * page_size + place of each row's token in the pool, -1 for rows from
+ *                  cu_tokens[n_seqs] on and for tokens on a page outside the pool.
+ *   n_tokens     : rows that the step has room for.
+ * Sequences that grow are served in their order, as long as there is room: one that needs pages is refused if it and those
+ * before it ask for more than are free (those given up in this call among them), and one whose tokens, with those before it,
+ * are more than n_tokens is too. A refused sequence keeps its length and gets no rows, so seq_lens tells which were granted.
+ * A length outside [0, pages_per_seq * page_size], free_ends outside the ring, more pages given up than the ring has room
+ * for, or a page number outside the pool set MBD_DEVERR_BAD_INDEX: the sequence stays as it is; nothing changes; the pages
+ * behind the ring's room are lost; the number is handed on (the cache's calls check it).
+ * page_size: a power of two up to 65536. Limits: n_seqs <= MBD_KV_MAX_RESIZE_SEQS, n_seqs * pages_per_seq < 2^31, n_tokens <=
+ * MBD_KV_MAX_ROWS. What is written must not overlap anything else. n_seqs == 0 is a no-op.
+ */
+#define MBD_KV_MAX_RESIZE_SEQS 8192
+mbd_status mbd_kv_cache_resize(int32_t* page_table, int64_t pages_per_seq, int64_t page_size, int64_t n_pages,
+                               int32_t* free_pages, int32_t* free_ends, int32_t* seq_lens, const int32_t* want_lens,
+                               int64_t n_seqs, int32_t* cu_tokens, int32_t* positions, int64_t* slots, int64_t n_tokens,
+                               int32_t* tokens_seen, mbd_stream_t stream);
+
+/*
+ * Rotary positions. Pair i (i < rotary_dim / 2) of each head is turned by t = position * f_i and stretched by the amplitude:
+ *     a' = bf16(amplitude * (a cos t - b sin t)),  b' = bf16(amplitude * (b cos t + a sin t))
+ * with a and b at i and i + rotary_dim / 2 (MBD_ROTARY_HALF) or at 2 i and 2 i + 1 (MBD_ROTARY_INTERLEAVED); elements from
+ * rotary_dim on stay as they are.
+ *   x, out     : n_tokens rows of n_heads * head_dim bf16, x_stride (out_stride) elements apart (0: dense). Queries and keys
+ *                that lie side by side in a stacked projection are one call. out may be x (with the same stride): then only
+ *                the turned elements are touched. Otherwise they must not overlap.
+ *   turns      : uint64 [rotary_dim / 2] on the device, 8-byte aligned: f_i as a fraction of a turn, in units of 2^-64 of it
+ *                (mbd_rotary_table makes them). position * turns mod 2^64 is the exact angle of the table's frequency,
+ *                whatever the position: nothing is lost at far ones.
+ *   positions  : int32 [n_tokens] on the device (negative ones turn back), or null: a token's position is its row.
+ *   amplitude  : finite.
+ * head_dim and rotary_dim are multiples of 16, rotary_dim <= head_dim <= 4096; n_tokens <= MBD_KV_MAX_ROWS, n_heads <= 2^20.
+ * The angle, its sine and cosine and the products are fp32 (sine and cosine to 2^-22 or so); one rounding to bf16.
+ */
+typedef enum { MBD_ROTARY_HALF = 0, MBD_ROTARY_INTERLEAVED = 1 } mbd_rotary_layout;
+
+mbd_status mbd_rotary(void* out, int64_t out_stride, const void* x, int64_t x_stride, const uint64_t* turns, float amplitude,
+                      const int32_t* positions, int64_t n_tokens, int64_t n_heads, int64_t head_dim, int64_t rotary_dim,
+                      int layout, mbd_stream_t stream);
+
+/*
+ * Fill `turns` (HOST memory, rotary_dim / 2 values, for the caller to copy to the device once) and *amplitude for a model's
+ * frequencies. With g_i = base^(-2 i / rotary_dim) radians a position:
+ *   MBD_ROTARY_PLAIN   : f_i = g_i.
+ *   MBD_ROTARY_LINEAR  : f_i = g_i / factor.
+ *   MBD_ROTARY_NTK     : base becomes base * factor^(rotary_dim / (rotary_dim - 2)).
+ *   MBD_ROTARY_LLAMA3  : with n_i = original * g_i / 2 pi, the turns over the original context, and s_i = (n_i - low) / (high -
+ *                        low) held to [0, 1]: f_i = (1 - s_i) g_i / factor + s_i g_i.
+ *   MBD_ROTARY_YARN    : with d(b) = rotary_dim ln(original / (2 pi b)) / (2 ln base), first = max(0, floor(d(beta_fast))), last =
+ *                        min(rotary_dim - 1, ceil(d(beta_slow))) and r_i = (i - first) / max(last - first, 0.001) held to
+ *                        [0, 1]: f_i = r_i g_i / factor + (1 - r_i) g_i.
+ *   MBD_ROTARY_FACTORS : f_i = g_i / factors[i], a factor for each pair.
+ * amplitude: as given; 0 means 1 (MBD_ROTARY_YARN: 0.1 ln(factor) + 1, and 1 for a factor up to 1). All in fp64. Host only: no stream, no launch.
+ * MBD_ERR_INVALID_ARG for a null pointer, an unknown kind, a non-zero reserved, a rotary_dim that is not positive and even (NTK:
+ * or is 2), a base or factor that is not positive and finite, an amplitude that is negative or not finite, and for values of a
+ * kind's own that give no finite frequencies (low >= high; base 1 or betas or original not positive).
+ */
+typedef enum {
+    MBD_ROTARY_PLAIN = 0,
+    MBD_ROTARY_LINEAR = 1,
+    MBD_ROTARY_NTK = 2,
+    MBD_ROTARY_LLAMA3 = 3,
+    MBD_ROTARY_YARN = 4,
+    MBD_ROTARY_FACTORS = 5
+} mbd_rotary_kind;
+
+typedef struct {
+    int32_t kind;            /* mbd_rotary_kind */
+    int32_t reserved;        /* must be 0 */
+    double base;
+    double factor;           /* LINEAR, NTK, LLAMA3, YARN */
+    double original;         /* LLAMA3, YARN: the context that the model was trained on first */
+    double low, high;        /* LLAMA3 */
+    double beta_fast, beta_slow;   /* YARN */
+    double amplitude;
+    const double* factors;   /* FACTORS: rotary_dim / 2 values on the host */
+} mbd_rotary_scaling;
+
+mbd_status mbd_rotary_table(uint64_t* turns, float* amplitude, int64_t rotary_dim, const mbd_rotary_scaling* scaling);
 
 #ifdef __cplusplus
 }

@@ -74,6 +74,19 @@ class KVCache(ctypes.Structure):
                 ("mode", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+ROTARY_HALF, ROTARY_INTERLEAVED = 0, 1
+ROTARY_LAYOUTS = {"half": ROTARY_HALF, "interleaved": ROTARY_INTERLEAVED}
+ROTARY_KINDS = {"none": 0, "linear": 1, "ntk": 2, "llama3": 3, "yarn": 4, "factors": 5}
+
+
+class RotaryScaling(ctypes.Structure):
+    """How a model's rotary frequencies are made (the C struct mbd_rotary_scaling); rotary_table() fills it."""
+    _fields_ = [("kind", ctypes.c_int32), ("reserved", ctypes.c_int32), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("original", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("amplitude", ctypes.c_double), ("factors", ctypes.POINTER(ctypes.c_double))]
+
+
 OP_NAMES = {0: "add_rmsnorm", 1: "add_rmsnorm_quant_fp8", 2: "add_rmsnorm_quant_nvfp4", 3: "swiglu",
             4: "swiglu_quant_fp8", 5: "swiglu_quant_nvfp4"}
 OP_KINDS = {v: k for k, v in OP_NAMES.items()}
@@ -123,6 +136,10 @@ def _load() -> ctypes.CDLL:
     lib.mbd_paged_attention_decode.argtypes = [vp, vp, i64, kvp, vp, i64, vp, i64, i64, f32, i64, vp, cint, vp,
                                                ctypes.c_size_t, vp]
     lib.mbd_kv_cache_evict.argtypes = [kvp, vp, vp, vp, i64, i64, i64, i64, vp]
+    lib.mbd_step_abi_version.restype = cint
+    lib.mbd_kv_cache_resize.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp, i64, vp, vp, vp, i64, vp, vp]
+    lib.mbd_rotary.argtypes = [vp, i64, vp, i64, vp, f32, vp, i64, i64, i64, i64, cint, vp]
+    lib.mbd_rotary_table.argtypes = [vp, ctypes.POINTER(f32), i64, ctypes.POINTER(RotaryScaling)]
     i32p = ctypes.POINTER(ctypes.c_int32)
     lib.mbd_launch_shape.argtypes = [cint, cint, i64, i64, i32p, i32p, i32p]
     lib.mbd_launch_shape.restype = cint
@@ -131,7 +148,7 @@ def _load() -> ctypes.CDLL:
                "mbd_fused_add_rmsnorm_quant_nvfp4", "mbd_swiglu_quant_nvfp4", "mbd_run_program",
                "mbd_run_independent", "mbd_run_independent_with_program", "mbd_program_plan_build", "mbd_program_plan_launch", "mbd_program_plan_upload",
                "mbd_program_plan_launch_uploaded", "mbd_program_plan_launch_static", "mbd_kv_cache_append",
-               "mbd_paged_attention_decode", "mbd_kv_cache_evict"):
+               "mbd_paged_attention_decode", "mbd_kv_cache_evict", "mbd_kv_cache_resize", "mbd_rotary", "mbd_rotary_table"):
         getattr(lib, fn).restype = cint
     return lib
 
@@ -331,6 +348,51 @@ def kv_cache_evict(cache: KVCache, new_lens, seq_lens, page_table, pages_per_seq
     (mbd_kv_cache_evict)."""
     _check(get_lib().mbd_kv_cache_evict(cache, _ptr(new_lens), _ptr(seq_lens), _ptr(page_table), int(pages_per_seq),
                                         int(n_seqs), int(budget), int(recent), _stream(stream)), "kv_cache_evict")
+
+
+# ------------------------------------------------------------------------------------------------ a serving step
+
+def step_abi_version() -> int:
+    return int(get_lib().mbd_step_abi_version())
+
+
+def kv_cache_resize(page_table, pages_per_seq: int, page_size: int, n_pages: int, free_pages, free_ends, seq_lens,
+                    want_lens, n_seqs: int, cu_tokens, positions, slots, n_tokens: int, tokens_seen=None,
+                    stream=None) -> None:
+    """Give every sequence its wanted length: pages from and to the ring of free ones, and offsets, positions and slots for
+    the new tokens (mbd_kv_cache_resize)."""
+    _check(get_lib().mbd_kv_cache_resize(_ptr(page_table), int(pages_per_seq), int(page_size), int(n_pages),
+                                         _ptr(free_pages), _ptr(free_ends), _ptr(seq_lens), _ptr(want_lens), int(n_seqs),
+                                         _ptr(cu_tokens), _ptr(positions), _ptr(slots), int(n_tokens), _ptr(tokens_seen),
+                                         _stream(stream)), "kv_cache_resize")
+
+
+def rotary_table(rotary_dim: int, base: float = 10000.0, scaling="none", factor: float = 1.0, original: float = 0.0,
+                 low: float = 1.0, high: float = 4.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                 amplitude: float = 0.0, factors=None) -> tuple:
+    """(turns, amplitude) for rotary(): a host array of rotary_dim / 2 uint64, to be copied to the device once, and the
+    factor of the turned pairs (mbd_rotary_table). scaling: "none", "linear", "ntk", "llama3", "yarn" or "factors" (then
+    `factors` has one for each pair)."""
+    rotary_dim = int(rotary_dim)
+    given = None
+    if factors is not None:
+        given = (ctypes.c_double * len(factors))(*[float(x) for x in factors])
+        if len(given) != rotary_dim // 2:
+            raise ValueError(f"{len(given)} factors for {rotary_dim // 2} pairs")
+    args = RotaryScaling(ROTARY_KINDS[scaling] if isinstance(scaling, str) else int(scaling), 0, float(base), float(factor),
+                         float(original), float(low), float(high), float(beta_fast), float(beta_slow), float(amplitude),
+                         ctypes.cast(given, ctypes.POINTER(ctypes.c_double)) if given is not None else None)
+    turns, amp = (ctypes.c_uint64 * max(1, rotary_dim // 2))(), ctypes.c_float()
+    _check(get_lib().mbd_rotary_table(turns, ctypes.byref(amp), rotary_dim, ctypes.byref(args)), "rotary_table")
+    return turns, amp.value
+
+
+def rotary(out, out_stride: int, x, x_stride: int, turns, amplitude: float, positions, n_tokens: int, n_heads: int,
+           head_dim: int, rotary_dim: int, layout="half", stream=None) -> None:
+    """Turn each head's pairs by its token's position (mbd_rotary); out may be x. layout: "half" or "interleaved"."""
+    _check(get_lib().mbd_rotary(_ptr(out), int(out_stride), _ptr(x), int(x_stride), _ptr(turns), float(amplitude),
+                                _ptr(positions), int(n_tokens), int(n_heads), int(head_dim), int(rotary_dim),
+                                ROTARY_LAYOUTS[layout] if isinstance(layout, str) else int(layout), _stream(stream)), "rotary")
 
 
 # ------------------------------------------------------------------------------------------------ programs

@@ -11,6 +11,7 @@
 #include <cuda.h>
 
 #include "mbd.h"
+#include "step.h"
 #include "kv.h"
 #include "launch.h"
 
@@ -926,7 +927,8 @@ mbd_status mbd_device_error_flags(uint32_t* flags, int clear) {
     if (e == cudaSuccess) e = mbd::device_error_flags_program(&d, clear != 0);
     unsigned int kv = 0;
     for (auto read : {mbd::device_error_flags_kv_cache, mbd::device_error_flags_kv_attention,
-                      mbd::device_error_flags_kv_attention_fp8, mbd::device_error_flags_kv_attention_fp8_dynamic}) {
+                      mbd::device_error_flags_kv_attention_fp8, mbd::device_error_flags_kv_attention_fp8_dynamic,
+                      mbd::device_error_flags_kv_pages}) {
         unsigned int f = 0;
         if (e == cudaSuccess) e = read(&f, clear != 0);
         kv |= f;

@@ -1,0 +1,49 @@
+// Internal interface between the host layer of a serving step's other operators (step_api.cu) and their kernels
+// (rotary.cu, kv_pages.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace mbd {
+
+struct RotaryParams {
+    const void* x;              // [n_tokens] rows of n_heads * head_dim bf16, x_bytes apart
+    void* out;                  // the same, out_bytes apart; may be x
+    int64_t x_bytes;
+    int64_t out_bytes;
+    const uint64_t* turns;      // [rotary_dim / 2]: 2^64 of a turn a position
+    const int32_t* positions;   // [n_tokens], or null: a token's position is its row
+    float amplitude;
+    int64_t n_tokens;
+    int n_heads;
+    int head_dim;
+    int rotary_dim;
+    int interleaved;
+    int units;                  // of 16 elements in a head: those turned, and where out is not x the rest
+};
+
+struct ResizeParams {
+    int32_t* table;             // [n_seqs, pages_per_seq]
+    int64_t pages_per_seq;
+    int64_t capacity;           // slots that a row of the table can name
+    int page_shift;
+    int64_t n_pages;
+    int32_t* ring;              // [n_pages]
+    int32_t* ends;              // [2]: place of the first free page in the ring, number of free pages
+    int32_t* lens;              // [n_seqs]
+    const int32_t* want;        // [n_seqs]
+    int32_t* seen;              // [n_seqs] or null
+    int64_t n_seqs;
+    int32_t* cu;                // [n_seqs + 1]
+    int32_t* positions;         // [n_tokens] or null
+    int64_t* slots;             // [n_tokens] or null
+    int64_t n_tokens;
+    int ctas;                   // of the cluster
+};
+
+cudaError_t launch_rotary(const RotaryParams& p, int sms, cudaStream_t s);
+cudaError_t launch_kv_resize(const ResizeParams& p, cudaStream_t s);
+cudaError_t device_error_flags_kv_pages(unsigned int* flags, bool clear);
+
+}  // namespace mbd
