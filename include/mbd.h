@@ -463,7 +463,11 @@ mbd_status mbd_launch_shape(int kind, int mode, int64_t n_tokens, int64_t width,
  *
  * Stored elements. MBD_KV_BF16: as they are. MBD_KV_FP8: E4M3 codes under this library's scale convention (value ~
  * code * scale): MBD_SCALE_STATIC_PER_TENSOR, k_scale and v_scale ONE fp32 value each; MBD_SCALE_DYNAMIC_PER_TOKEN, one
- * for each token and head, fp32 [n_pages, n_kv_heads, page_size], written by the append.
+ * for each token and head, fp32 [n_pages, n_kv_heads, page_size], written by the append. MBD_KV_NVFP4: E2M1 codes, two a byte
+ * (element 2i in the low bits), with an E4M3 scale for each 16 elements of a row and one fp32 tensor scale, k_scale and v_scale
+ * (value ~ code * block scale * tensor scale, as in mbd_fused_add_rmsnorm_quant_nvfp4; mode is static): 4.5 bits an element. A
+ * page then holds its codes, [n_kv_heads, page_size, head_dim / 2] bytes, and behind them the scales of its blocks, [n_kv_heads,
+ * page_size, head_dim / 16] bytes; its size and page_stride count bytes, and a dense page is rounded up to 16 of them.
  *
  * weight and position, both [n_pages, n_kv_heads, page_size] and dense, are for caches that evict (else null): the
  * attention weight that a slot has been given so far, and the position of its token in the sequence.
@@ -480,17 +484,17 @@ mbd_status mbd_launch_shape(int kind, int mode, int64_t n_tokens, int64_t width,
 #define MBD_KV_ABI_VERSION 1
 int mbd_kv_abi_version(void);
 
-typedef enum { MBD_KV_BF16 = 0, MBD_KV_FP8 = 1 } mbd_kv_format;
+typedef enum { MBD_KV_BF16 = 0, MBD_KV_FP8 = 1, MBD_KV_NVFP4 = 4 } mbd_kv_format;
 
 typedef struct {
-    void* k;               /* bf16 or E4M3 codes */
+    void* k;               /* bf16, E4M3 codes, or E2M1 codes and their blocks' scales */
     void* v;
-    float* k_scale;        /* MBD_KV_FP8 */
+    float* k_scale;        /* MBD_KV_FP8, MBD_KV_NVFP4 */
     float* v_scale;
     float* weight;         /* or null */
     int32_t* position;     /* or null */
     int64_t n_pages;       /* 1 .. 2^31 - 1 */
-    int64_t page_stride;   /* elements; 0: n_kv_heads * page_size * head_dim */
+    int64_t page_stride;   /* elements (MBD_KV_NVFP4: bytes); 0: dense pages */
     int32_t page_size;
     int32_t n_kv_heads;
     int32_t head_dim;
@@ -516,7 +520,10 @@ typedef struct {
  *               sequence was evicted from, its slots fall behind its positions, and they have to be given: by its slot the
  *               newest token would count as older than those kept.
  * FP8: code = e4m3(value / scale), both divisions rounded to nearest; dynamic: scale = amax / 448 of the head's
- * head_dim values, zero codes where that is 0. If the cache has `weight`, the new slots' is set to 0.
+ * head_dim values, zero codes where that is 0. NVFP4: block scale = e4m3(amax / (6 * tensor scale)) of its 16 values, code =
+ * e2m1(value / (block scale * tensor scale)), each product and division in fp32, rounded to nearest; zero codes where the
+ * block scale is 0. (A tensor scale outside [2^-64, 2^64] gives zeros, and counts as 0 in the attention.) If the cache has
+ * `weight`, the new slots' is set to 0.
  */
 mbd_status mbd_kv_cache_append(const mbd_kv_cache* cache, const void* k, const void* v, int64_t row_stride,
                                const int32_t* page_table, int64_t pages_per_seq, const int32_t* seq_lens, int64_t n_seqs,
@@ -545,8 +552,8 @@ mbd_status mbd_kv_cache_append(const mbd_kv_cache* cache, const void* k, const v
  *                one each. (CTAs that share a sequence find each other there by a 64-bit number that each call draws anew:
  *                memory that holds this number by chance would mislead them.)
  * Sums, maxima and lse are fp32. For the product with v_j, exp(x_j - lse) is rounded: to the sum of two bf16 terms in a bf16
- * cache (off by 2^-16 of it), to one f16 term in an FP8 cache (off by 2^-11 of it, or by 2^-31 of the largest of the
- * sequence where that is more; dynamic: of the largest product with the scale of v_j). So in an FP8 cache what L slots
+ * cache (off by 2^-16 of it), to one f16 term in an FP8 or NVFP4 cache (off by 2^-11 of it, or by 2^-31 of the largest of the
+ * sequence where that is more; dynamic: of the largest product with the scale of v_j). So in such a cache what L slots
  * in view hold can be lost up to L 2^-31 of the largest |v|: 2^-9 of it, half a step of bf16, at four million slots. The
  * result does not depend on what else runs, and equal calls give equal bits.
  */

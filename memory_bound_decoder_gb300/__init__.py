@@ -61,8 +61,8 @@ class TuningEntry(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
-KV_BF16, KV_FP8 = 0, 1
-KV_FORMATS = {"bf16": KV_BF16, "fp8": KV_FP8, KV_BF16: KV_BF16, KV_FP8: KV_FP8}
+KV_BF16, KV_FP8, KV_NVFP4 = 0, 1, 4
+KV_FORMATS = {"bf16": KV_BF16, "fp8": KV_FP8, "nvfp4": KV_NVFP4, KV_BF16: KV_BF16, KV_FP8: KV_FP8, KV_NVFP4: KV_NVFP4}
 
 
 class KVCache(ctypes.Structure):
@@ -308,8 +308,9 @@ def kv_abi_version() -> int:
 def kv_cache(k, v, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, fmt="bf16", mode="static", k_scale=None,
              v_scale=None, weight=None, position=None, page_stride: int = 0) -> KVCache:
     """The description of a paged cache: pools k and v of n_pages pages [n_kv_heads, page_size, head_dim], page_stride
-    elements apart (0: dense), in `fmt` "bf16" or "fp8" (with `mode` and scales), and the accumulated weights and
-    positions of a cache that evicts. It holds the tensors' device pointers, not the tensors."""
+    elements apart (0: dense), in `fmt` "bf16", "fp8" (with `mode` and scales) or "nvfp4" (with tensor scales; pages of
+    codes and their blocks' scales, page_stride in bytes), and the accumulated weights and positions of a cache that
+    evicts. It holds the tensors' device pointers, not the tensors."""
     return KVCache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(weight), _ptr(position), int(n_pages),
                    int(page_stride), int(page_size), int(n_kv_heads), int(head_dim),
                    KV_FORMATS[fmt] if isinstance(fmt, str) else int(fmt), _mode(mode), 0)

@@ -9,13 +9,19 @@
 
 namespace mbd {
 
-// How a cache stores an element: bf16, E4M3 under one scale for all of k (of v), or E4M3 under a scale for each
-// token and head.
-enum KvStore : int { kKvBf16 = 0, kKvFp8Static = 1, kKvFp8Dynamic = 2 };
+// How a cache stores an element: bf16, E4M3 under one scale for all of k (of v), E4M3 under a scale for each token and
+// head, or E2M1 under an E4M3 scale for each 16 elements and one scale for all of k (of v).
+enum KvStore : int { kKvBf16 = 0, kKvFp8Static = 1, kKvFp8Dynamic = 2, kKvNvfp4 = 3 };
+
+// Bytes of a row, the scales of its blocks apart.
+constexpr int kv_row_bytes(int head_dim, int store) {
+    return store == kKvBf16 ? head_dim * 2 : (store == kKvNvfp4 ? head_dim / 2 : head_dim);
+}
 
 // A paged cache as the kernels see it. Token `slot` of a sequence lies in page table[seq][slot >> page_shift]; the
-// row of one head starts page * page_bytes + (head * page_size + slot % page_size) * row_bytes into k (and v);
-// scales, weights and positions are dense, [n_pages, n_kv_heads, page_size].
+// row of one head starts page * page_bytes + (head * page_size + slot % page_size) * row_bytes into k (and v); scales,
+// weights and positions are dense, [n_pages, n_kv_heads, page_size]. kKvNvfp4: the scales of a row's blocks, head_dim / 16
+// bytes, start page * page_bytes + block_offset + (head * page_size + slot % page_size) * head_dim / 16 into k (and v).
 struct KvView {
     void* k;
     void* v;
@@ -24,6 +30,7 @@ struct KvView {
     float* weight;
     int32_t* position;
     int64_t page_bytes;
+    int64_t block_offset;
     int64_t n_pages;
     const int32_t* table;   // [n_seqs, pages_per_seq]
     int64_t pages_per_seq;
@@ -90,15 +97,17 @@ struct AttendPlan {
 void plan_kv_attend(int head_dim, int store, int group, int sms, int64_t capacity, int64_t rows, AttendPlan* plan);
 
 cudaError_t launch_kv_append(const AppendParams& p, int sms, cudaStream_t s);
-cudaError_t launch_kv_attend(const AttendParams& p, cudaStream_t s);   // any store; the other two: their own
+cudaError_t launch_kv_attend(const AttendParams& p, cudaStream_t s);   // any store; the others: their own
 cudaError_t launch_kv_attend_fp8(const AttendParams& p, cudaStream_t s);
 cudaError_t launch_kv_attend_fp8_dynamic(const AttendParams& p, cudaStream_t s);
+cudaError_t launch_kv_attend_nvfp4(const AttendParams& p, cudaStream_t s);
 cudaError_t launch_kv_weights(const AttendParams& p, cudaStream_t s);
 cudaError_t launch_kv_evict(const EvictParams& p, cudaStream_t s);
 cudaError_t device_error_flags_kv_cache(unsigned int* flags, bool clear);
 cudaError_t device_error_flags_kv_attention(unsigned int* flags, bool clear);
 cudaError_t device_error_flags_kv_attention_fp8(unsigned int* flags, bool clear);
 cudaError_t device_error_flags_kv_attention_fp8_dynamic(unsigned int* flags, bool clear);
+cudaError_t device_error_flags_kv_attention_nvfp4(unsigned int* flags, bool clear);
 
 // What the C-ABI layer keeps for every entry point (api.cu): the SM count of the current device, and the status of
 // a launch (counts it, or keeps its cudaError_t).

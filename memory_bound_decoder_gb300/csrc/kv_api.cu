@@ -27,12 +27,24 @@ int log2_of(int64_t x) {
 
 int store_of(const mbd_kv_cache* c) {
     if (c->format == MBD_KV_BF16) return mbd::kKvBf16;
+    if (c->format == MBD_KV_NVFP4) return mbd::kKvNvfp4;
     return c->mode == MBD_SCALE_DYNAMIC_PER_TOKEN ? mbd::kKvFp8Dynamic : mbd::kKvFp8Static;
+}
+
+// Bytes of `elements` of a page (NVFP4: codes and block scales; whole blocks), and of a dense page: a multiple of 16.
+uint64_t page_bytes(const mbd_kv_cache* c, uint64_t elements) {
+    return c->format == MBD_KV_BF16 ? elements * 2 : (c->format == MBD_KV_NVFP4 ? elements / 16 * 9 : elements);
+}
+
+uint64_t dense_page_bytes(const mbd_kv_cache* c) {
+    return (page_bytes(c, uint64_t(c->n_kv_heads) * c->page_size * c->head_dim) + 15) / 16 * 16;
 }
 
 // Sizes and kinds (pointers apart), and the table's extent. They are checked for empty calls too.
 mbd_status check_shape(const mbd_kv_cache* c, int64_t pages_per_seq, int64_t n_seqs) {
-    if (!c || c->reserved != 0 || (c->format != MBD_KV_BF16 && c->format != MBD_KV_FP8)) return MBD_ERR_INVALID_ARG;
+    if (!c || c->reserved != 0 || (c->format != MBD_KV_BF16 && c->format != MBD_KV_FP8 && c->format != MBD_KV_NVFP4))
+        return MBD_ERR_INVALID_ARG;
+    if (c->format == MBD_KV_NVFP4 && c->mode != MBD_SCALE_STATIC_PER_TENSOR) return MBD_ERR_INVALID_ARG;
     if (c->format == MBD_KV_FP8 && c->mode != MBD_SCALE_STATIC_PER_TENSOR && c->mode != MBD_SCALE_DYNAMIC_PER_TOKEN)
         return MBD_ERR_INVALID_ARG;
     if (c->n_pages <= 0 || c->page_size <= 0 || c->n_kv_heads <= 0 || c->head_dim <= 0 || c->page_stride < 0 ||
@@ -45,7 +57,10 @@ mbd_status check_shape(const mbd_kv_cache* c, int64_t pages_per_seq, int64_t n_s
         return MBD_ERR_UNSUPPORTED;
     const int64_t dense = int64_t{c->n_kv_heads} * c->page_size * c->head_dim;
     const int size = c->format == MBD_KV_BF16 ? 2 : 1;
-    if (c->page_stride != 0) {
+    if (c->page_stride != 0 && c->format == MBD_KV_NVFP4) {   // in bytes
+        if (c->page_stride < static_cast<int64_t>(page_bytes(c, uint64_t(dense)))) return MBD_ERR_INVALID_ARG;
+        if (c->page_stride % 16 != 0) return MBD_ERR_MISALIGNED;
+    } else if (c->page_stride != 0) {
         if (c->page_stride < dense) return MBD_ERR_INVALID_ARG;
         if (c->page_stride * size % 16 != 0) return MBD_ERR_MISALIGNED;
     }
@@ -56,20 +71,20 @@ mbd_status check_shape(const mbd_kv_cache* c, int64_t pages_per_seq, int64_t n_s
 
 // The pointers of a cache whose shape has been checked.
 mbd_status check_cache(const mbd_kv_cache* c, const int32_t* page_table, int64_t pages_per_seq, Cache* out) {
-    const bool fp8 = c->format == MBD_KV_FP8, dynamic = fp8 && c->mode == MBD_SCALE_DYNAMIC_PER_TOKEN;
-    const uint64_t size = fp8 ? 1 : 2;
-    if (!c->k || !c->v || !page_table || (fp8 && (!c->k_scale || !c->v_scale))) return MBD_ERR_INVALID_ARG;
+    const bool scaled = c->format != MBD_KV_BF16, dynamic = c->format == MBD_KV_FP8 && c->mode == MBD_SCALE_DYNAMIC_PER_TOKEN;
+    const uint64_t size = c->format == MBD_KV_BF16 ? 2 : 1;   // of page_stride's units
+    if (!c->k || !c->v || !page_table || (scaled && (!c->k_scale || !c->v_scale))) return MBD_ERR_INVALID_ARG;
     if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(page_table, 4) || !aligned(c->weight, 4) ||
-        !aligned(c->position, 4) || (fp8 && (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))))
+        !aligned(c->position, 4) || (scaled && (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))))
         return MBD_ERR_MISALIGNED;
-    const uint64_t dense = uint64_t(c->n_kv_heads) * c->page_size * c->head_dim * size;
+    const uint64_t dense = dense_page_bytes(c);
     const uint64_t stride = c->page_stride ? uint64_t(c->page_stride) * size : dense;
     const uint64_t pool = uint64_t(c->n_pages - 1) * stride + dense;
     const uint64_t meta = uint64_t(c->n_pages) * c->n_kv_heads * c->page_size * 4, scales = dynamic ? meta : 4;
     out->k = {c->k, pool};
     out->v = {c->v, pool};
-    out->k_scale = {fp8 ? c->k_scale : nullptr, scales};
-    out->v_scale = {fp8 ? c->v_scale : nullptr, scales};
+    out->k_scale = {scaled ? c->k_scale : nullptr, scales};
+    out->v_scale = {scaled ? c->v_scale : nullptr, scales};
     out->weight = {c->weight, meta};
     out->position = {c->position, meta};
     if (overlap(out->k, out->v)) {   // allowed where the pages of one lie between the pages of the other
@@ -91,6 +106,7 @@ mbd_status check_cache(const mbd_kv_cache* c, const int32_t* page_table, int64_t
     v.weight = c->weight;
     v.position = c->position;
     v.page_bytes = static_cast<int64_t>(stride);
+    v.block_offset = int64_t{c->n_kv_heads} * c->page_size * c->head_dim / 2;
     v.n_pages = c->n_pages;
     v.table = page_table;
     v.pages_per_seq = pages_per_seq;

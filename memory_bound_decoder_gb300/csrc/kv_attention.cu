@@ -88,7 +88,7 @@ void plan_kv_attend(int head_dim, int store, int group, int sms, int64_t capacit
     // accumulators would not fit the registers), in chunks of 16 (8).
     plan->chunk_heads = group > 8 && head_dim < 256 ? 16 : 8;
     plan->chunks = (group + plan->chunk_heads - 1) / plan->chunk_heads;
-    const int64_t tile = int64_t{step_keys(head_dim, store)} * kWarps;
+    const int64_t tile = int64_t{step_keys(head_dim, store, plan->chunk_heads / 8)} * kWarps;
     // CTAs that are resident at once, no more than there can be tiles.
     const int64_t resident = int64_t{sms} * resident_ctas(head_dim, store, plan->chunk_heads / 8);
     const int64_t items = rows * plan->chunks;
@@ -102,6 +102,7 @@ cudaError_t launch_kv_attend(const AttendParams& p, cudaStream_t s) {
         case kKvBf16: return launch_store<kKvBf16>(p, s);
         case kKvFp8Static: return launch_kv_attend_fp8(p, s);
         case kKvFp8Dynamic: return launch_kv_attend_fp8_dynamic(p, s);
+        case kKvNvfp4: return launch_kv_attend_nvfp4(p, s);
     }
     return cudaErrorInvalidValue;
 }

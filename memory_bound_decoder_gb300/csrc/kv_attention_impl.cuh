@@ -71,6 +71,19 @@ __device__ __forceinline__ uint4 ld16(const char* p) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
     return v;
 }
+__device__ __forceinline__ uint32_t ld4(const char* p) {
+    uint32_t v;
+    asm volatile("ld.global.L1::no_allocate.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+// N bytes (1 or 2) of the scales of blocks, in the low ones of a word.
+template <int N>
+__device__ __forceinline__ uint32_t ld_blocks(const char* p) {
+    unsigned short v;
+    if constexpr (N == 1) asm volatile("ld.global.u8 %0, [%1];" : "=h"(v) : "l"(p) : "memory");
+    else asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p) : "memory");
+    return v;
+}
 __device__ __forceinline__ uint2 ld8(const char* p) {
     uint2 v;
     asm volatile("ld.global.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
@@ -105,30 +118,55 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
     return h;
 }
 
+// Four pairs of E2M1 codes, one a byte (the low bits first), to f16, exact.
+__device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n\t.reg .b8 q0, q1, q2, q3;\n\t"
+        "mov.b32 {q0, q1, q2, q3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, q0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, q1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, q2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, q3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 
-// Keys of a warp's step.
-constexpr int step_keys(int d, int store) {
-    const int row = d * (store == kKvBf16 ? 2 : 1);
-    return row >= 256 ? 16 : 16 * 256 / row;
+// Keys of a warp's step, with nt 8-column operands: 4 KB of K and of V where rows are at most 256 bytes, as many as the
+// registers hold besides their logits.
+constexpr int step_keys(int d, int store, int nt) {
+    const int row = kv_row_bytes(d, store), keys = row >= 256 ? 16 : 16 * 256 / row;
+    const int most = nt == 2 && d == 128 ? 32 : 64;
+    return keys > most ? most : keys;
 }
 
-// What a (D, STORE) variant loads and holds. A step is 16 NG keys of one warp, 4 KB of K and of V where rows are at
-// most 256 bytes.
-template <int D, int STORE>
+// What a (D, STORE, NT) variant loads and holds. A step is 16 NG keys of one warp.
+template <int D, int STORE, int NT>
 struct Shape {
-    static constexpr bool kF8 = STORE != kKvBf16;
-    static constexpr int kRow = D * (kF8 ? 1 : 2);           // bytes of a row
-    static constexpr int kKv = kRow / 64;                    // 16-byte vectors of a K row in one lane (4 lanes a row)
-    static constexpr int kVb = kRow / 8 < 16 ? 8 : 16;       // bytes of a vector of V (8 lanes a row)
+    static constexpr bool kF4 = STORE == kKvNvfp4;
+    static constexpr bool kF8 = STORE != kKvBf16;            // products in f16
+    static constexpr int kRow = kv_row_bytes(D, STORE);      // bytes of a row
+    static constexpr int kKb = kRow / 4 < 16 ? 8 : 16;       // bytes of a vector of K (4 lanes a row)
+    static constexpr int kKv = kRow / 4 / kKb;               // of them in one lane
+    static constexpr int kKw = kKb / 4;                      // words of one
+    static constexpr int kKd = kKb * D / kRow;               // elements of one
+    static constexpr int kVb = kRow / 8 < 16 ? kRow / 8 : 16;   // bytes of a vector of V (8 lanes a row)
     static constexpr int kVv = kRow / 8 / kVb;               // of them in one lane
     static constexpr int kVw = kVb / 4;                      // words of one
-    static constexpr int kVd = kVb / (kF8 ? 1 : 2);          // elements of one
-    static constexpr int kStep = step_keys(D, STORE);
+    static constexpr int kVd = kVb * D / kRow;               // elements of one
+    static constexpr int kKs = kF4 ? kKd / 16 : 1;           // blocks of a vector of K, and of V (at least one)
+    static constexpr int kVs = kF4 && kVd > 16 ? kVd / 16 : 1;
+    static constexpr int kStep = step_keys(D, STORE, NT);
     static constexpr int kGroups = kStep / 16;
     static constexpr int kTile = kStep * kWarps;
     static constexpr int kK = D / 16;                        // k-steps of S^T, m-tiles of O^T
@@ -250,7 +288,10 @@ struct MergeSmem {
 template <int D, int STORE>
 __device__ __forceinline__ void write_out(const AttendParams& p, int64_t head, int dim, const float4& acc, float m, float t,
                                           float mo) {
-    const float one = STORE == kKvFp8Dynamic ? ex2(mo - m) : (STORE == kKvFp8Static ? *p.c.v_scale : 1.0f);
+    const float one = STORE == kKvFp8Dynamic  ? ex2(mo - m)
+                      : STORE == kKvFp8Static ? *p.c.v_scale
+                      : STORE == kKvNvfp4     ? nvfp4_tensor_scale_of(*p.c.v_scale)
+                                              : 1.0f;
     const float f = mo == -INFINITY || t == 0.0f ? 0.0f : one / t;   // (t == 0: every logit is -inf)
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + head * D + dim) =
         make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
@@ -351,8 +392,8 @@ __device__ __forceinline__ void join_two(const AttendParams& p, const Cut& cut, 
 template <int D, int STORE, int NT, int GRAN>
 __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
     kv_attend_kernel(const __grid_constant__ AttendParams p) {
-    using S = Shape<D, STORE>;
-    constexpr bool kF8 = S::kF8, kDyn = STORE == kKvFp8Dynamic;
+    using S = Shape<D, STORE, NT>;
+    constexpr bool kF8 = S::kF8, kF4 = S::kF4, kDyn = STORE == kKvFp8Dynamic;
     constexpr bool SMALL = GRAN == 1;
     constexpr int H = GRAN == 8 ? 2 : 1;   // lookups of a group
     constexpr int HT = 8 * NT, NG = S::kGroups, KV = S::kKv, VV = S::kVv, VW = S::kVw, KK = S::kK;
@@ -450,14 +491,20 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
         }
     }
     if (unit >= end) return;
-    const float k_static = STORE == kKvFp8Static ? *p.c.k_scale : 1.0f;
+    const float k_static = STORE == kKvFp8Static ? *p.c.k_scale : (kF4 ? nvfp4_tensor_scale_of(*p.c.k_scale) : 1.0f);
     // This lane's places in a step whose first row is row 0 of the pools: keys r and r + 8 of K; 2c, 2c + 1 and these
     // plus 8 of V.
-    const char* k_lane = static_cast<const char*>(p.c.k) + (SMALL ? 0 : r * S::kRow) + c * 16;
+    const char* k_lane = static_cast<const char*>(p.c.k) + (SMALL ? 0 : r * S::kRow) + c * S::kKb;
     const char* v_lane = static_cast<const char*>(p.c.v) + (SMALL ? 0 : 2 * c * S::kRow) + r * S::kVb;
+    // The same of the blocks' scales: those of this lane's elements.
+    constexpr int kBlocks = D / 16;
+    const char* kb_lane = static_cast<const char*>(p.c.k) + (SMALL ? 0 : r * kBlocks) + c * S::kKs;
+    const char* vb_lane = static_cast<const char*>(p.c.v) + (SMALL ? 0 : 2 * c * kBlocks) + r * S::kVd / 16;
 
-    uint4 kx[NG][2][KV];
+    uint32_t kx[NG][2][KV][S::kKw];
     uint32_t vx[NG][4][VV][VW];
+    uint32_t kb[NG][2][KV], vb[NG][4][VV];   // NVFP4: scales of their blocks
+    int64_t block[NG][H];                  // NVFP4: byte offset of those of the group's (half's) first row, as `row`
     uint32_t q[NT][KK][2];
     float ks[NG][2], vs[NG][2];            // dynamic scales of the keys r and r + 8: k's, and log2 of v's
     float ks_next[NG][2], vs_next[NG][2];
@@ -487,7 +534,9 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
             for (int h = 0; h < H; ++h) {
                 const bool good = on_pool(page[g][h]);
                 full_next &= SMALL ? __all_sync(0xffffffffu, good) : good;
-                row[g][h] = kv_row(p.c, good ? page[g][h] : 0, cur.head, step + g * 16 + h * 8 + (SMALL ? lane & 15 : 0), S::kRow);
+                const int key = step + g * 16 + h * 8 + (SMALL ? lane & 15 : 0);
+                row[g][h] = kv_row(p.c, good ? page[g][h] : 0, cur.head, key, S::kRow);
+                if constexpr (kF4) block[g][h] = kv_blocks(p.c, good ? page[g][h] : 0, cur.head, key);
             }
 #pragma unroll
         for (int g = 0; g < NG; ++g) live_next[g] = 0xffffu;
@@ -529,16 +578,34 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
         if (SMALL) return __shfl_sync(0xffffffffu, row[g][0], at);
         return row[g][H == 2 ? rows / 8 : 0] + (H == 2 ? rows % 8 : rows) * S::kRow;
     };
+    auto block_offset = [&](int g, int at, int rows) {
+        if (SMALL) return __shfl_sync(0xffffffffu, block[g][0], at);
+        return block[g][H == 2 ? rows / 8 : 0] + (H == 2 ? rows % 8 : rows) * kBlocks;
+    };
+    auto load_k_row = [&](int g, int i, const char* at, const char* blocks) {
+#pragma unroll
+        for (int j = 0; j < KV; ++j) {
+            if constexpr (S::kKw == 4) {
+                const uint4 x = ld16(at + j * 64);
+                kx[g][i][j][0] = x.x;
+                kx[g][i][j][1] = x.y;
+                kx[g][i][j][2] = x.z;
+                kx[g][i][j][3] = x.w;
+            } else {
+                const uint2 x = ld8(at + j * 32);
+                kx[g][i][j][0] = x.x;
+                kx[g][i][j][1] = x.y;
+            }
+            if constexpr (kF4) kb[g][i][j] = ld_blocks<S::kKs>(blocks + j * 4 * S::kKs);
+        }
+    };
     auto load_k = [&] {
         if (full_next) {
 #pragma unroll
             for (int g = 0; g < NG; ++g)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const char* at = k_lane + offset(g, r + 8 * i, 8 * i);
-#pragma unroll
-                    for (int j = 0; j < KV; ++j) kx[g][i][j] = ld16(at + j * 64);
-                }
+                for (int i = 0; i < 2; ++i)
+                    load_k_row(g, i, k_lane + offset(g, r + 8 * i, 8 * i), kF4 ? kb_lane + block_offset(g, r + 8 * i, 8 * i) : nullptr);
             return;
         }
 #pragma unroll
@@ -546,12 +613,17 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const char* at = k_lane + offset(g, r + 8 * i, 8 * i);
-                const bool in = (live_next[g] >> (r + 8 * i)) & 1u;
+                const char* blocks = kF4 ? kb_lane + block_offset(g, r + 8 * i, 8 * i) : nullptr;
 #pragma unroll
-                for (int j = 0; j < KV; ++j) kx[g][i][j] = in ? ld16(at + j * 64) : make_uint4(0, 0, 0, 0);
+                for (int j = 0; j < KV; ++j) {
+#pragma unroll
+                    for (int w = 0; w < S::kKw; ++w) kx[g][i][j][w] = 0;
+                    kb[g][i][j] = 0;
+                }
+                if ((live_next[g] >> (r + 8 * i)) & 1u) load_k_row(g, i, at, blocks);
             }
     };
-    auto load_v_row = [&](int g, int i, const char* from) {
+    auto load_v_row = [&](int g, int i, const char* from, const char* blocks) {
 #pragma unroll
         for (int j = 0; j < VV; ++j) {
             if constexpr (VW == 4) {
@@ -560,11 +632,14 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
                 vx[g][i][j][1] = x.y;
                 vx[g][i][j][2] = x.z;
                 vx[g][i][j][3] = x.w;
-            } else {
+            } else if constexpr (VW == 2) {
                 const uint2 x = ld8(from + j * 8 * S::kVb);
                 vx[g][i][j][0] = x.x;
                 vx[g][i][j][1] = x.y;
+            } else {
+                vx[g][i][j][0] = ld4(from + j * 8 * S::kVb);
             }
+            if constexpr (kF4) vb[g][i][j] = ld_blocks<S::kVs>(blocks + j * 8 * S::kVd / 16);
         }
     };
     auto load_v = [&] {
@@ -574,7 +649,8 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     constexpr int kRows[4] = {0, 1, 8, 9};
-                    load_v_row(g, i, v_lane + offset(g, 2 * c + kRows[i], kRows[i]));
+                    load_v_row(g, i, v_lane + offset(g, 2 * c + kRows[i], kRows[i]),
+                               kF4 ? vb_lane + block_offset(g, 2 * c + kRows[i], kRows[i]) : nullptr);
                 }
             return;
         }
@@ -584,14 +660,17 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
             for (int i = 0; i < 4; ++i) {
                 constexpr int kRows[4] = {0, 1, 8, 9};
                 const char* from = v_lane + offset(g, 2 * c + kRows[i], kRows[i]);
+                const char* blocks = kF4 ? vb_lane + block_offset(g, 2 * c + kRows[i], kRows[i]) : nullptr;
 #pragma unroll
-                for (int j = 0; j < VV; ++j)
+                for (int j = 0; j < VV; ++j) {
 #pragma unroll
                     for (int w = 0; w < VW; ++w) vx[g][i][j][w] = 0;
-                if ((live_next[g] >> (2 * c + kRows[i])) & 1u) load_v_row(g, i, from);
+                    vb[g][i][j] = 0;
+                }
+                if ((live_next[g] >> (2 * c + kRows[i])) & 1u) load_v_row(g, i, from, blocks);
             }
     };
-    // Query heads of the chunk, lane r's: bf16 in the order of K's vectors (E4M3: 16 elements a vector).
+    // Query heads of the chunk, lane r's: bf16 in the order of K's vectors (E4M3: 16 elements a vector; E2M1: 32, or 16).
     auto load_q = [&] {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -600,7 +679,8 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
                                (static_cast<int64_t>(cur.head) * p.group + h) * D * 2;
 #pragma unroll
             for (int j = 0; j < KK / 2; ++j) {
-                const int vec = kF8 ? ((j >> 1) * 4 + c) * 2 + (j & 1) : j * 4 + c;
+                constexpr int per = S::kKd / 8;   // of q's vectors to one of K's
+                const int vec = (j / per * 4 + c) * per + j % per;
                 uint4 x = make_uint4(0, 0, 0, 0);
                 if (h < p.group) x = ld16(from + vec * 16);
                 q[nt][2 * j][0] = x.x;
@@ -720,9 +800,27 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
         for (int j = 0; j < KV; ++j)
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                const uint32_t a[4] = {kx[g][0][j].x, kx[g][0][j].y, kx[g][0][j].z, kx[g][0][j].w};
-                const uint32_t b[4] = {kx[g][1][j].x, kx[g][1][j].y, kx[g][1][j].z, kx[g][1][j].w};
-                if constexpr (kF8) {
+                const auto &a = kx[g][0][j], &b = kx[g][1][j];
+                if constexpr (kF4) {
+                    // Values of a block: codes times its scale, exact in f16 (2 and 4 significant bits, 2^-10 .. 2688).
+                    const uint32_t sa = e4m3x2_to_f16x2(kb[g][0][j]), sb = e4m3x2_to_f16x2(kb[g][1][j]);
+#pragma unroll
+                    for (int i = 0; i < S::kKw; ++i) {
+                        const uint32_t fa = __byte_perm(sa, sa, i < 2 ? 0x1010 : 0x3232), fb = __byte_perm(sb, sb, i < 2 ? 0x1010 : 0x3232);
+                        uint32_t x[4], y[4];
+                        e2m1x8_to_f16x2(a[i], x);
+                        e2m1x8_to_f16x2(b[i], y);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const uint32_t a0 = mul_f16x2(x[2 * half], fa), a2 = mul_f16x2(x[2 * half + 1], fa);
+                            const uint32_t a1 = mul_f16x2(y[2 * half], fb), a3 = mul_f16x2(y[2 * half + 1], fb);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma<true>(s[g][nt], a0, a1, a2, a3, q[nt][(j * S::kKw + i) * 2 + half][0],
+                                          q[nt][(j * S::kKw + i) * 2 + half][1]);
+                        }
+                    }
+                } else if constexpr (kF8) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t a0 = e4m3x2_to_f16x2(a[i]), a2 = e4m3x2_to_f16x2(a[i] >> 16);
@@ -857,7 +955,28 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
 #pragma unroll
                 for (int i = 0; i < VW; ++i) {
                     const uint32_t w0 = vx[g][0][j][i], w1 = vx[g][1][j][i], w2 = vx[g][2][j][i], w3 = vx[g][3][j][i];
-                    if constexpr (kF8) {
+                    if constexpr (kF4) {
+                        // A byte for each element: its codes of two keys, whose scales make the other factor.
+                        constexpr uint32_t kLow = 0x0f0f0f0fu;
+                        const uint32_t even01 = (w0 & kLow) | ((w1 & kLow) << 4), odd01 = ((w0 >> 4) & kLow) | (w1 & ~kLow);
+                        const uint32_t even23 = (w2 & kLow) | ((w3 & kLow) << 4), odd23 = ((w2 >> 4) & kLow) | (w3 & ~kLow);
+                        const int at = S::kVs == 2 && i >= VW / 2 ? 1 : 0;   // the word's block of the vector
+                        const uint32_t f01 = e4m3x2_to_f16x2(__byte_perm(vb[g][0][j], vb[g][1][j], at ? 0x0051 : 0x0040));
+                        const uint32_t f23 = e4m3x2_to_f16x2(__byte_perm(vb[g][2][j], vb[g][3][j], at ? 0x0051 : 0x0040));
+                        uint32_t x0[4], x1[4], x2[4], x3[4];
+                        e2m1x8_to_f16x2(even01, x0);
+                        e2m1x8_to_f16x2(odd01, x1);
+                        e2m1x8_to_f16x2(even23, x2);
+                        e2m1x8_to_f16x2(odd23, x3);
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            const uint32_t a0 = mul_f16x2(x0[m], f01), a1 = mul_f16x2(x1[m], f01);
+                            const uint32_t a2 = mul_f16x2(x2[m], f23), a3 = mul_f16x2(x3[m], f23);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma<true>(o[nt][(j * VW + i) * 4 + m], a0, a1, a2, a3, hi[nt][0], hi[nt][1]);
+                        }
+                    } else if constexpr (kF8) {
 #pragma unroll
                         for (int half = 0; half < 2; ++half) {
                             const uint32_t a = __byte_perm(w0, w1, half ? 0x7362 : 0x5140);

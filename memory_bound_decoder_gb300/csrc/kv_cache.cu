@@ -100,6 +100,26 @@ __device__ __forceinline__ uint2 encode(const uint4& x, const Divisor& s) {
     return make_uint2(pack_e4m3x4(d[0], d[1]), pack_e4m3x4(d[2], d[3]));
 }
 
+// Half of a block of 16 bf16 values, whose largest magnitude is amax, as E2M1 codes under the block's scale, whose E4M3 code goes to
+// *block. Quotients rounded to nearest, as above: values and scales are short numbers, so ties are common.
+__device__ __forceinline__ uint32_t encode_nvfp4(const uint4& x, float amax, float tensor_scale, uint32_t* block) {
+    *block = 0;
+    if (tensor_scale == 0.0f) return 0u;
+    *block = pack_e4m3x2(__fdiv_rn(amax, 6.0f * tensor_scale), 0.0f) & 0xffu;
+    if (*block == 0u) return 0u;
+    const Divisor s = divisor(e4m3_value(*block) * tensor_scale);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float2 d[4];
+    if (s.fast) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = quotient(bf16x2_to_float2(clamp_bf16x2(w[i], s)), s);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = make_float2(__fdiv_rn(bf16_lo(w[i]), s.scale), __fdiv_rn(bf16_hi(w[i]), s.scale));
+    }
+    return pack_e2m1x8(d[0], d[1], d[2], d[3]);
+}
+
 // Largest magnitude of eight bf16 values.
 __device__ __forceinline__ float amax(const uint4& x) {
     uint32_t m = max_bf16x2_bits(max_bf16x2_bits(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
@@ -111,9 +131,10 @@ template <int STORE, int LANES>   // LANES = head_dim / 8: the lanes that own on
 __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ AppendParams p,
                                                                    int tokens_per_cta, unsigned inverse) {
     // Of each token: the byte offset of head 0's row in the pools (-1: no slot), the index of its scale, the slot.
-    __shared__ int64_t s_row[kAppendMaxTokens], s_meta[kAppendMaxTokens];
+    // (NVFP4: and of its blocks' scales.)
+    __shared__ int64_t s_row[kAppendMaxTokens], s_meta[kAppendMaxTokens], s_blocks[STORE == kKvNvfp4 ? kAppendMaxTokens : 1];
     __shared__ int s_slot[kAppendMaxTokens];
-    constexpr int kRow = LANES * (STORE == kKvBf16 ? 16 : 8);
+    constexpr int kRow = kv_row_bytes(LANES * 8, STORE);
     pdl_trigger();
     pdl_wait();
     const int64_t first = static_cast<int64_t>(blockIdx.x) * tokens_per_cta;
@@ -150,6 +171,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
             }
             s_row[j] = page >= 0 ? kv_row(p.c, page, 0, slot, kRow) : -1;
             s_meta[j] = page >= 0 ? kv_meta(p.c, page, 0, slot) : 0;
+            if constexpr (STORE == kKvNvfp4) s_blocks[j] = page >= 0 ? kv_blocks(p.c, page, 0, slot) : 0;
             s_slot[j] = static_cast<int>(slot);
         }
     }
@@ -159,7 +181,12 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
         ks = divisor(*p.c.k_scale);
         vs = divisor(*p.c.v_scale);
     }
-    // Every thread stays in the loop until all are done: the dynamic scale shuffles.
+    float k_tensor = 0.0f, v_tensor = 0.0f;
+    if constexpr (STORE == kKvNvfp4) {
+        k_tensor = nvfp4_tensor_scale_of(*p.c.k_scale);
+        v_tensor = nvfp4_tensor_scale_of(*p.c.v_scale);
+    }
+    // Every thread stays in the loop until all are done: the dynamic scale and the blocks' scales shuffle.
     for (int base = 0; base < total; base += kAppendThreads * kBatch) {
         if (base > 0) load(base);
 #pragma unroll
@@ -174,6 +201,21 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
                 if (live) {
                     *reinterpret_cast<uint4*>(static_cast<char*>(p.c.k) + to) = k[u];
                     *reinterpret_cast<uint4*>(static_cast<char*>(p.c.v) + to) = v[u];
+                }
+            } else if constexpr (STORE == kKvNvfp4) {   // a lane has half of a block
+                float ka = amax(k[u]), va = amax(v[u]);
+                ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, 1));
+                va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, 1));
+                uint32_t kf, vf;
+                const uint32_t kq = encode_nvfp4(k[u], ka, k_tensor, &kf), vq = encode_nvfp4(v[u], va, v_tensor, &vf);
+                if (live) {
+                    *reinterpret_cast<uint32_t*>(static_cast<char*>(p.c.k) + to) = kq;
+                    *reinterpret_cast<uint32_t*>(static_cast<char*>(p.c.v) + to) = vq;
+                    if ((lane & 1) == 0) {
+                        const int64_t block = s_blocks[local] + (static_cast<int64_t>(head) << p.c.page_shift) * (LANES / 2) + lane / 2;
+                        static_cast<uint8_t*>(p.c.k)[block] = static_cast<uint8_t>(kf);
+                        static_cast<uint8_t*>(p.c.v)[block] = static_cast<uint8_t>(vf);
+                    }
                 }
             } else {
                 if constexpr (STORE == kKvFp8Dynamic) {
@@ -457,8 +499,8 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const __grid
     cluster.sync();   // the lists are complete; no CTA touches another's shared memory from here on
     const int mine = min(static_cast<int>(chunk), static_cast<int>(moves) - rank * static_cast<int>(chunk));
     if (mine <= 0) return;
-    const int row_bytes = p.c.head_dim * (p.c.store == kKvBf16 ? 2 : 1);
-    const int lanes = row_bytes / 16, part = tid % lanes, groups = kEvictThreads / lanes;   // 4 to 32 lanes own a row
+    const int row_bytes = kv_row_bytes(p.c.head_dim, p.c.store);
+    const int lanes = row_bytes / 16, part = tid % lanes, groups = kEvictThreads / lanes;   // 2 to 32 lanes own a row
     // Weights, positions and scales, a thread for a row: neighbours in the lists are neighbours in the cache, and share
     // sectors. (With the row's own lanes, one word each, they took longer than k and v: 26 of 58 thousand cycles at
     // 1546 rows of 128 bytes a CTA.)
@@ -472,6 +514,16 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const __grid
         if (p.c.store == kKvFp8Dynamic) {
             ks = p.c.k_scale[a];
             vs = p.c.v_scale[a];
+        }
+        if (p.c.store == kKvNvfp4) {   // the scales of the row's blocks: 4, 8 or 16 bytes of k and of v
+            const int64_t from = kv_blocks(p.c, move.y >> p.c.page_shift, head, move.y);
+            const int64_t to = kv_blocks(p.c, move.x >> p.c.page_shift, head, move.x);
+            for (int64_t j = 0; j < p.c.head_dim / 16; j += 4) {
+                const uint32_t kf = *reinterpret_cast<const uint32_t*>(static_cast<const char*>(p.c.k) + from + j);
+                const uint32_t vf = *reinterpret_cast<const uint32_t*>(static_cast<const char*>(p.c.v) + from + j);
+                *reinterpret_cast<uint32_t*>(static_cast<char*>(p.c.k) + to + j) = kf;
+                *reinterpret_cast<uint32_t*>(static_cast<char*>(p.c.v) + to + j) = vf;
+            }
         }
         p.c.weight[b] = w;
         p.c.position[b] = at_position;
@@ -515,6 +567,7 @@ cudaError_t launch_kv_append(const AppendParams& p, int sms, cudaStream_t s) {
         case kKvBf16: return launch_append<kKvBf16>(p, grid, t, inverse, s);
         case kKvFp8Static: return launch_append<kKvFp8Static>(p, grid, t, inverse, s);
         case kKvFp8Dynamic: return launch_append<kKvFp8Dynamic>(p, grid, t, inverse, s);
+        case kKvNvfp4: return launch_append<kKvNvfp4>(p, grid, t, inverse, s);
     }
     return cudaErrorInvalidValue;
 }

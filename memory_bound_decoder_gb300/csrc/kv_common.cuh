@@ -29,6 +29,11 @@ __device__ __forceinline__ int64_t kv_meta(const KvView& c, int64_t page, int he
     return ((page * c.n_kv_heads + head) << c.page_shift) + at;
 }
 
+// Byte offset into k (and v) of the scales of a row's blocks.
+__device__ __forceinline__ int64_t kv_blocks(const KvView& c, int64_t page, int head, int64_t slot) {
+    return kv_row(c, page, head, slot, c.head_dim / 16) + c.block_offset;
+}
+
 // Length of a sequence as the kernels use it: within [0, capacity], anything else sets the error bit.
 __device__ __forceinline__ int64_t kv_len(const KvView& c, int32_t len) {
     if (len >= 0 && len <= c.capacity) return len;
