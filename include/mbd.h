@@ -15,7 +15,9 @@
  *   mbd_kv_cache_append, mbd_paged_attention_decode, mbd_kv_cache_evict
  *                                    the decode step's paged key-value cache: new tokens in, the attention of
  *                                    one new token per sequence over it, eviction by accumulated weight
- *   mbd_kv_cache_resize, mbd_rotary    the cache's pages and the new tokens' slots, handed out on the GPU; rotary positions
+ *   mbd_kv_cache_resize, mbd_rotary, mbd_prompt_attention
+ *                                    the cache's pages and the new tokens' slots, handed out on the GPU; rotary positions;
+ *                                    the causal attention of whole prompts
  *
  * Definitions (cited by page title and section):
  *   [TRT] "TensorRT-LLM: Compiling Inference Engines Ahead of Time", section "Fusing operations, measured":
@@ -625,6 +627,30 @@ mbd_status mbd_kv_cache_resize(int32_t* page_table, int64_t pages_per_seq, int64
                                int32_t* free_pages, int32_t* free_ends, int32_t* seq_lens, const int32_t* want_lens,
                                int64_t n_seqs, int32_t* cu_tokens, int32_t* positions, int64_t* slots, int64_t n_tokens,
                                int32_t* tokens_seen, mbd_stream_t stream);
+
+/*
+ * Causal attention of whole prompts, packed one behind the other: rows cu_tokens[b] .. cu_tokens[b + 1] - 1 are sequence b's
+ * tokens in order. Query head h reads key-value head h / (n_q_heads / n_kv_heads). Row i of a sequence sees its rows j <= i, with
+ * window > 0 the last `window` of them:
+ *     x_ij = scale * (q_i . k_j),   lse_i = log(sum_j exp(x_ij)),   out_i = bf16(sum_j exp(x_ij - lse_i) * v_j)
+ * A row whose logits are all -inf gives zeros and lse = -inf. A logit of NaN or +inf gives NaN. What lies in masked places (later
+ * tokens, tokens before the window, other sequences' rows) changes nothing, NaN and infinities among it; an infinite value in view
+ * gives an infinity (where its probability is above 2^-100: far below, the product with zero is NaN).
+ *   out       : [n_tokens, n_q_heads * head_dim] bf16, 16-byte aligned, written; rows from cu_tokens[n_seqs] on are left alone.
+ *   q         : n_tokens rows of n_q_heads * head_dim bf16, q_stride elements apart (0: dense); k, v: rows of n_kv_heads *
+ *               head_dim, kv_stride elements apart (0: dense): slices of the stacked projection need no copy.
+ *   cu_tokens : int32 [n_seqs + 1] on the device, ascending from 0 to at most n_tokens; equal neighbours are an empty sequence. A
+ *               sequence whose bounds are not (MBD_DEVERR_BAD_INDEX) is left out.
+ *   scale     : finite (also times log2(e)), usually 1 / sqrt(head_dim).   window: 0 (none) or the number of tokens in view.
+ *   lse       : fp32 [n_tokens, n_q_heads], written, or null.
+ * Logits, maxima and sums are fp32; exp(x_ij - lse_i) is rounded to bf16 for the product with v_j (off by 2^-8 of it). The
+ * result does not depend on what else runs, and equal calls give equal bits. head_dim: 64, 128 or 256. Limits: n_tokens and n_seqs
+ * <= MBD_KV_MAX_ROWS, n_q_heads <= 4096. n_tokens == 0 or n_seqs == 0 is a no-op. Bounded waits: see MBD_DEVERR_EXCHANGE_TIMEOUT.
+ */
+mbd_status mbd_prompt_attention(void* out, const void* q, int64_t q_stride, const void* k, const void* v, int64_t kv_stride,
+                                const int32_t* cu_tokens, int64_t n_seqs, int64_t n_tokens, int64_t n_q_heads,
+                                int64_t n_kv_heads, int64_t head_dim, float scale, int64_t window, float* lse,
+                                mbd_stream_t stream);
 
 /*
  * Rotary positions. Pair i (i < rotary_dim / 2) of each head is turned by t = position * f_i and stretched by the amplitude:

@@ -138,6 +138,7 @@ def _load() -> ctypes.CDLL:
     lib.mbd_kv_cache_evict.argtypes = [kvp, vp, vp, vp, i64, i64, i64, i64, vp]
     lib.mbd_step_abi_version.restype = cint
     lib.mbd_kv_cache_resize.argtypes = [vp, i64, i64, i64, vp, vp, vp, vp, i64, vp, vp, vp, i64, vp, vp]
+    lib.mbd_prompt_attention.argtypes = [vp, vp, i64, vp, vp, i64, vp, i64, i64, i64, i64, i64, f32, i64, vp, vp]
     lib.mbd_rotary.argtypes = [vp, i64, vp, i64, vp, f32, vp, i64, i64, i64, i64, cint, vp]
     lib.mbd_rotary_table.argtypes = [vp, ctypes.POINTER(f32), i64, ctypes.POINTER(RotaryScaling)]
     i32p = ctypes.POINTER(ctypes.c_int32)
@@ -148,7 +149,8 @@ def _load() -> ctypes.CDLL:
                "mbd_fused_add_rmsnorm_quant_nvfp4", "mbd_swiglu_quant_nvfp4", "mbd_run_program",
                "mbd_run_independent", "mbd_run_independent_with_program", "mbd_program_plan_build", "mbd_program_plan_launch", "mbd_program_plan_upload",
                "mbd_program_plan_launch_uploaded", "mbd_program_plan_launch_static", "mbd_kv_cache_append",
-               "mbd_paged_attention_decode", "mbd_kv_cache_evict", "mbd_kv_cache_resize", "mbd_rotary", "mbd_rotary_table"):
+               "mbd_paged_attention_decode", "mbd_kv_cache_evict", "mbd_kv_cache_resize", "mbd_rotary", "mbd_rotary_table",
+               "mbd_prompt_attention"):
         getattr(lib, fn).restype = cint
     return lib
 
@@ -366,6 +368,15 @@ def kv_cache_resize(page_table, pages_per_seq: int, page_size: int, n_pages: int
                                          _ptr(free_pages), _ptr(free_ends), _ptr(seq_lens), _ptr(want_lens), int(n_seqs),
                                          _ptr(cu_tokens), _ptr(positions), _ptr(slots), int(n_tokens), _ptr(tokens_seen),
                                          _stream(stream)), "kv_cache_resize")
+
+
+def prompt_attention(out, q, q_stride: int, k, v, kv_stride: int, cu_tokens, n_seqs: int, n_tokens: int, n_q_heads: int,
+                     n_kv_heads: int, head_dim: int, scale: float, window: int = 0, lse=None, stream=None) -> None:
+    """Causal attention of whole prompts, packed one behind the other (mbd_prompt_attention)."""
+    _check(get_lib().mbd_prompt_attention(_ptr(out), _ptr(q), int(q_stride), _ptr(k), _ptr(v), int(kv_stride),
+                                          _ptr(cu_tokens), int(n_seqs), int(n_tokens), int(n_q_heads), int(n_kv_heads),
+                                          int(head_dim), float(scale), int(window), _ptr(lse), _stream(stream)),
+           "prompt_attention")
 
 
 def rotary_table(rotary_dim: int, base: float = 10000.0, scaling="none", factor: float = 1.0, original: float = 0.0,

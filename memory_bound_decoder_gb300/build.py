@@ -20,7 +20,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libmbd.so")
 SOURCES = ["api.cu", "norm.cu", "swiglu.cu", "program.cu", "selftest.cu", "kv_api.cu", "kv_cache.cu",
            "kv_attention.cu", "kv_attention_fp8.cu", "kv_attention_fp8_dynamic.cu", "kv_attention_nvfp4.cu",
-           "kv_pages.cu", "step_api.cu", "rotary.cu"]
+           "kv_pages.cu", "step_api.cu", "rotary.cu", "prompt_attention.cu"]
 HEADERS = ["common.cuh", "launch.h", "norm_impl.cuh", "swiglu_impl.cuh", "kv.h", "kv_common.cuh",
            "kv_attention_impl.cuh", "checks.h", "step.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -928,7 +928,8 @@ mbd_status mbd_device_error_flags(uint32_t* flags, int clear) {
     unsigned int kv = 0;
     for (auto read : {mbd::device_error_flags_kv_cache, mbd::device_error_flags_kv_attention,
                       mbd::device_error_flags_kv_attention_fp8, mbd::device_error_flags_kv_attention_fp8_dynamic,
-                      mbd::device_error_flags_kv_attention_nvfp4, mbd::device_error_flags_kv_pages}) {
+                      mbd::device_error_flags_kv_attention_nvfp4, mbd::device_error_flags_kv_pages,
+                      mbd::device_error_flags_prompt}) {
         unsigned int f = 0;
         if (e == cudaSuccess) e = read(&f, clear != 0);
         kv |= f;

@@ -1,0 +1,605 @@
+// Causal attention of whole prompts, packed one behind the other.
+//
+// For query row i of a sequence, with the keys j in view (j <= i, and with a window the last `window` of them):
+//     x_ij = scale * q_i . k_j,  lse_i = log sum_j exp(x_ij),  out_i = sum_j exp(x_ij - lse_i) v_j
+//
+// Bound by the tensor cores: 4 D operations for each query head and pair in view, on tcgen05 with accumulators in TMEM. A CTA
+// works on two tiles of 128 query rows at a time, of two query heads of one group (or, where a group is odd, of two
+// neighbouring row tiles of one head), against blocks of 128 keys that both tiles use:
+//   - one thread brings Q, K and V into shared memory by TMA, in rows of 128 swizzled bytes;
+//   - one thread issues S = Q K^T (both operands from shared memory) and O += P V (P from TMEM, V as it lies, its keys along
+//     the contraction), for the two tiles in turn;
+//   - a warpgroup for each tile, a thread for each row, takes S out of TMEM, keeps the row's running maximum and sum in its
+//     registers, and puts P = exp2(S - maximum), rounded to bf16, back over S.
+// While one tile's softmax runs, the tensor cores have the other tile's two products to do. The maximum that a row's sums are
+// relative to is kept until a logit exceeds it by 2^8, so O is rescaled in the first blocks and hardly ever after them.
+//
+// P in bf16 is the operands' type (V is bf16, and both must agree); it is off by 2^-8 of itself, as the output's rounding is,
+// and adds up over a row's keys as a random walk does. Sums of P are kept in fp32 from the values before rounding.
+//
+// Values in masked places. A masked P is 0, and 0 times an infinite or NaN value would be NaN. So in blocks that hold masked
+// places (the diagonal, the window's edge; rows behind the sequence's end are masked by causality) the warpgroup looks at V
+// first, and where it holds such a value adds that block's product itself, over the keys in view alone.
+//
+// Every wait is bounded: one that runs out sets the error bit, and all roles leave.
+#include <cuda.h>
+
+#include "kv_common.cuh"
+#include "step.h"
+
+namespace mbd {
+
+namespace {
+
+constexpr int kRows = 128;       // query rows of a tile, keys of a block
+constexpr float kLazy = 8.0f;    // units of log2 that a logit may exceed the kept maximum by
+constexpr float kLn2 = 0.693147180559945309f;
+
+template <int D>
+struct Prompt {
+    static constexpr int kTiles = D <= 128 ? 2 : 1;   // (TMEM: 128 columns of S and D of O for each)
+    static constexpr int kThreads = kTiles * 128 + 128;   // (whole warpgroups, for setmaxnreg)
+    static constexpr int kChunks = D / 64;            // of 64 elements, 128 bytes, in a row
+    static constexpr int kChunkBytes = kRows * 128;
+    static constexpr int kBlockBytes = kChunks * kChunkBytes;
+    static constexpr int kStages = D == 64 ? 8 : (D == 128 ? 5 : 2);
+    static constexpr int kShared = (kTiles + kStages) * kBlockBytes + 1024;   // (and room to align to 1024)
+    static constexpr int kColumnsO = 256;             // first column of tile 0's O; tile 1's 128 on
+};
+
+struct PromptSmem {
+    unsigned long long q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], looked[2], kv_full[8], kv_empty[8];
+    uint32_t tmem;
+    int by_hand[2];             // this block's P V of the tile is the warpgroup's
+    volatile unsigned odd[2];   // the last of the looks at V, counted from 1, that found a value that is not finite
+    volatile int abort;
+};
+
+// ------------------------------------------------------------------------------------------ PTX
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+__device__ __forceinline__ void mbar_init(const void* bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(const void* bar) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(const void* bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(const void* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+    return done != 0;
+}
+// Waits for the phase of `parity` to complete; false (and the error bit, and every other wait gives up too) if it does not.
+__device__ __forceinline__ bool mbar_wait(PromptSmem& sm, const void* bar, uint32_t parity) {
+    if (mbar_try(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try(bar, parity)) {
+        if (sm.abort || clock64() - t0 > kWaitLimitCycles) {
+            sm.abort = 1;
+            atomicOr(&g_device_error_flags, kDevErrExchangeTimeout);
+            return false;
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ void tma_load(void* to, const CUtensorMap* map, int x, int y, const void* bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                 ::"r"(smem_addr(to)), "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar)) : "memory");
+}
+
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(const void* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// Shared memory descriptor of a tile in rows of 128 swizzled bytes. K-major (rows are the operand's M or N): groups of 8 rows
+// are 1024 bytes apart. MN-major (rows are the contraction): so are groups of 8 rows, and chunks of 64 elements kChunkBytes.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t leading) {
+    return (static_cast<uint64_t>(addr >> 4) & 0x3fff) | (static_cast<uint64_t>(leading >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (uint64_t{1} << 46) | (uint64_t{2} << 61);
+}
+// bf16 x bf16 -> fp32, M 128.
+constexpr uint32_t instr_desc(int n, bool b_rows_are_k) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (b_rows_are_k ? 1u << 16 : 0u) | (static_cast<uint32_t>(n / 8) << 17) | (128u / 16 << 24);
+}
+constexpr uint32_t kNegateA = 1u << 13;
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)) : "memory");
+}
+
+#define MBD_R4(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3])
+#define MBD_R16(a, i) MBD_R4(a, i), MBD_R4(a, i + 4), MBD_R4(a, i + 8), MBD_R4(a, i + 12)
+#define MBD_W4(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3])
+#define MBD_W16(a, i) MBD_W4(a, i), MBD_W4(a, i + 4), MBD_W4(a, i + 8), MBD_W4(a, i + 12)
+// 32 (16, 4) columns of this thread's lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t at) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : MBD_R16(r, 0), MBD_R16(r, 16) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void tmem_st32(const uint32_t (&r)[32], uint32_t at) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+                 ::"r"(at), MBD_W16(r, 0), MBD_W16(r, 16) : "memory");
+}
+__device__ __forceinline__ void tmem_st16(const uint32_t (&r)[16], uint32_t at) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+                 "%16};"
+                 ::"r"(at), MBD_W16(r, 0) : "memory");
+}
+__device__ __forceinline__ void tmem_ld4(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];" : MBD_R4(r, 0) : "r"(at) : "memory");
+}
+#undef MBD_R4
+#undef MBD_R16
+#undef MBD_W4
+#undef MBD_W16
+
+// ------------------------------------------------------------------------------------------ work
+
+// Two tiles (one) against the blocks lo .. hi of one key-value head's keys.
+struct Item {
+    int64_t base;        // the sequence's first row
+    int len;
+    int kv_head;
+    int head[2], row[2]; // query head and first row (in the sequence) of each tile
+    int lo[2], hi[2];    // blocks that the tile's rows see any key of; none if lo > hi
+};
+
+// Item `index`, found by a whole warp. Row tiles are numbered over all sequences with room for one more in each, which needs
+// no sums: sequence b's begin at cu[b] / rows + b. Some numbers are no tile's then. The last rows, which see the most keys,
+// come first.
+template <int TILES>
+__device__ __forceinline__ Item item_at(const PromptParams& p, int64_t index) {
+    const int lane = threadIdx.x & 31, shift = p.pair_rows ? 8 : 7;
+    const int64_t number = index / p.units, unit = index - number * p.units;
+    const int64_t slot = p.slots - 1 - number;
+    int64_t lo = 0, hi = p.n_seqs;   // the last b whose tiles begin at or before slot
+    while (hi - lo > 1) {
+        const int64_t step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
+        const unsigned above = __ballot_sync(0xffffffffu, at >= hi || (static_cast<int64_t>(p.cu[at]) >> shift) + at > slot);
+        const int64_t from = lo + (__ffs(above) - 1) * step;
+        hi = min(hi, from + step);
+        lo = from;
+    }
+    const int64_t begin = p.cu[lo], end = p.cu[lo + 1];
+    Item it;
+    it.lo[0] = it.lo[1] = 0;
+    it.hi[0] = it.hi[1] = -1;
+    it.base = begin;
+    it.len = 0;
+    if (begin < 0 || end < begin || end > p.n_tokens) {
+        if (lane == 0) kv_bad_index();
+        return it;
+    }
+    it.len = static_cast<int>(end - begin);
+    const int64_t row0 = (slot - ((begin >> shift) + lo)) << shift;
+    const int first_head = static_cast<int>(p.pair_rows || TILES == 1 ? unit : 2 * unit);
+    it.kv_head = first_head / p.group;
+#pragma unroll
+    for (int i = 0; i < TILES; ++i) {
+        it.head[i] = first_head + (p.pair_rows ? 0 : i);
+        const int64_t row = row0 + (p.pair_rows ? i * kRows : 0);
+        it.row[i] = static_cast<int>(row);
+        if (row < 0 || row >= it.len) continue;
+        const int64_t last = min(row + kRows, static_cast<int64_t>(it.len)) - 1;
+        it.lo[i] = p.window > 0 ? static_cast<int>(max(int64_t{0}, row - p.window + 1) / kRows) : 0;
+        it.hi[i] = static_cast<int>(last / kRows);
+    }
+    return it;
+}
+
+template <int TILES>
+__device__ __forceinline__ void blocks_of(const Item& it, int* lo, int* hi) {
+    *lo = it.lo[0];
+    *hi = it.hi[0];
+    if (TILES == 2 && it.hi[1] >= it.lo[1]) {   // (a second row tile is there only if the first is)
+        *lo = min(*lo, it.lo[1]);
+        *hi = max(*hi, it.hi[1]);
+    }
+}
+
+// ------------------------------------------------------------------------------------------ softmax
+
+// This thread's row of one block's P V, over the keys klo .. khi in view, on top of what O holds (if `add`); p is in TMEM.
+template <int D>
+__device__ __noinline__ void product_by_hand(const char* v, uint32_t p_at, uint32_t o_at, int key0, int klo, int khi, bool add) {
+#pragma unroll 1
+    for (int d0 = 0; d0 < D; d0 += 32) {
+        uint32_t o[32];
+        if (add) {
+            tmem_ld32(o, o_at + d0);
+            tc_wait_ld();
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0;
+        }
+#pragma unroll 1
+        for (int c0 = 0; c0 < kRows; c0 += 8) {
+            uint32_t p[4];
+            __syncwarp();
+            tmem_ld4(p, p_at + c0 / 2);
+            tc_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const int at = c0 + c;
+                if (key0 + at < klo || key0 + at > khi) continue;
+                const float pc = c & 1 ? bf16_hi(p[c / 2]) : bf16_lo(p[c / 2]);
+                const char* row = v + (d0 / 64) * Prompt<D>::kChunkBytes + at * 128;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(row + ((((d0 % 64) / 8 + j) ^ (at & 7)) * 16));
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        o[j * 8 + 2 * k] = __float_as_uint(fmaf(pc, bf16_lo(w[k]), __uint_as_float(o[j * 8 + 2 * k])));
+                        o[j * 8 + 2 * k + 1] = __float_as_uint(fmaf(pc, bf16_hi(w[k]), __uint_as_float(o[j * 8 + 2 * k + 1])));
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        tmem_st32(o, o_at + d0);
+    }
+    tc_wait_st();
+}
+
+// O times `factor` for this thread's row.
+template <int D>
+__device__ __forceinline__ void rescale(uint32_t o_at, float factor) {
+#pragma unroll 1
+    for (int d0 = 0; d0 < D; d0 += 32) {
+        uint32_t o[32];
+        tmem_ld32(o, o_at + d0);
+        tc_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor);
+        tmem_st32(o, o_at + d0);
+    }
+    tc_wait_st();
+}
+
+template <int D>
+__global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __grid_constant__ PromptParams p) {
+    using P = Prompt<D>;
+    constexpr int TILES = P::kTiles;
+    extern __shared__ char dynamic[];
+    __shared__ PromptSmem sm;
+    char* const base = dynamic + ((1024 - (smem_addr(dynamic) & 1023)) & 1023);
+    auto q_tile = [&](int i) { return base + i * P::kBlockBytes; };
+    auto kv_stage = [&](unsigned n) { return base + (TILES + n % P::kStages) * P::kBlockBytes; };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_trigger();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.q_full[i], 1);
+            mbar_init(&sm.q_empty[i], 1);
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.p_full[i], 4);
+            mbar_init(&sm.pv_done[i], 1);
+            mbar_init(&sm.looked[i], 4);
+            sm.by_hand[i] = 0;
+            sm.odd[i] = 0;
+        }
+        for (int i = 0; i < P::kStages; ++i) {
+            mbar_init(&sm.kv_full[i], 1);
+            mbar_init(&sm.kv_empty[i], 1);
+        }
+        sm.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == TILES * 4) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sm.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    pdl_wait();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+
+    // Registers: the launch gives every thread 168 where there are three warpgroups; a row of S takes more, the others less.
+    if (warp >= TILES * 4) {
+    if constexpr (TILES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == TILES * 4 + 1) {
+        // ---- loads
+        unsigned n = 0;                 // blocks of keys or values so far
+        uint32_t q_phase[2] = {0, 0};
+        bool ok = true;
+        for (int64_t index = blockIdx.x; ok && index < p.items; index += gridDim.x) {
+            const Item it = item_at<TILES>(p, index);
+            int lo, hi;
+            blocks_of<TILES>(it, &lo, &hi);
+            if (lane == 0) {
+                for (int i = 0; i < TILES; ++i) {
+                    if (it.hi[i] < it.lo[i]) continue;
+                    if (!(ok = mbar_wait(sm, &sm.q_empty[i], q_phase[i] ^ 1))) break;
+                    q_phase[i] ^= 1;
+                    mbar_expect(&sm.q_full[i], P::kBlockBytes);
+                    for (int c = 0; c < P::kChunks; ++c)
+                        tma_load(q_tile(i) + c * P::kChunkBytes, &p.q_map, it.head[i] * D + c * 64,
+                                 static_cast<int>(it.base) + it.row[i], &sm.q_full[i]);
+                }
+                for (int j = lo; ok && j <= hi; ++j)
+                    for (int kv = 0; kv < 2; ++kv, ++n) {
+                        if (!(ok = mbar_wait(sm, &sm.kv_empty[n % P::kStages], (n / P::kStages & 1) ^ 1))) break;
+                        void* const bar = &sm.kv_full[n % P::kStages];
+                        mbar_expect(bar, P::kBlockBytes);
+                        for (int c = 0; c < P::kChunks; ++c)
+                            tma_load(kv_stage(n) + c * P::kChunkBytes, kv ? &p.v_map : &p.k_map, it.kv_head * D + c * 64,
+                                     static_cast<int>(it.base) + j * kRows, bar);
+                    }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        if (lane == 0) {   // the copies in flight land before the CTA's memory goes to another
+            for (unsigned k = n > P::kStages ? n - P::kStages : 0; k < n; ++k) {
+                const long long t0 = clock64();
+                while (!mbar_try(&sm.kv_full[k % P::kStages], k / P::kStages & 1) && clock64() - t0 < kWaitLimitCycles) {}
+            }
+            for (int i = 0; i < TILES; ++i) {
+                const long long t0 = clock64();
+                while (!mbar_try(&sm.q_full[i], q_phase[i] ^ 1) && clock64() - t0 < kWaitLimitCycles) {}
+            }
+        }
+    } else if (warp == TILES * 4) {
+        // ---- products
+        unsigned n = 0;
+        uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+        bool ok = true;
+        constexpr uint32_t kDescO = instr_desc(D, true);
+        const uint32_t desc_s = instr_desc(kRows, false) | (p.negate ? kNegateA : 0u);
+        for (int64_t index = blockIdx.x; ok && index < p.items; index += gridDim.x) {
+            const Item it = item_at<TILES>(p, index);
+            int lo, hi;
+            blocks_of<TILES>(it, &lo, &hi);
+            if (lane == 0 && lo <= hi) {
+                auto sees = [&](int i, int j) { return j >= it.lo[i] && j <= it.hi[i]; };
+                auto product_s = [&](int i, int j, unsigned stage) {
+                    const uint32_t a = smem_addr(q_tile(i)), b = smem_addr(kv_stage(stage));
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t at = (k / 4) * P::kChunkBytes + (k % 4) * 32;
+                        mma_ss(tmem + i * kRows, smem_desc(a + at, 16), smem_desc(b + at, 16), desc_s, k > 0);
+                    }
+                    tc_commit(&sm.s_full[i]);
+                    if (j == it.hi[i]) tc_commit(&sm.q_empty[i]);
+                };
+                auto product_o = [&](int i, int j, unsigned stage) {
+                    const uint32_t b = smem_addr(kv_stage(stage));
+                    if (!sm.by_hand[i]) {
+#pragma unroll
+                        for (int k = 0; k < kRows / 16; ++k)
+                            mma_ts(tmem + P::kColumnsO + i * kRows, tmem + i * kRows + k * 8, smem_desc(b + k * 2048, P::kChunkBytes),
+                                   kDescO, j > it.lo[i] || k > 0);
+                    }
+                    tc_commit(&sm.pv_done[i]);
+                };
+                auto kv_wait = [&](unsigned k) { return mbar_wait(sm, &sm.kv_full[k % P::kStages], k / P::kStages & 1); };
+                ok = kv_wait(n);
+                for (int i = 0; ok && i < TILES; ++i) {
+                    if (it.hi[i] < it.lo[i]) continue;
+                    if (!(ok = mbar_wait(sm, &sm.q_full[i], q_phase[i]))) break;
+                    q_phase[i] ^= 1;
+                    tc_fence_after();
+                    if (sees(i, lo)) product_s(i, lo, n);
+                }
+                if (ok) tc_commit(&sm.kv_empty[n % P::kStages]);
+                for (int j = lo; ok && j <= hi; ++j, n += 2) {
+                    if (!(ok = kv_wait(n + 1))) break;
+                    for (int i = 0; i < TILES; ++i) {
+                        if (sees(i, j)) {
+                            if (!(ok = mbar_wait(sm, &sm.p_full[i], p_phase[i]))) break;
+                            p_phase[i] ^= 1;
+                            tc_fence_after();
+                            product_o(i, j, n + 1);
+                        }
+                        if (j < hi && sees(i, j + 1)) {
+                            if (!(ok = kv_wait(n + 2))) break;
+                            tc_fence_after();
+                            product_s(i, j + 1, n + 2);
+                        }
+                    }
+                    if (!ok) break;
+                    tc_commit(&sm.kv_empty[(n + 1) % P::kStages]);
+                    if (j < hi) tc_commit(&sm.kv_empty[(n + 2) % P::kStages]);
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+    }
+    } else {
+        if constexpr (TILES == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        // ---- softmax of tile i, this thread's row of it
+        const int i = warp / 4, tid = threadIdx.x & 127;
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) * 32 << 16;
+        const uint32_t s_at = tmem + lanes + i * kRows, o_at = tmem + lanes + P::kColumnsO + i * kRows;
+        unsigned n = 0, looks = 0;
+        uint32_t s_phase = 0, pv_phase = 0;   // of the next S, of the next P V
+        bool ok = true;
+        const float scale = p.scale_log2;
+        for (int64_t index = blockIdx.x; ok && index < p.items; index += gridDim.x) {
+            const Item it = item_at<TILES>(p, index);
+            int all_lo, all_hi;
+            blocks_of<TILES>(it, &all_lo, &all_hi);
+            const int lo = it.lo[i], hi = it.hi[i], row0 = it.row[i], row = row0 + tid;
+            const int klo = p.window > 0 && row >= p.window ? row - static_cast<int>(p.window) + 1 : 0;
+            float ref = 0.0f, lim = -INFINITY;
+            float2 sum[4] = {f2(0.0f), f2(0.0f), f2(0.0f), f2(0.0f)};
+#pragma unroll 1
+            for (int j = lo; j <= hi; ++j) {
+                const int key0 = j * kRows;
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(sm, &sm.s_full[i], s_phase)))) break;
+                s_phase ^= 1;
+                tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(s[c], s_at + c * 32);
+                tc_wait_ld();
+                const bool masked = key0 + kRows - 1 > row0 || (p.window > 0 && key0 < row0 + kRows - p.window);
+                if (masked) {
+#pragma unroll
+                    for (int c = 0; c < kRows; ++c)
+                        if (key0 + c > row || key0 + c < klo) s[c / 32][c % 32] = 0xff800000u;   // -inf
+                }
+                float m[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    m[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+                    for (int e = 1; e < 31; e += 2) m[c] = max3(m[c], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+                    m[c] = fmaxf(m[c], __uint_as_float(s[c][31]));
+                }
+                const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * scale;
+                if (__any_sync(0xffffffffu, top > lim)) {
+                    const float t = fmaxf(top, lim - kLazy), next = t == -INFINITY ? 0.0f : t;   // (lim - kLazy: the kept maximum)
+                    const float old = lim == -INFINITY ? 0.0f : ex2(ref - next);
+                    ref = next;
+                    lim = t + kLazy;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) sum[c] = __fmul2_rn(sum[c], f2(old));
+                    if (j > lo) {
+                        if (!(ok = __all_sync(0xffffffffu, mbar_wait(sm, &sm.pv_done[i], pv_phase ^ 1)))) break;
+                        tc_fence_after();
+                        rescale<D>(o_at, old);
+                    }
+                }
+                const float2 scale2 = f2(scale), ref2 = f2(-ref);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t packed[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), scale2, ref2);
+                        x = make_float2(ex2(x.x), ex2(x.y));
+                        sum[e / 2 % 4] = __fadd2_rn(sum[e / 2 % 4], x);
+                        packed[e / 2] = pack_bf16x2(x);
+                    }
+                    tmem_st16(packed, s_at + c * 16);
+                }
+                tc_wait_st();
+                if (masked) {
+                    // V's rows of this block: any value that is not finite?
+                    const unsigned stage = n + 2 * (j - all_lo) + 1;
+                    ok = __all_sync(0xffffffffu, mbar_wait(sm, &sm.kv_full[stage % P::kStages], stage / P::kStages & 1));
+                    uint32_t odd = 0;
+                    const char* v = kv_stage(stage);
+#pragma unroll
+                    for (int k = 0; k < D / 8; ++k) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(v + (k / 8) * P::kChunkBytes + tid * 128 + ((k + tid) & 7) * 16);
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)   // 0 times it: 0 if it is finite, else NaN
+                            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(odd) : "r"(w[e]), "r"(0u));
+                    }
+                    // (The warpgroup agrees through a barrier in shared memory, whose wait is bounded.)
+                    ++looks;
+                    if (odd != 0) sm.odd[i] = looks;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sm.looked[i]);
+                    if (!(ok = __all_sync(0xffffffffu, ok && mbar_wait(sm, &sm.looked[i], (looks & 1) ^ 1)))) break;
+                    const bool any = sm.odd[i] == looks;
+                    if (any) {
+                        if (j > lo) {
+                            if (!(ok = __all_sync(0xffffffffu, mbar_wait(sm, &sm.pv_done[i], pv_phase ^ 1)))) break;
+                            tc_fence_after();
+                        }
+                        product_by_hand<D>(v, s_at, o_at, key0, klo, row, j > lo);
+                    }
+                    if (tid == 0) sm.by_hand[i] = any;
+                } else if (tid == 0) {
+                    sm.by_hand[i] = 0;
+                }
+                pv_phase ^= 1;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.p_full[i]);
+            }
+            if (ok && lo <= hi) {
+                // ---- the tile's rows of the output
+                ok = __all_sync(0xffffffffu, mbar_wait(sm, &sm.pv_done[i], pv_phase ^ 1));
+                tc_fence_after();
+                const float2 both = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+                const float total = both.x + both.y, f = total == 0.0f ? 0.0f : 1.0f / total;   // (0: every logit is -inf)
+                const bool in = ok && row < it.len;
+                char* out = static_cast<char*>(p.out) + ((it.base + row) * p.n_q_heads + it.head[i]) * (D * 2);
+#pragma unroll 1
+                for (int d0 = 0; d0 < D; d0 += 32) {
+                    uint32_t o[32];
+                    __syncwarp();
+                    tmem_ld32(o, o_at + d0);
+                    tc_wait_ld();
+                    if (in) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            auto pair = [&](int k) { return pack_bf16x2(__uint_as_float(o[e + k]) * f, __uint_as_float(o[e + k + 1]) * f); };
+                            *reinterpret_cast<uint4*>(out + (d0 + e) * 2) = make_uint4(pair(0), pair(2), pair(4), pair(6));
+                        }
+                    }
+                }
+                if (in && p.lse) p.lse[(it.base + row) * p.n_q_heads + it.head[i]] = total == 0.0f ? -INFINITY : (ref + log2f(total)) * kLn2;
+                tc_fence_before();
+            }
+            if (all_hi >= all_lo) n += 2 * (all_hi - all_lo + 1);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == TILES * 4) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+template <int D>
+cudaError_t launch(const PromptParams& p, int sms, cudaStream_t s) {
+    using P = Prompt<D>;
+    const cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kShared);
+    if (e != cudaSuccess) return e;
+    const unsigned grid = static_cast<unsigned>(p.items < sms ? p.items : sms);
+    return kv_launch(prompt_kernel<D>, grid, P::kThreads, P::kShared, 1, s, p);
+}
+
+}  // namespace
+
+int prompt_tiles(int head_dim) { return head_dim <= 128 ? 2 : 1; }
+
+cudaError_t launch_prompt(const PromptParams& p, int sms, cudaStream_t s) {
+    switch (p.head_dim) {
+        case 64: return launch<64>(p, sms, s);
+        case 128: return launch<128>(p, sms, s);
+        case 256: return launch<256>(p, sms, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t device_error_flags_prompt(unsigned int* flags, bool clear) { return kv_error_flags(flags, clear); }
+
+}  // namespace mbd

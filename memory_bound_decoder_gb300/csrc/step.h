@@ -1,7 +1,8 @@
 // Internal interface between the host layer of a serving step's other operators (step_api.cu) and their kernels
-// (rotary.cu, kv_pages.cu).
+// (rotary.cu, kv_pages.cu, prompt_attention.cu).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -42,6 +43,28 @@ struct ResizeParams {
     int ctas;                   // of the cluster
 };
 
+struct PromptParams {
+    CUtensorMap q_map, k_map, v_map;   // boxes of 64 elements and 128 rows, swizzled by 128 bytes
+    void* out;                  // [n_tokens, n_q_heads * head_dim] bf16
+    float* lse;                 // [n_tokens, n_q_heads] or null
+    const int32_t* cu;          // [n_seqs + 1]
+    int64_t n_seqs;
+    int64_t n_tokens;
+    int64_t window;             // 0: no window
+    int64_t slots;              // numbers of row tiles, some of them no tile's
+    int64_t units;              // query heads, or pairs of them, that share a row tile's number
+    int64_t items;              // slots * units
+    float scale_log2;           // |scale| * log2(e), not 0
+    int negate;                 // the scale is negative
+    int pair_rows;              // a CTA's two tiles are neighbours in the rows, not two heads
+    int n_q_heads;
+    int group;                  // query heads of a key-value head
+    int head_dim;
+};
+
+int prompt_tiles(int head_dim);   // tiles of 128 query rows that a CTA works on at a time
+cudaError_t launch_prompt(const PromptParams& p, int sms, cudaStream_t s);
+cudaError_t device_error_flags_prompt(unsigned int* flags, bool clear);
 cudaError_t launch_rotary(const RotaryParams& p, int sms, cudaStream_t s);
 cudaError_t launch_kv_resize(const ResizeParams& p, cudaStream_t s);
 cudaError_t device_error_flags_kv_pages(unsigned int* flags, bool clear);

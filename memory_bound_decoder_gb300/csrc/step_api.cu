@@ -1,4 +1,4 @@
-// C ABI of what goes with the key-value cache in a serving step: pages and slots, rotary positions. Host-side argument
+// C ABI of what goes with the key-value cache in a serving step: pages and slots, rotary positions, prompts. Host-side argument
 // checks and dispatch; as everywhere in the library, every check runs before anything is enqueued.
 #include <cmath>
 #include <cstdint>
@@ -16,6 +16,30 @@ constexpr double kTwoPi = 6.283185307179586476925286766559;
 
 bool positive(double x) { return std::isfinite(x) && x > 0.0; }
 double held(double x) { return x < 0.0 ? 0.0 : (x > 1.0 ? 1.0 : x); }
+
+// The runtime's way to the driver's encoder of tensor maps, so that the library links no driver library; null without one.
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+EncodeTiled encoder() {
+    static const EncodeTiled entry = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
+        (void)cudaGetLastError();
+        return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeTiled>(p) : nullptr;
+    }();
+    return entry;
+}
+
+// Rows of `width` bf16 in boxes of 64 elements and 128 rows.
+bool encode_rows(CUtensorMap* map, const void* base, int64_t width, int64_t rows, int64_t stride) {
+    const EncodeTiled encode = encoder();
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
+    const cuuint32_t box[2] = {64, 128}, steps[2] = {1, 1};
+    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, steps,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 }  // namespace
 
@@ -65,6 +89,55 @@ mbd_status mbd_kv_cache_resize(int32_t* page_table, int64_t pages_per_seq, int64
     p.n_tokens = n_tokens;
     p.ctas = n_seqs + n_tokens <= 1024 ? 1 : 8;
     return static_cast<mbd_status>(mbd::kv_finish_launch(mbd::launch_kv_resize(p, reinterpret_cast<cudaStream_t>(stream))));
+}
+
+mbd_status mbd_prompt_attention(void* out, const void* q, int64_t q_stride, const void* k, const void* v, int64_t kv_stride,
+                                const int32_t* cu_tokens, int64_t n_seqs, int64_t n_tokens, int64_t n_q_heads,
+                                int64_t n_kv_heads, int64_t head_dim, float scale, int64_t window, float* lse,
+                                mbd_stream_t stream) {
+    if (n_seqs < 0 || n_tokens < 0 || n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads != 0 || head_dim <= 0 ||
+        window < 0 || !std::isfinite(scale * 1.44269504088896341f))
+        return MBD_ERR_INVALID_ARG;
+    if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || n_q_heads > 4096 || n_tokens > MBD_KV_MAX_ROWS ||
+        n_seqs > MBD_KV_MAX_ROWS)
+        return MBD_ERR_UNSUPPORTED;
+    const int64_t width = n_q_heads * head_dim, kv_width = n_kv_heads * head_dim;
+    mbd_status st = check_stride(&q_stride, width);
+    if (st == MBD_OK) st = check_stride(&kv_stride, kv_width);
+    if (st != MBD_OK) return st;
+    if (n_seqs == 0 || n_tokens == 0) return MBD_OK;
+    if (!out || !q || !k || !v || !cu_tokens) return MBD_ERR_INVALID_ARG;
+    if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(cu_tokens, 4) || !aligned(lse, 4))
+        return MBD_ERR_MISALIGNED;
+    const Range writes[] = {{out, uint64_t(n_tokens) * width * 2}, {lse, uint64_t(n_tokens) * n_q_heads * 4}};
+    const uint64_t kv_rows = rows_bytes(n_tokens, kv_stride, kv_width);
+    for (const Range& r : {Range{q, rows_bytes(n_tokens, q_stride, width)}, Range{k, kv_rows}, Range{v, kv_rows},
+                           Range{cu_tokens, uint64_t(n_seqs + 1) * 4}})
+        if (overlaps_any(r, writes)) return MBD_ERR_INVALID_ARG;
+    if (overlap(writes[0], writes[1])) return MBD_ERR_INVALID_ARG;
+    mbd::PromptParams p{};
+    if (!encode_rows(&p.q_map, q, width, n_tokens, q_stride) || !encode_rows(&p.k_map, k, kv_width, n_tokens, kv_stride) ||
+        !encode_rows(&p.v_map, v, kv_width, n_tokens, kv_stride))
+        return static_cast<mbd_status>(mbd::kv_finish_launch(cudaErrorInvalidValue));
+    p.out = out;
+    p.lse = lse;
+    p.cu = cu_tokens;
+    p.n_seqs = n_seqs;
+    p.n_tokens = n_tokens;
+    p.window = window < n_tokens ? window : 0;
+    p.n_q_heads = static_cast<int>(n_q_heads);
+    p.group = static_cast<int>(n_q_heads / n_kv_heads);
+    p.head_dim = static_cast<int>(head_dim);
+    const int tiles = mbd::prompt_tiles(p.head_dim);
+    p.pair_rows = tiles == 2 && p.group % 2 != 0;
+    p.slots = (n_tokens >> (p.pair_rows ? 8 : 7)) + n_seqs;
+    p.units = p.pair_rows || tiles == 1 ? n_q_heads : n_q_heads / 2;
+    p.items = p.slots * p.units;
+    p.negate = scale < 0.0f;
+    // A scale of 0 makes every logit 0, also in units of log2: the least factor does, and leaves -inf where it is.
+    p.scale_log2 = std::fmax(std::fabs(scale * 1.44269504088896341f), 0x1p-149f);
+    return static_cast<mbd_status>(mbd::kv_finish_launch(
+        mbd::launch_prompt(p, mbd::kv_sm_count(), reinterpret_cast<cudaStream_t>(stream))));
 }
 
 mbd_status mbd_rotary(void* out, int64_t out_stride, const void* x, int64_t x_stride, const uint64_t* turns, float amplitude,

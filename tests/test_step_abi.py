@@ -203,3 +203,40 @@ def test_reference_prompt_closed_forms():
     f = wl.bf16_bits_to_f32(v).astype(np.float64)
     np.testing.assert_allclose(out[:, 0], [f[0], f[0:2].mean(0), f[1:3].mean(0), f[3], f[3:5].mean(0), f[4:6].mean(0), f[5:7].mean(0)])
     np.testing.assert_allclose(lse[:, 0] - 8, np.log([1, 2, 2, 1, 2, 2, 2]), atol=1e-12)
+
+
+# ------------------------------------------------------------------------------------------------ prompts
+
+def prompt(**kw):
+    a = dict(out=A, q=2 * A, q_stride=0, k=3 * A, v=4 * A, kv_stride=0, cu_tokens=5 * A, n_seqs=3, n_tokens=50, n_q_heads=4,
+             n_kv_heads=2, head_dim=64, scale=0.125, window=0, lse=6 * A, stream=None)
+    a.update(kw)
+    return lambda: mbd.prompt_attention(*a.values())
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(n_seqs=-1), mbd.ERR_INVALID_ARG), (dict(n_tokens=-1), mbd.ERR_INVALID_ARG), (dict(n_q_heads=0), mbd.ERR_INVALID_ARG),
+    (dict(n_kv_heads=0), mbd.ERR_INVALID_ARG), (dict(n_q_heads=3), mbd.ERR_INVALID_ARG), (dict(head_dim=0), mbd.ERR_INVALID_ARG),
+    (dict(window=-1), mbd.ERR_INVALID_ARG), (dict(scale=math.inf), mbd.ERR_INVALID_ARG),
+    (dict(scale=math.nan), mbd.ERR_INVALID_ARG), (dict(scale=3e38), mbd.ERR_INVALID_ARG),
+    (dict(out=None), mbd.ERR_INVALID_ARG), (dict(q=None), mbd.ERR_INVALID_ARG), (dict(k=None), mbd.ERR_INVALID_ARG),
+    (dict(v=None), mbd.ERR_INVALID_ARG), (dict(cu_tokens=None), mbd.ERR_INVALID_ARG),
+    (dict(q_stride=248), mbd.ERR_INVALID_ARG), (dict(kv_stride=120), mbd.ERR_INVALID_ARG),
+    (dict(out=2 * A + 512), mbd.ERR_INVALID_ARG), (dict(out=3 * A), mbd.ERR_INVALID_ARG), (dict(out=4 * A + 16), mbd.ERR_INVALID_ARG),
+    (dict(lse=A + 64), mbd.ERR_INVALID_ARG), (dict(lse=2 * A + 64), mbd.ERR_INVALID_ARG), (dict(cu_tokens=A + 64), mbd.ERR_INVALID_ARG),
+    (dict(out=A + 8), mbd.ERR_MISALIGNED), (dict(q=2 * A + 2), mbd.ERR_MISALIGNED), (dict(k=3 * A + 8), mbd.ERR_MISALIGNED),
+    (dict(v=4 * A + 4), mbd.ERR_MISALIGNED), (dict(q_stride=260), mbd.ERR_MISALIGNED), (dict(kv_stride=132), mbd.ERR_MISALIGNED),
+    (dict(cu_tokens=5 * A + 2), mbd.ERR_MISALIGNED), (dict(lse=6 * A + 2), mbd.ERR_MISALIGNED),
+    (dict(head_dim=80), mbd.ERR_UNSUPPORTED), (dict(head_dim=512), mbd.ERR_UNSUPPORTED),
+    (dict(n_q_heads=8192), mbd.ERR_UNSUPPORTED), (dict(n_tokens=(1 << 24) + 1), mbd.ERR_UNSUPPORTED),
+    (dict(n_seqs=(1 << 24) + 1), mbd.ERR_UNSUPPORTED),
+])
+def test_prompt_arguments(lib, kw, status):
+    assert _rc(prompt(**kw)) == status
+
+
+def test_empty_prompts(lib):
+    n0 = mbd.kernel_launches()
+    for kw in (dict(n_seqs=0), dict(n_tokens=0)):
+        prompt(**{**dict(out=None, q=None, k=None, v=None, cu_tokens=None), **kw})()
+    assert mbd.kernel_launches() == n0
