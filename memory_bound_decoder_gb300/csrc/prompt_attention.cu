@@ -109,31 +109,40 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tc_commit(const void* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+
+// One lane's: the whole warp comes here with the same operands, so that they stay in uniform registers. (Issued from a branch that
+// one lane takes, a product's operands went through vector registers and each instruction took 80 to 120 cycles; the tensor
+// cores are done with one in 64.)
+__device__ __forceinline__ void tc_commit(const void* bar, uint32_t elected) {
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+                 ::"r"(smem_addr(bar)), "r"(elected) : "memory");
 }
 
-// Shared memory descriptor of a tile in rows of 128 swizzled bytes. K-major (rows are the operand's M or N): groups of 8 rows
-// are 1024 bytes apart. MN-major (rows are the contraction): so are groups of 8 rows, and chunks of 64 elements kChunkBytes.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t leading) {
-    return (static_cast<uint64_t>(addr >> 4) & 0x3fff) | (static_cast<uint64_t>(leading >> 4) << 16) |
-           (static_cast<uint64_t>(1024 >> 4) << 32) | (uint64_t{1} << 46) | (uint64_t{2} << 61);
-}
+// Shared memory descriptor of a tile in rows of 128 swizzled bytes, its low word: address and leading offset (in 16 bytes). K-major
+// (rows are the operand's M or N): groups of 8 rows are 1024 bytes apart. MN-major (rows are the contraction): so are groups of
+// 8 rows, and chunks of 64 elements, the leading dimension, kChunkBytes.
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t leading) { return (addr >> 4) | (leading >> 4 << 16); }
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 // bf16 x bf16 -> fp32, M 128.
 constexpr uint32_t instr_desc(int n, bool b_rows_are_k) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (b_rows_are_k ? 1u << 16 : 0u) | (static_cast<uint32_t>(n / 8) << 17) | (128u / 16 << 24);
 }
 constexpr uint32_t kNegateA = 1u << 13;
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)) : "memory");
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add, uint32_t elected) {
+    asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b64 x, y;\n\t"
+                 "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 e, %6, 0;\n\t"
+                 "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}"
+                 ::"r"(d), "r"(a), "r"(b), "r"(kDescHigh), "r"(idesc), "r"(add), "r"(elected) : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)) : "memory");
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t add, uint32_t elected) {
+    asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b64 y;\n\t"
+                 "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 e, %6, 0;\n\t"
+                 "mov.b64 y, {%2, %3};\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}"
+                 ::"r"(d), "r"(a), "r"(b), "r"(kDescHigh), "r"(idesc), "r"(add), "r"(elected) : "memory");
 }
 
 #define MBD_R4(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3])
@@ -378,63 +387,79 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
         bool ok = true;
         constexpr uint32_t kDescO = instr_desc(D, true);
         const uint32_t desc_s = instr_desc(kRows, false) | (p.negate ? kNegateA : 0u);
+        uint32_t elected;
+        asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(elected));
+        auto wait = [&](const void* bar, uint32_t parity) {
+            ok = __all_sync(0xffffffffu, ok && mbar_wait(sm, bar, parity));
+            return ok;
+        };
+        auto kv_wait = [&](unsigned k) { return wait(&sm.kv_full[k % P::kStages], k / P::kStages & 1); };
+        auto kv_done = [&](unsigned k) { tc_commit(&sm.kv_empty[k % P::kStages], elected); };
         for (int64_t index = blockIdx.x; ok && index < p.items; index += gridDim.x) {
             const Item it = item_at<TILES>(p, index);
-            int lo, hi;
+            int tile_lo[TILES], tile_hi[TILES], lo, hi;
             blocks_of<TILES>(it, &lo, &hi);
-            if (lane == 0 && lo <= hi) {
-                auto sees = [&](int i, int j) { return j >= it.lo[i] && j <= it.hi[i]; };
-                auto product_s = [&](int i, int j, unsigned stage) {
-                    const uint32_t a = smem_addr(q_tile(i)), b = smem_addr(kv_stage(stage));
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t at = (k / 4) * P::kChunkBytes + (k % 4) * 32;
-                        mma_ss(tmem + i * kRows, smem_desc(a + at, 16), smem_desc(b + at, 16), desc_s, k > 0);
-                    }
-                    tc_commit(&sm.s_full[i]);
-                    if (j == it.hi[i]) tc_commit(&sm.q_empty[i]);
-                };
-                auto product_o = [&](int i, int j, unsigned stage) {
-                    const uint32_t b = smem_addr(kv_stage(stage));
-                    if (!sm.by_hand[i]) {
-#pragma unroll
-                        for (int k = 0; k < kRows / 16; ++k)
-                            mma_ts(tmem + P::kColumnsO + i * kRows, tmem + i * kRows + k * 8, smem_desc(b + k * 2048, P::kChunkBytes),
-                                   kDescO, j > it.lo[i] || k > 0);
-                    }
-                    tc_commit(&sm.pv_done[i]);
-                };
-                auto kv_wait = [&](unsigned k) { return mbar_wait(sm, &sm.kv_full[k % P::kStages], k / P::kStages & 1); };
-                ok = kv_wait(n);
-                for (int i = 0; ok && i < TILES; ++i) {
-                    if (it.hi[i] < it.lo[i]) continue;
-                    if (!(ok = mbar_wait(sm, &sm.q_full[i], q_phase[i]))) break;
-                    q_phase[i] ^= 1;
-                    tc_fence_after();
-                    if (sees(i, lo)) product_s(i, lo, n);
-                }
-                if (ok) tc_commit(&sm.kv_empty[n % P::kStages]);
-                for (int j = lo; ok && j <= hi; ++j, n += 2) {
-                    if (!(ok = kv_wait(n + 1))) break;
-                    for (int i = 0; i < TILES; ++i) {
-                        if (sees(i, j)) {
-                            if (!(ok = mbar_wait(sm, &sm.p_full[i], p_phase[i]))) break;
-                            p_phase[i] ^= 1;
-                            tc_fence_after();
-                            product_o(i, j, n + 1);
-                        }
-                        if (j < hi && sees(i, j + 1)) {
-                            if (!(ok = kv_wait(n + 2))) break;
-                            tc_fence_after();
-                            product_s(i, j + 1, n + 2);
-                        }
-                    }
-                    if (!ok) break;
-                    tc_commit(&sm.kv_empty[(n + 1) % P::kStages]);
-                    if (j < hi) tc_commit(&sm.kv_empty[(n + 2) % P::kStages]);
-                }
+            for (int i = 0; i < TILES; ++i) {
+                tile_lo[i] = __shfl_sync(0xffffffffu, it.lo[i], 0);
+                tile_hi[i] = __shfl_sync(0xffffffffu, it.hi[i], 0);
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+            lo = __shfl_sync(0xffffffffu, lo, 0);
+            hi = __shfl_sync(0xffffffffu, hi, 0);
+            if (lo > hi) continue;
+            auto product_s = [&](int i, int j, unsigned stage) {
+                const uint32_t a = __shfl_sync(0xffffffffu, desc_low(smem_addr(q_tile(i)), 16), 0);
+                const uint32_t b = __shfl_sync(0xffffffffu, desc_low(smem_addr(kv_stage(stage)), 16), 0);
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t at = ((k / 4) * P::kChunkBytes + (k % 4) * 32) >> 4;
+                    mma_ss(tmem + i * kRows, a + at, b + at, desc_s, k > 0, elected);
+                }
+                tc_commit(&sm.s_full[i], elected);
+                if (j == tile_hi[i]) tc_commit(&sm.q_empty[i], elected);
+            };
+            auto product_o = [&](int i, int j, unsigned stage) {
+                const uint32_t b = __shfl_sync(0xffffffffu, desc_low(smem_addr(kv_stage(stage)), P::kChunkBytes), 0);
+                if (!__shfl_sync(0xffffffffu, sm.by_hand[i], 0)) {
+#pragma unroll
+                    for (int k = 0; k < kRows / 16; ++k)
+                        mma_ts(tmem + P::kColumnsO + i * kRows, tmem + i * kRows + k * 8, b + (k * 2048 >> 4), kDescO,
+                               k > 0 || j > tile_lo[i], elected);
+                }
+                tc_commit(&sm.pv_done[i], elected);
+            };
+            kv_wait(n);
+#pragma unroll
+            for (int i = 0; i < TILES; ++i) {
+                if (tile_hi[i] < tile_lo[i]) continue;
+                if (!wait(&sm.q_full[i], q_phase[i])) break;
+                q_phase[i] ^= 1;
+                tc_fence_after();
+                if (tile_lo[i] == lo) product_s(i, lo, n);
+            }
+            if (!ok) break;
+            kv_done(n);
+#pragma unroll 1
+            for (int j = lo; j <= hi; ++j, n += 2) {
+                if (!kv_wait(n + 1)) break;
+#pragma unroll
+                for (int i = 0; i < TILES; ++i) {
+                    if (j >= tile_lo[i] && j <= tile_hi[i]) {
+                        if (!wait(&sm.p_full[i], p_phase[i])) break;
+                        p_phase[i] ^= 1;
+                        tc_fence_after();
+                        product_o(i, j, n + 1);
+                    }
+                    if (j < hi && j + 1 >= tile_lo[i] && j + 1 <= tile_hi[i]) {
+                        if (!kv_wait(n + 2)) break;
+                        tc_fence_after();
+                        product_s(i, j + 1, n + 2);
+                    }
+                }
+                if (!ok) break;
+                kv_done(n + 1);
+                if (j < hi) kv_done(n + 2);
+            }
         }
     }
     } else {
