@@ -37,18 +37,35 @@ constexpr float kLn2 = 0.693147180559945309f;
 
 template <int D>
 struct Prompt {
-    static constexpr int kTiles = D <= 128 ? 2 : 1;   // (TMEM: 128 columns of S and D of O for each)
+    // TMEM has 512 columns. O takes D of them for each tile, S 128, P (bf16) 64. At D 128 that leaves one S, which the two tiles
+    // use in turn; at D 256 there is one tile.
+    static constexpr int kTiles = D <= 128 ? 2 : 1;
+    static constexpr int kBuffers = D == 64 ? 2 : 1;   // of S
+    static constexpr int kColumnsS = 0, kColumnsP = kBuffers * kRows, kColumnsO = kColumnsP + kTiles * kRows / 2;
+    static_assert(kColumnsO + kTiles * D <= 512, "TMEM");
     static constexpr int kThreads = kTiles * 128 + 128;   // (whole warpgroups, for setmaxnreg)
     static constexpr int kChunks = D / 64;            // of 64 elements, 128 bytes, in a row
     static constexpr int kChunkBytes = kRows * 128;
     static constexpr int kBlockBytes = kChunks * kChunkBytes;
     static constexpr int kStages = D == 64 ? 8 : (D == 128 ? 5 : 2);
     static constexpr int kShared = (kTiles + kStages) * kBlockBytes + 1024;   // (and room to align to 1024)
-    static constexpr int kColumnsO = 256;             // first column of tile 0's O; tile 1's 128 on
+};
+
+// Two tiles (one) against the blocks lo .. hi of one key-value head's keys.
+struct Item {
+    int base;            // the sequence's first row
+    int len;
+    int kv_head;
+    int head[2], row[2]; // query head and first row (in the sequence) of each tile
+    int lo[2], hi[2];    // blocks that the tile's rows see any key of; none if lo > hi
+    int more;            // 0: there is none, and none follows
 };
 
 struct PromptSmem {
-    unsigned long long q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2], looked[2], kv_full[8], kv_empty[8];
+    unsigned long long q_full[2], q_empty[2], s_full[2], s_free[2], p_full[2], pv_done[2], looked[2], kv_full[8], kv_empty[8];
+    unsigned long long item_full, item_empty, stolen;
+    alignas(16) uint4 reply;
+    Item item;
     uint32_t tmem;
     int by_hand[2];             // this block's P V of the tile is the warpgroup's
     volatile unsigned odd[2];   // the last of the looks at V, counted from 1, that found a value that is not finite
@@ -82,6 +99,14 @@ __device__ __forceinline__ bool mbar_try(const void* bar, uint32_t parity) {
     uint32_t done;
     asm volatile("{\n\t.reg .pred p;\n\t"
                  "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ bool mbar_test(const void* bar, uint32_t parity) {   // without waiting
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(done) : "r"(smem_addr(bar)), "r"(parity) : "memory");
     return done != 0;
@@ -175,56 +200,107 @@ __device__ __forceinline__ void tmem_ld4(uint32_t (&r)[4], uint32_t at) {
 
 // ------------------------------------------------------------------------------------------ work
 
-// Two tiles (one) against the blocks lo .. hi of one key-value head's keys.
-struct Item {
-    int64_t base;        // the sequence's first row
-    int len;
-    int kv_head;
-    int head[2], row[2]; // query head and first row (in the sequence) of each tile
-    int lo[2], hi[2];    // blocks that the tile's rows see any key of; none if lo > hi
+// The row tiles (pairs of them) of all sequences, numbered, by a whole warp.
+struct Rows {
+    // Up to 256 sequences: by their place in their sequence, the last places first, as they see the most keys, so that what is
+    // begun last takes the shortest. Sequence 32 c + lane has tiles[c]; `before` tiles lie at higher places than `place`.
+    static constexpr int kMany = 8;
+    int tiles[kMany];
+    int place;
+    int64_t before;
+
+    __device__ __forceinline__ void begin(const PromptParams& p, int shift) {
+        const int lane = threadIdx.x & 31;
+        int most = 0;
+#pragma unroll
+        for (int c = 0; c < kMany; ++c) {
+            tiles[c] = 0;
+            const int64_t b = c * 32 + lane;
+            if (c * 32 >= p.n_seqs || b >= p.n_seqs || p.n_seqs > kMany * 32) continue;
+            const int64_t first = p.cu[b], end = p.cu[b + 1];
+            if (first >= 0 && end >= first && end <= p.n_tokens) tiles[c] = static_cast<int>((end - first + (1 << shift) - 1) >> shift);
+            else kv_bad_index();
+            most = max(most, tiles[c]);
+        }
+        place = __reduce_max_sync(0xffffffffu, most) - 1;
+        before = 0;
+    }
+    // Sequence and place of tile `number` (ascending from call to call); false if there are not so many.
+    __device__ __forceinline__ bool find(const PromptParams& p, int shift, int64_t number, int64_t* seq, int64_t* at) {
+        const int lane = threadIdx.x & 31;
+        if (p.n_seqs <= kMany * 32) {
+            for (; place >= 0; --place) {
+                unsigned there[kMany];
+                int count = 0;
+#pragma unroll
+                for (int c = 0; c < kMany; ++c) {
+                    there[c] = c * 32 < p.n_seqs ? __ballot_sync(0xffffffffu, tiles[c] > place) : 0u;
+                    count += __popc(there[c]);
+                }
+                if (number >= before + count) {
+                    before += count;
+                    continue;
+                }
+                int k = static_cast<int>(number - before);
+                for (int c = 0; c < kMany; ++c) {
+                    if (k < __popc(there[c])) {
+                        const bool it = ((there[c] >> lane) & 1u) && __popc(there[c] & ((1u << lane) - 1u)) == k;
+                        *seq = c * 32 + __ffs(__ballot_sync(0xffffffffu, it)) - 1;
+                        *at = place;
+                        return true;
+                    }
+                    k -= __popc(there[c]);
+                }
+            }
+            return false;
+        }
+        // More: one sequence behind the other, with room for one tile more in each, which needs no sums (sequence b's begin at cu[b]
+        // / rows + b); some numbers are no tile's.
+        const int64_t slot = p.slots - 1 - number;
+        int64_t lo = 0, hi = p.n_seqs;   // the last b whose tiles begin at or before slot
+        while (hi - lo > 1) {
+            const int64_t step = (hi - lo + 31) / 32, to = lo + (lane + 1) * step;
+            const unsigned above = __ballot_sync(0xffffffffu, to >= hi || (static_cast<int64_t>(p.cu[to]) >> shift) + to > slot);
+            const int64_t from = lo + (__ffs(above) - 1) * step;
+            hi = min(hi, from + step);
+            lo = from;
+        }
+        const int64_t first = p.cu[lo], end = p.cu[lo + 1];
+        if (first < 0 || end < first || end > p.n_tokens) {
+            kv_bad_index();
+            return false;
+        }
+        *seq = lo;
+        *at = slot - ((first >> shift) + lo);
+        return *at >= 0 && *at << shift < end - first;
+    }
 };
 
-// Item `index`, found by a whole warp. Row tiles are numbered over all sequences with room for one more in each, which needs
-// no sums: sequence b's begin at cu[b] / rows + b. Some numbers are no tile's then. The last rows, which see the most keys,
-// come first.
+// Item `index`; false if it is none.
 template <int TILES>
-__device__ __forceinline__ Item item_at(const PromptParams& p, int64_t index) {
-    const int lane = threadIdx.x & 31, shift = p.pair_rows ? 8 : 7;
+__device__ __forceinline__ bool item_at(const PromptParams& p, Rows& rows, int64_t index, Item* item) {
+    const int shift = p.pair_rows ? 8 : 7;
     const int64_t number = index / p.units, unit = index - number * p.units;
-    const int64_t slot = p.slots - 1 - number;
-    int64_t lo = 0, hi = p.n_seqs;   // the last b whose tiles begin at or before slot
-    while (hi - lo > 1) {
-        const int64_t step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
-        const unsigned above = __ballot_sync(0xffffffffu, at >= hi || (static_cast<int64_t>(p.cu[at]) >> shift) + at > slot);
-        const int64_t from = lo + (__ffs(above) - 1) * step;
-        hi = min(hi, from + step);
-        lo = from;
-    }
-    const int64_t begin = p.cu[lo], end = p.cu[lo + 1];
-    Item it;
-    it.lo[0] = it.lo[1] = 0;
-    it.hi[0] = it.hi[1] = -1;
-    it.base = begin;
-    it.len = 0;
-    if (begin < 0 || end < begin || end > p.n_tokens) {
-        if (lane == 0) kv_bad_index();
-        return it;
-    }
-    it.len = static_cast<int>(end - begin);
-    const int64_t row0 = (slot - ((begin >> shift) + lo)) << shift;
+    int64_t seq, at;
+    if (!rows.find(p, shift, number, &seq, &at)) return false;
+    const int64_t first = p.cu[seq];
+    Item& it = *item;
+    it.base = static_cast<int>(first);
+    it.len = static_cast<int>(p.cu[seq + 1] - first);
     const int first_head = static_cast<int>(p.pair_rows || TILES == 1 ? unit : 2 * unit);
     it.kv_head = first_head / p.group;
+    it.more = 1;
 #pragma unroll
-    for (int i = 0; i < TILES; ++i) {
+    for (int i = 0; i < 2; ++i) {
         it.head[i] = first_head + (p.pair_rows ? 0 : i);
-        const int64_t row = row0 + (p.pair_rows ? i * kRows : 0);
-        it.row[i] = static_cast<int>(row);
-        if (row < 0 || row >= it.len) continue;
-        const int64_t last = min(row + kRows, static_cast<int64_t>(it.len)) - 1;
-        it.lo[i] = p.window > 0 ? static_cast<int>(max(int64_t{0}, row - p.window + 1) / kRows) : 0;
-        it.hi[i] = static_cast<int>(last / kRows);
+        it.row[i] = static_cast<int>(at << shift) + (p.pair_rows ? i * kRows : 0);
+        it.lo[i] = 0;
+        it.hi[i] = -1;
+        if (i >= TILES || it.row[i] >= it.len) continue;
+        it.lo[i] = p.window > 0 ? static_cast<int>(max(int64_t{0}, it.row[i] - p.window + 1) / kRows) : 0;
+        it.hi[i] = (min(it.row[i] + kRows, it.len) - 1) / kRows;
     }
-    return it;
+    return true;
 }
 
 template <int TILES>
@@ -235,6 +311,11 @@ __device__ __forceinline__ void blocks_of(const Item& it, int* lo, int* hi) {
         *lo = min(*lo, it.lo[1]);
         *hi = max(*hi, it.hi[1]);
     }
+}
+
+// Whether a block that begins at key0 holds places that are masked for a row of the tile that begins at `row`.
+__device__ __forceinline__ bool some_masked(const PromptParams& p, int row, int key0) {
+    return key0 + kRows - 1 > row || (p.window > 0 && key0 < row + kRows - p.window);
 }
 
 // ------------------------------------------------------------------------------------------ softmax
@@ -313,6 +394,7 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
             mbar_init(&sm.q_full[i], 1);
             mbar_init(&sm.q_empty[i], 1);
             mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.s_free[i], 4);
             mbar_init(&sm.p_full[i], 4);
             mbar_init(&sm.pv_done[i], 1);
             mbar_init(&sm.looked[i], 4);
@@ -323,6 +405,9 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
             mbar_init(&sm.kv_full[i], 1);
             mbar_init(&sm.kv_empty[i], 1);
         }
+        mbar_init(&sm.item_full, 1);
+        mbar_init(&sm.item_empty, 2 + TILES * 4);
+        mbar_init(&sm.stolen, 1);
         sm.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -336,37 +421,91 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
     tc_fence_after();
     const uint32_t tmem = sm.tmem;
 
+    // Items come by way of shared memory: k counts them.
+    auto next_item = [&](unsigned k, Item* it) {
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(sm, &sm.item_full, k & 1));
+        if (!ok) return false;
+        *it = sm.item;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.item_empty);
+        return it->more != 0;
+    };
+    Item it;
+    int all_lo, all_hi;   // blocks that either tile sees
     // Registers: the launch gives every thread 168 where there are three warpgroups; a row of S takes more, the others less.
     if (warp >= TILES * 4) {
     if constexpr (TILES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == TILES * 4 + 1) {
+    if (warp == TILES * 4 + 2) {
+        // ---- what to do: the CTA's own index, then those of CTAs that have not begun, which it takes from the launch
+        Rows rows;
+        rows.begin(p, p.pair_rows ? 8 : 7);
+        unsigned replies = 0;
+        // The index of a CTA that will not begin any more, or -1: all have.
+        auto steal = [&](bool* ok) {
+            int index = -1;
+            if (lane == 0) {
+                mbar_expect(&sm.stolen, 16);
+                asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                             ::"r"(smem_addr(&sm.reply)), "r"(smem_addr(&sm.stolen)) : "memory");
+            }
+            __syncwarp();
+            *ok = __all_sync(0xffffffffu, mbar_wait(sm, &sm.stolen, replies & 1));
+            ++replies;
+            if (*ok)
+                asm volatile("{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+                             "ld.shared.b128 r, [%1];\n\t"
+                             "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+                             "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, r;\n\t}"
+                             : "+r"(index) : "r"(smem_addr(&sm.reply)) : "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the reply is read before the next one is written
+            __syncwarp();
+            return __shfl_sync(0xffffffffu, index, 0);
+        };
+        // One item ahead of what the softmax is at, no more: what is taken earlier may be missing elsewhere at the end.
+        bool ok = true;
+        int64_t index = blockIdx.x;
+        for (unsigned k = 0; ok; ++k) {
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(sm, &sm.item_empty, (k & 1) ^ 1)))) break;
+            if (k > 0) index = steal(&ok);
+            bool found = false;
+            while (ok && index >= 0 && !(found = item_at<TILES>(p, rows, index, &it))) index = steal(&ok);
+            if (!ok) break;
+            if (!found) it.more = 0;
+            if (lane == 0) {
+                sm.item = it;
+                mbar_arrive(&sm.item_full);
+            }
+            if (!found) break;
+        }
+    } else if (warp == TILES * 4 + 1) {
         // ---- loads
         unsigned n = 0;                 // blocks of keys or values so far
         uint32_t q_phase[2] = {0, 0};
         bool ok = true;
-        for (int64_t index = blockIdx.x; ok && index < p.items; index += gridDim.x) {
-            const Item it = item_at<TILES>(p, index);
-            int lo, hi;
-            blocks_of<TILES>(it, &lo, &hi);
+        for (unsigned k = 0; ok && next_item(k, &it); ++k) {
+            blocks_of<TILES>(it, &all_lo, &all_hi);
             if (lane == 0) {
-                for (int i = 0; i < TILES; ++i) {
+                for (int i = 0; ok && i < TILES; ++i) {
                     if (it.hi[i] < it.lo[i]) continue;
                     if (!(ok = mbar_wait(sm, &sm.q_empty[i], q_phase[i] ^ 1))) break;
                     q_phase[i] ^= 1;
                     mbar_expect(&sm.q_full[i], P::kBlockBytes);
                     for (int c = 0; c < P::kChunks; ++c)
                         tma_load(q_tile(i) + c * P::kChunkBytes, &p.q_map, it.head[i] * D + c * 64,
-                                 static_cast<int>(it.base) + it.row[i], &sm.q_full[i]);
+                                 it.base + it.row[i], &sm.q_full[i]);
                 }
-                for (int j = lo; ok && j <= hi; ++j)
-                    for (int kv = 0; kv < 2; ++kv, ++n) {
-                        if (!(ok = mbar_wait(sm, &sm.kv_empty[n % P::kStages], (n / P::kStages & 1) ^ 1))) break;
-                        void* const bar = &sm.kv_full[n % P::kStages];
-                        mbar_expect(bar, P::kBlockBytes);
-                        for (int c = 0; c < P::kChunks; ++c)
-                            tma_load(kv_stage(n) + c * P::kChunkBytes, kv ? &p.v_map : &p.k_map, it.kv_head * D + c * 64,
-                                     static_cast<int>(it.base) + j * kRows, bar);
-                    }
+                // K of block lo, then K of each next block and V of this one.
+                const int blocks = all_hi - all_lo + 1;
+                for (int m = 0; ok && m < 2 * blocks; ++m, ++n) {
+                    if (!(ok = mbar_wait(sm, &sm.kv_empty[n % P::kStages], (n / P::kStages & 1) ^ 1))) break;
+                    const bool values = m == 2 * blocks - 1 || (m > 0 && m % 2 == 0);
+                    const int j = all_lo + (values ? (m - 1) / 2 : (m + 1) / 2);
+                    void* const bar = &sm.kv_full[n % P::kStages];
+                    mbar_expect(bar, P::kBlockBytes);
+                    for (int c = 0; c < P::kChunks; ++c)
+                        tma_load(kv_stage(n) + c * P::kChunkBytes, values ? &p.v_map : &p.k_map, it.kv_head * D + c * 64,
+                                 it.base + j * kRows, bar);
+                }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
         }
@@ -381,85 +520,115 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
             }
         }
     } else if (warp == TILES * 4) {
-        // ---- products
-        unsigned n = 0;
-        uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-        bool ok = true;
-        constexpr uint32_t kDescO = instr_desc(D, true);
-        const uint32_t desc_s = instr_desc(kRows, false) | (p.negate ? kNegateA : 0u);
+        // ---- products. The tensor cores take few instructions ahead, so what this warp does between two products has to be short:
+        // it looks at the next one's barriers while it issues this one, a wait that has run out is looked at once a block only (what
+        // is issued in between works on whatever lies in this CTA's memory), and stages are counted, not divided.
         uint32_t elected;
         asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(elected));
-        auto wait = [&](const void* bar, uint32_t parity) {
-            ok = __all_sync(0xffffffffu, ok && mbar_wait(sm, bar, parity));
-            return ok;
+        constexpr uint32_t kDescO = instr_desc(D, true);
+        const uint32_t desc_s = instr_desc(kRows, false) | (p.negate ? kNegateA : 0u);
+        const uint32_t low = __shfl_sync(0xffffffffu, smem_addr(base) >> 4, 0);   // of a tile: this and its place / 16
+        constexpr uint32_t kBlock = P::kBlockBytes >> 4;
+        uint32_t q_phase = 0, p_phase[2] = {0, 0}, s_phase[2] = {0, 0};
+        bool ok = true;
+        auto wait = [&](const void* bar, uint32_t parity) { ok &= mbar_wait(sm, bar, parity); };
+        struct Stage {
+            uint32_t at, phase;
+            __device__ __forceinline__ Stage next() const { return at + 1 == P::kStages ? Stage{0u, phase ^ 1u} : Stage{at + 1, phase}; }
         };
-        auto kv_wait = [&](unsigned k) { return wait(&sm.kv_full[k % P::kStages], k / P::kStages & 1); };
-        auto kv_done = [&](unsigned k) { tc_commit(&sm.kv_empty[k % P::kStages], elected); };
-        for (int64_t index = blockIdx.x; ok && index < p.items; index += gridDim.x) {
-            const Item it = item_at<TILES>(p, index);
-            int tile_lo[TILES], tile_hi[TILES], lo, hi;
-            blocks_of<TILES>(it, &lo, &hi);
+        Stage stage{0, 0};   // the next block of keys or values
+        for (unsigned k = 0; next_item(k, &it); ++k) {
+            int tile_lo[TILES], tile_hi[TILES], row[TILES];
 #pragma unroll
             for (int i = 0; i < TILES; ++i) {
                 tile_lo[i] = __shfl_sync(0xffffffffu, it.lo[i], 0);
                 tile_hi[i] = __shfl_sync(0xffffffffu, it.hi[i], 0);
+                row[i] = __shfl_sync(0xffffffffu, it.row[i], 0);
             }
-            lo = __shfl_sync(0xffffffffu, lo, 0);
-            hi = __shfl_sync(0xffffffffu, hi, 0);
-            if (lo > hi) continue;
-            auto product_s = [&](int i, int j, unsigned stage) {
-                const uint32_t a = __shfl_sync(0xffffffffu, desc_low(smem_addr(q_tile(i)), 16), 0);
-                const uint32_t b = __shfl_sync(0xffffffffu, desc_low(smem_addr(kv_stage(stage)), 16), 0);
+            blocks_of<TILES>(it, &all_lo, &all_hi);
+            const int lo = __shfl_sync(0xffffffffu, all_lo, 0), hi = __shfl_sync(0xffffffffu, all_hi, 0);
+            // S of tile i and block j: the block's keys are there, and what was in the buffer has been read. `look` is called before
+            // the last two instructions; `ready`: the barriers were seen complete.
+            auto s_ready = [&](int i, const Stage& keys) {
+                const int f = i & (P::kBuffers - 1);
+                return mbar_test(&sm.kv_full[keys.at], keys.phase) & mbar_test(&sm.s_free[f], s_phase[f] ^ 1);
+            };
+            auto product_s = [&](int i, int j, const Stage& keys, bool ready, auto look) {
+                const int f = i & (P::kBuffers - 1);
+                const uint32_t a = low + i * kBlock + (1u << 16), b = low + (TILES + keys.at) * kBlock + (1u << 16);
+                if (!ready) {
+                    wait(&sm.kv_full[keys.at], keys.phase);
+                    wait(&sm.s_free[f], s_phase[f] ^ 1);
+                }
+                s_phase[f] ^= 1;
+                tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
+                    if (k == D / 16 - 2) look();
                     const uint32_t at = ((k / 4) * P::kChunkBytes + (k % 4) * 32) >> 4;
-                    mma_ss(tmem + i * kRows, a + at, b + at, desc_s, k > 0, elected);
+                    mma_ss(tmem + P::kColumnsS + f * kRows, a + at, b + at, desc_s, k > 0, elected);
                 }
                 tc_commit(&sm.s_full[i], elected);
                 if (j == tile_hi[i]) tc_commit(&sm.q_empty[i], elected);
             };
-            auto product_o = [&](int i, int j, unsigned stage) {
-                const uint32_t b = __shfl_sync(0xffffffffu, desc_low(smem_addr(kv_stage(stage)), P::kChunkBytes), 0);
-                if (!__shfl_sync(0xffffffffu, sm.by_hand[i], 0)) {
+            auto o_ready = [&](int i, const Stage& values) {
+                return mbar_test(&sm.kv_full[values.at], values.phase) & mbar_test(&sm.p_full[i], p_phase[i]);
+            };
+            auto product_o = [&](int i, int j, const Stage& values, bool ready, auto look) {
+                const uint32_t b = low + (TILES + values.at) * kBlock + (P::kChunkBytes >> 4 << 16);
+                if (!ready) {
+                    wait(&sm.kv_full[values.at], values.phase);
+                    wait(&sm.p_full[i], p_phase[i]);
+                }
+                p_phase[i] ^= 1;
+                tc_fence_after();
+                bool by_hand = false;
+                if (some_masked(p, row[i], j * kRows)) by_hand = __shfl_sync(0xffffffffu, sm.by_hand[i], 0);
+                if (!by_hand) {
 #pragma unroll
-                    for (int k = 0; k < kRows / 16; ++k)
-                        mma_ts(tmem + P::kColumnsO + i * kRows, tmem + i * kRows + k * 8, b + (k * 2048 >> 4), kDescO,
+                    for (int k = 0; k < kRows / 16; ++k) {
+                        if (k == kRows / 16 - 2) look();
+                        mma_ts(tmem + P::kColumnsO + i * D, tmem + P::kColumnsP + i * (kRows / 2) + k * 8, b + (k * 2048 >> 4), kDescO,
                                k > 0 || j > tile_lo[i], elected);
+                    }
                 }
                 tc_commit(&sm.pv_done[i], elected);
             };
-            kv_wait(n);
+            auto nothing = [] {};
 #pragma unroll
             for (int i = 0; i < TILES; ++i) {
                 if (tile_hi[i] < tile_lo[i]) continue;
-                if (!wait(&sm.q_full[i], q_phase[i])) break;
-                q_phase[i] ^= 1;
-                tc_fence_after();
-                if (tile_lo[i] == lo) product_s(i, lo, n);
+                wait(&sm.q_full[i], q_phase >> i & 1);
+                q_phase ^= 1u << i;
+                if (tile_lo[i] == lo) product_s(i, lo, stage, false, nothing);
             }
-            if (!ok) break;
-            kv_done(n);
+            tc_commit(&sm.kv_empty[stage.at], elected);
+            stage = stage.next();
+            // The next block's S goes before this block's P V, which waits for the softmax.
+            bool ready_s = false;
 #pragma unroll 1
-            for (int j = lo; j <= hi; ++j, n += 2) {
-                if (!kv_wait(n + 1)) break;
+            for (int j = lo; j <= hi; ++j) {
+                const Stage keys = stage, values = j < hi ? keys.next() : keys;
 #pragma unroll
                 for (int i = 0; i < TILES; ++i) {
-                    if (j >= tile_lo[i] && j <= tile_hi[i]) {
-                        if (!wait(&sm.p_full[i], p_phase[i])) break;
-                        p_phase[i] ^= 1;
-                        tc_fence_after();
-                        product_o(i, j, n + 1);
-                    }
-                    if (j < hi && j + 1 >= tile_lo[i] && j + 1 <= tile_hi[i]) {
-                        if (!kv_wait(n + 2)) break;
-                        tc_fence_after();
-                        product_s(i, j + 1, n + 2);
-                    }
+                    bool ready = ready_s;
+                    ready_s = false;
+                    if (j < hi && j + 1 >= tile_lo[i] && j + 1 <= tile_hi[i])
+                        product_s(i, j + 1, keys, ready, [&] { ready = o_ready(i, values); });
+                    else ready = false;
+                    // (The next S: of the other tile, or of the next block.)
+                    if (j >= tile_lo[i] && j <= tile_hi[i])
+                        product_o(i, j, values, ready, [&] {
+                            if (i + 1 < TILES) ready_s = s_ready(i + 1, keys);
+                            else if (j + 1 < hi) ready_s = s_ready(0, values.next());
+                        });
                 }
-                if (!ok) break;
-                kv_done(n + 1);
-                if (j < hi) kv_done(n + 2);
+                if (j < hi) tc_commit(&sm.kv_empty[keys.at], elected);
+                tc_commit(&sm.kv_empty[values.at], elected);
+                stage = values.next();
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
             }
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
         }
     }
     } else {
@@ -467,30 +636,34 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
         // ---- softmax of tile i, this thread's row of it
         const int i = warp / 4, tid = threadIdx.x & 127;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) * 32 << 16;
-        const uint32_t s_at = tmem + lanes + i * kRows, o_at = tmem + lanes + P::kColumnsO + i * kRows;
+        const uint32_t s_at = tmem + lanes + P::kColumnsS + (P::kBuffers == 2 ? i * kRows : 0);
+        const uint32_t p_at = tmem + lanes + P::kColumnsP + i * (kRows / 2), o_at = tmem + lanes + P::kColumnsO + i * D;
         unsigned n = 0, looks = 0;
         uint32_t s_phase = 0, pv_phase = 0;   // of the next S, of the next P V
         bool ok = true;
         const float scale = p.scale_log2;
-        for (int64_t index = blockIdx.x; ok && index < p.items; index += gridDim.x) {
-            const Item it = item_at<TILES>(p, index);
-            int all_lo, all_hi;
+        for (unsigned k = 0; ok && next_item(k, &it); ++k) {
             blocks_of<TILES>(it, &all_lo, &all_hi);
-            const int lo = it.lo[i], hi = it.hi[i], row0 = it.row[i], row = row0 + tid;
+            const int lo = i ? it.lo[1] : it.lo[0], hi = i ? it.hi[1] : it.hi[0], row0 = i ? it.row[1] : it.row[0];
+            const int head = i ? it.head[1] : it.head[0], row = row0 + tid;
             const int klo = p.window > 0 && row >= p.window ? row - static_cast<int>(p.window) + 1 : 0;
             float ref = 0.0f, lim = -INFINITY;
             float2 sum[4] = {f2(0.0f), f2(0.0f), f2(0.0f), f2(0.0f)};
 #pragma unroll 1
             for (int j = lo; j <= hi; ++j) {
                 const int key0 = j * kRows;
-                if (!(ok = __all_sync(0xffffffffu, mbar_wait(sm, &sm.s_full[i], s_phase)))) break;
+                ok &= mbar_wait(sm, &sm.s_full[i], s_phase);
                 s_phase ^= 1;
+                __syncwarp();
                 tc_fence_after();
                 uint32_t s[4][32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32(s[c], s_at + c * 32);
                 tc_wait_ld();
-                const bool masked = key0 + kRows - 1 > row0 || (p.window > 0 && key0 < row0 + kRows - p.window);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.s_free[P::kBuffers == 2 ? i : 0]);
+                const bool masked = some_masked(p, row0, key0);
                 if (masked) {
 #pragma unroll
                     for (int c = 0; c < kRows; ++c)
@@ -505,6 +678,10 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
                     m[c] = fmaxf(m[c], __uint_as_float(s[c][31]));
                 }
                 const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * scale;
+                if (j > lo) {   // the block before is in O, and its P read
+                    ok &= mbar_wait(sm, &sm.pv_done[i], pv_phase ^ 1);
+                    tc_fence_after();
+                }
                 if (__any_sync(0xffffffffu, top > lim)) {
                     const float t = fmaxf(top, lim - kLazy), next = t == -INFINITY ? 0.0f : t;   // (lim - kLazy: the kept maximum)
                     const float old = lim == -INFINITY ? 0.0f : ex2(ref - next);
@@ -512,11 +689,7 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
                     lim = t + kLazy;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) sum[c] = __fmul2_rn(sum[c], f2(old));
-                    if (j > lo) {
-                        if (!(ok = __all_sync(0xffffffffu, mbar_wait(sm, &sm.pv_done[i], pv_phase ^ 1)))) break;
-                        tc_fence_after();
-                        rescale<D>(o_at, old);
-                    }
+                    if (j > lo) rescale<D>(o_at, old);
                 }
                 const float2 scale2 = f2(scale), ref2 = f2(-ref);
 #pragma unroll
@@ -529,13 +702,12 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
                         sum[e / 2 % 4] = __fadd2_rn(sum[e / 2 % 4], x);
                         packed[e / 2] = pack_bf16x2(x);
                     }
-                    tmem_st16(packed, s_at + c * 16);
+                    tmem_st16(packed, p_at + c * 16);
                 }
-                tc_wait_st();
                 if (masked) {
                     // V's rows of this block: any value that is not finite?
-                    const unsigned stage = n + 2 * (j - all_lo) + 1;
-                    ok = __all_sync(0xffffffffu, mbar_wait(sm, &sm.kv_full[stage % P::kStages], stage / P::kStages & 1));
+                    const unsigned stage = n + 2 * (j - all_lo) + (j < all_hi ? 2 : 1);
+                    ok &= mbar_wait(sm, &sm.kv_full[stage % P::kStages], stage / P::kStages & 1);
                     uint32_t odd = 0;
                     const char* v = kv_stage(stage);
 #pragma unroll
@@ -551,23 +723,21 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
                     if (odd != 0) sm.odd[i] = looks;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sm.looked[i]);
-                    if (!(ok = __all_sync(0xffffffffu, ok && mbar_wait(sm, &sm.looked[i], (looks & 1) ^ 1)))) break;
+                    ok &= mbar_wait(sm, &sm.looked[i], (looks & 1) ^ 1);
+                    __syncwarp();
                     const bool any = sm.odd[i] == looks;
                     if (any) {
-                        if (j > lo) {
-                            if (!(ok = __all_sync(0xffffffffu, mbar_wait(sm, &sm.pv_done[i], pv_phase ^ 1)))) break;
-                            tc_fence_after();
-                        }
-                        product_by_hand<D>(v, s_at, o_at, key0, klo, row, j > lo);
+                        tc_wait_st();
+                        product_by_hand<D>(v, p_at, o_at, key0, klo, row, j > lo);
                     }
                     if (tid == 0) sm.by_hand[i] = any;
-                } else if (tid == 0) {
-                    sm.by_hand[i] = 0;
                 }
                 pv_phase ^= 1;
+                tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm.p_full[i]);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
             }
             if (ok && lo <= hi) {
                 // ---- the tile's rows of the output
@@ -576,7 +746,7 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
                 const float2 both = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
                 const float total = both.x + both.y, f = total == 0.0f ? 0.0f : 1.0f / total;   // (0: every logit is -inf)
                 const bool in = ok && row < it.len;
-                char* out = static_cast<char*>(p.out) + ((it.base + row) * p.n_q_heads + it.head[i]) * (D * 2);
+                char* out = static_cast<char*>(p.out) + (static_cast<int64_t>(it.base + row) * p.n_q_heads + head) * (D * 2);
 #pragma unroll 1
                 for (int d0 = 0; d0 < D; d0 += 32) {
                     uint32_t o[32];
@@ -591,10 +761,10 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
                         }
                     }
                 }
-                if (in && p.lse) p.lse[(it.base + row) * p.n_q_heads + it.head[i]] = total == 0.0f ? -INFINITY : (ref + log2f(total)) * kLn2;
+                if (in && p.lse) p.lse[static_cast<int64_t>(it.base + row) * p.n_q_heads + head] = total == 0.0f ? -INFINITY : (ref + log2f(total)) * kLn2;
                 tc_fence_before();
             }
-            if (all_hi >= all_lo) n += 2 * (all_hi - all_lo + 1);
+            n += 2 * (all_hi - all_lo + 1);
         }
     }
     tc_fence_before();
@@ -604,23 +774,22 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
 }
 
 template <int D>
-cudaError_t launch(const PromptParams& p, int sms, cudaStream_t s) {
+cudaError_t launch(const PromptParams& p, cudaStream_t s) {
     using P = Prompt<D>;
     const cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kShared);
     if (e != cudaSuccess) return e;
-    const unsigned grid = static_cast<unsigned>(p.items < sms ? p.items : sms);
-    return kv_launch(prompt_kernel<D>, grid, P::kThreads, P::kShared, 1, s, p);
+    return kv_launch(prompt_kernel<D>, static_cast<unsigned>(p.items), P::kThreads, P::kShared, 1, s, p);
 }
 
 }  // namespace
 
 int prompt_tiles(int head_dim) { return head_dim <= 128 ? 2 : 1; }
 
-cudaError_t launch_prompt(const PromptParams& p, int sms, cudaStream_t s) {
+cudaError_t launch_prompt(const PromptParams& p, cudaStream_t s) {
     switch (p.head_dim) {
-        case 64: return launch<64>(p, sms, s);
-        case 128: return launch<128>(p, sms, s);
-        case 256: return launch<256>(p, sms, s);
+        case 64: return launch<64>(p, s);
+        case 128: return launch<128>(p, s);
+        case 256: return launch<256>(p, s);
     }
     return cudaErrorInvalidValue;
 }

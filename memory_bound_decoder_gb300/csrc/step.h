@@ -53,7 +53,7 @@ struct PromptParams {
     int64_t window;             // 0: no window
     int64_t slots;              // numbers of row tiles, some of them no tile's
     int64_t units;              // query heads, or pairs of them, that share a row tile's number
-    int64_t items;              // slots * units
+    int64_t items;              // slots * units, at most 2^31 - 1: the grid
     float scale_log2;           // |scale| * log2(e), not 0
     int negate;                 // the scale is negative
     int pair_rows;              // a CTA's two tiles are neighbours in the rows, not two heads
@@ -63,7 +63,7 @@ struct PromptParams {
 };
 
 int prompt_tiles(int head_dim);   // tiles of 128 query rows that a CTA works on at a time
-cudaError_t launch_prompt(const PromptParams& p, int sms, cudaStream_t s);
+cudaError_t launch_prompt(const PromptParams& p, cudaStream_t s);
 cudaError_t device_error_flags_prompt(unsigned int* flags, bool clear);
 cudaError_t launch_rotary(const RotaryParams& p, int sms, cudaStream_t s);
 cudaError_t launch_kv_resize(const ResizeParams& p, cudaStream_t s);

@@ -105,6 +105,10 @@ mbd_status mbd_prompt_attention(void* out, const void* q, int64_t q_stride, cons
     mbd_status st = check_stride(&q_stride, width);
     if (st == MBD_OK) st = check_stride(&kv_stride, kv_width);
     if (st != MBD_OK) return st;
+    const int tiles = mbd::prompt_tiles(static_cast<int>(head_dim));
+    const bool pair_rows = tiles == 2 && n_q_heads / n_kv_heads % 2 != 0;
+    const int64_t slots = (n_tokens >> (pair_rows ? 8 : 7)) + n_seqs, units = pair_rows || tiles == 1 ? n_q_heads : n_q_heads / 2;
+    if (slots * units > INT32_MAX) return MBD_ERR_UNSUPPORTED;
     if (n_seqs == 0 || n_tokens == 0) return MBD_OK;
     if (!out || !q || !k || !v || !cu_tokens) return MBD_ERR_INVALID_ARG;
     if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(cu_tokens, 4) || !aligned(lse, 4))
@@ -128,16 +132,15 @@ mbd_status mbd_prompt_attention(void* out, const void* q, int64_t q_stride, cons
     p.n_q_heads = static_cast<int>(n_q_heads);
     p.group = static_cast<int>(n_q_heads / n_kv_heads);
     p.head_dim = static_cast<int>(head_dim);
-    const int tiles = mbd::prompt_tiles(p.head_dim);
-    p.pair_rows = tiles == 2 && p.group % 2 != 0;
-    p.slots = (n_tokens >> (p.pair_rows ? 8 : 7)) + n_seqs;
-    p.units = p.pair_rows || tiles == 1 ? n_q_heads : n_q_heads / 2;
-    p.items = p.slots * p.units;
+    p.pair_rows = pair_rows;
+    p.slots = slots;
+    p.units = units;
+    p.items = slots * units;
     p.negate = scale < 0.0f;
     // A scale of 0 makes every logit 0, also in units of log2: the least factor does, and leaves -inf where it is.
     p.scale_log2 = std::fmax(std::fabs(scale * 1.44269504088896341f), 0x1p-149f);
     return static_cast<mbd_status>(mbd::kv_finish_launch(
-        mbd::launch_prompt(p, mbd::kv_sm_count(), reinterpret_cast<cudaStream_t>(stream))));
+        mbd::launch_prompt(p, reinterpret_cast<cudaStream_t>(stream))));
 }
 
 mbd_status mbd_rotary(void* out, int64_t out_stride, const void* x, int64_t x_stride, const uint64_t* turns, float amplitude,
