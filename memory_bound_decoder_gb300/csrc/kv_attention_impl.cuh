@@ -90,6 +90,16 @@ __device__ __forceinline__ uint2 ld8(const char* p) {
     return v;
 }
 
+// N bytes (4, 8 or 16) into shared memory on their own, or zeros.
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t to, const char* from, bool in) {
+    const int bytes = in ? N : 0;
+    if constexpr (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(to), "l"(from), "r"(bytes), "n"(N) : "memory");
+}
+
 template <bool F16>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
@@ -168,6 +178,9 @@ struct Shape {
     static constexpr int kVs = kF4 && kVd > 16 ? kVd / 16 : 1;
     static constexpr int kStep = step_keys(D, STORE, NT);
     static constexpr int kGroups = kStep / 16;
+    // What a warp's step takes in shared memory where it is staged there: each lane's vectors, and the scales as they lie.
+    static constexpr int kStageK = 0, kStageV = kStep * kRow, kStageKb = 2 * kStep * kRow, kStageVb = kStageKb + kStep * (D / 16);
+    static constexpr int kStage = kStageVb + kStep * (D / 16);
     static constexpr int kTile = kStep * kWarps;
     static constexpr int kK = D / 16;                        // k-steps of S^T, m-tiles of O^T
 };
@@ -387,6 +400,12 @@ __device__ __forceinline__ void join_two(const AttendParams& p, const Cut& cut, 
                             m, t, mo);
 }
 
+// Where a step's keys and values go through shared memory: NVFP4, in pages of at least a group. A step of it is as many
+// instructions as in the other formats for half of their bytes, and the registers that hold a step of loads are not enough to keep the
+// next values on their way during all of this step's: 32 sequences of up to 8192 tokens take 52.7 us without it.
+template <int STORE, int GRAN>
+constexpr bool kStaged = STORE == kKvNvfp4 && GRAN == 16;
+
 // GRAN: keys that share a lookup in the page table: 16 (a group), 8 (half of one), or 1 for pages of fewer than 8 slots
 // (SMALL), whose rows' places lanes look up and hand to one another.
 template <int D, int STORE, int NT, int GRAN>
@@ -397,7 +416,9 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
     constexpr bool SMALL = GRAN == 1;
     constexpr int H = GRAN == 8 ? 2 : 1;   // lookups of a group
     constexpr int HT = 8 * NT, NG = S::kGroups, KV = S::kKv, VV = S::kVv, VW = S::kVw, KK = S::kK;
+    constexpr bool STAGED = kStaged<STORE, GRAN>;
     __shared__ MergeSmem<D, HT> sm;
+    extern __shared__ __align__(16) char stages[];   // STAGED: two of each warp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const int heads = p.c.n_kv_heads * p.chunks;
     pdl_trigger();
@@ -670,6 +691,84 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
                 if ((live_next[g] >> (2 * c + kRows[i])) & 1u) load_v_row(g, i, from, blocks);
             }
     };
+    // STAGED: the step whose rows are placed, into buffer b of the warp.
+    const uint32_t stage_lane = STAGED ? smem_addr(stages) + warp * 2 * S::kStage : 0;
+    auto stage = [&](int b) {
+        const uint32_t to = stage_lane + b * S::kStage;
+        __syncwarp();   // every lane has read what was there
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < KV; ++j)
+                    copy_async<S::kKb>(to + S::kStageK + (((g * 2 + i) * KV + j) * 32 + lane) * S::kKb,
+                                       k_lane + offset(g, r + 8 * i, 8 * i) + j * 4 * S::kKb, (live_next[g] >> (r + 8 * i)) & 1u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                constexpr int kRows[4] = {0, 1, 8, 9};
+#pragma unroll
+                for (int j = 0; j < VV; ++j)
+                    copy_async<S::kVb>(to + S::kStageV + (((g * 4 + i) * VV + j) * 32 + lane) * S::kVb,
+                                       v_lane + offset(g, 2 * c + kRows[i], kRows[i]) + j * 8 * S::kVb,
+                                       (live_next[g] >> (2 * c + kRows[i])) & 1u);
+            }
+            // A group's scales lie together: 16 rows of kBlocks bytes.
+            constexpr int kPiece = kBlocks > 8 ? 8 : 4, kPieces = 16 * kBlocks / kPiece;
+            if (lane < kPieces) {
+                const bool in = (live_next[g] >> (lane * kPiece / kBlocks)) & 1u;
+                copy_async<kPiece>(to + S::kStageKb + g * 16 * kBlocks + lane * kPiece, static_cast<const char*>(p.c.k) + block[g][0] + lane * kPiece, in);
+                copy_async<kPiece>(to + S::kStageVb + g * 16 * kBlocks + lane * kPiece, static_cast<const char*>(p.c.v) + block[g][0] + lane * kPiece, in);
+            }
+        }
+    };
+    auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+    // This lane's vectors of the staged step, as load_k and load_v leave them.
+    auto unstage_k = [&](int b, int g, int j) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const char* from = stages + (warp * 2 + b) * S::kStage;
+            const char* at = from + S::kStageK + (((g * 2 + i) * KV + j) * 32 + lane) * S::kKb;
+            if constexpr (S::kKw == 4) {
+                const uint4 x = *reinterpret_cast<const uint4*>(at);
+                kx[g][i][j][0] = x.x;
+                kx[g][i][j][1] = x.y;
+                kx[g][i][j][2] = x.z;
+                kx[g][i][j][3] = x.w;
+            } else {
+                const uint2 x = *reinterpret_cast<const uint2*>(at);
+                kx[g][i][j][0] = x.x;
+                kx[g][i][j][1] = x.y;
+            }
+            const char* blocks = from + S::kStageKb + (g * 16 + r + 8 * i) * kBlocks + (j * 4 + c) * S::kKs;
+            kb[g][i][j] = S::kKs == 2 ? *reinterpret_cast<const uint16_t*>(blocks) : *reinterpret_cast<const uint8_t*>(blocks);
+        }
+    };
+    auto unstage_v = [&](int b, int g) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < VV; ++j) {
+                constexpr int kRows[4] = {0, 1, 8, 9};
+                const char* from = stages + (warp * 2 + b) * S::kStage;
+                const char* at = from + S::kStageV + (((g * 4 + i) * VV + j) * 32 + lane) * S::kVb;
+                if constexpr (VW == 4) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(at);
+                    vx[g][i][j][0] = x.x;
+                    vx[g][i][j][1] = x.y;
+                    vx[g][i][j][2] = x.z;
+                    vx[g][i][j][3] = x.w;
+                } else if constexpr (VW == 2) {
+                    const uint2 x = *reinterpret_cast<const uint2*>(at);
+                    vx[g][i][j][0] = x.x;
+                    vx[g][i][j][1] = x.y;
+                } else {
+                    vx[g][i][j][0] = *reinterpret_cast<const uint32_t*>(at);
+                }
+                const char* blocks = from + S::kStageVb + (g * 16 + 2 * c + kRows[i]) * kBlocks + (j * 8 + r) * S::kVd / 16;
+                vb[g][i][j] = S::kVs == 2 ? *reinterpret_cast<const uint16_t*>(blocks) : *reinterpret_cast<const uint8_t*>(blocks);
+            }
+    };
     // Query heads of the chunk, lane r's: bf16 in the order of K's vectors (E4M3: 16 elements a vector; E2M1: 32, or 16).
     auto load_q = [&] {
 #pragma unroll
@@ -758,10 +857,40 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
 
     // Starts on the part of an item that begins at cur.key: `tiles` of the `left` tiles that the item has from there.
     int left, tiles;
+    int buffer = 0;   // STAGED: where the next step to be worked on lies
     auto start = [&] {
         left = (cur.len - cur.key + S::kTile - 1) / S::kTile;
         tiles = static_cast<int>(min(static_cast<int64_t>(left), (end - unit + 1) / 2));
         load_pages(cur.key);
+        if constexpr (STAGED) {   // the first two steps
+            int page0[NG];
+#pragma unroll
+            for (int g = 0; g < NG; ++g) page0[g] = page[g][0];
+            if (tiles > 1) load_pages(cur.key + S::kTile);
+            load_q();
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const int page1 = page[g][0];
+                page[g][0] = page0[g];
+                page0[g] = page1;
+            }
+            place(cur.key);
+            stage(buffer);
+            commit();
+            full = full_next;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                live[g] = live_next[g];
+                page[g][0] = page0[g];
+            }
+            if (tiles > 1) {
+                place(cur.key + S::kTile);
+                stage(buffer ^ 1);
+            }
+            commit();
+            if (tiles > 2) load_pages(cur.key + 2 * S::kTile);
+            return;
+        }
         load_q();
         place(cur.key);
         load_k();
@@ -777,10 +906,15 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
 #pragma unroll 1
         for (int tile = cur.key; tile <= last_tile; tile += S::kTile) {
         const bool more = tile < last_tile;
-        full = full_next;
+        if constexpr (STAGED) {
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            __syncwarp();   // (lanes read scales that others copied)
+        } else {
+            full = full_next;
+        }
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            live[g] = live_next[g];
+            if constexpr (!STAGED) live[g] = live_next[g];
             if constexpr (kDyn)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -800,6 +934,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
         for (int j = 0; j < KV; ++j)
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
+                if constexpr (STAGED) unstage_k(buffer, g, j);
                 const auto &a = kx[g][0][j], &b = kx[g][1][j];
                 if constexpr (kF4) {
                     // Values of a block: codes times its scale, exact in f16 (2 and 4 significant bits, 2^-10 .. 2688).
@@ -839,9 +974,11 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
                 }
             }
         if (more) {
-            place(tile + S::kTile);
-            load_k();
-            if (tile + S::kTile < last_tile) load_pages(tile + 2 * S::kTile);
+            if constexpr (!STAGED) {
+                place(tile + S::kTile);
+                load_k();
+                if (tile + S::kTile < last_tile) load_pages(tile + 2 * S::kTile);
+            }
             if (kAhead > 0 && tile + (kAhead + 1) * S::kTile <= last_tile) warm(cur, tile + (kAhead + 1) * S::kTile);
         }
 
@@ -950,6 +1087,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
                     }
                 }
             }
+            if constexpr (STAGED) unstage_v(buffer, g);
 #pragma unroll
             for (int j = 0; j < VV; ++j)
 #pragma unroll
@@ -998,7 +1136,20 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
                     }
                 }
         }
-        if (more) load_v();
+        if constexpr (STAGED) {   // the step after the next one takes this one's place
+            full = full_next;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) live[g] = live_next[g];
+            if (tile + S::kTile < last_tile) {
+                place(tile + 2 * S::kTile);
+                stage(buffer);
+                if (tile + 2 * S::kTile < last_tile) load_pages(tile + 3 * S::kTile);
+            }
+            commit();
+            buffer ^= 1;
+        } else if (more) {
+            load_v();
+        }
         }
 
         // The part is over: on to the next item before its end is dealt with.
@@ -1133,7 +1284,14 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
 
 template <int D, int STORE, int NT>
 cudaError_t launch_nt(const AttendParams& p, cudaStream_t s) {
-    if (p.c.page_shift >= 4) return kv_launch(kv_attend_kernel<D, STORE, NT, 16>, p.grid, kThreads, 0, 1, s, p);
+    if (p.c.page_shift >= 4) {
+        constexpr int kShared = kStaged<STORE, 16> ? kWarps * 2 * Shape<D, STORE, NT>::kStage : 0;
+        if (kShared > 0) {
+            const cudaError_t e = cudaFuncSetAttribute(kv_attend_kernel<D, STORE, NT, 16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kShared);
+            if (e != cudaSuccess) return e;
+        }
+        return kv_launch(kv_attend_kernel<D, STORE, NT, 16>, p.grid, kThreads, kShared, 1, s, p);
+    }
     if (p.c.page_shift == 3) return kv_launch(kv_attend_kernel<D, STORE, NT, 8>, p.grid, kThreads, 0, 1, s, p);
     return kv_launch(kv_attend_kernel<D, STORE, NT, 1>, p.grid, kThreads, 0, 1, s, p);
 }
