@@ -178,7 +178,7 @@ struct Shape {
     static constexpr int kVs = kF4 && kVd > 16 ? kVd / 16 : 1;
     static constexpr int kStep = step_keys(D, STORE, NT);
     static constexpr int kGroups = kStep / 16;
-    // What a warp's step takes in shared memory where it is staged there: each lane's vectors, and the scales as they lie.
+    // What a warp's step takes in shared memory where it is staged there: rows of K, of V, and the scales of their blocks.
     static constexpr int kStageK = 0, kStageV = kStep * kRow, kStageKb = 2 * kStep * kRow, kStageVb = kStageKb + kStep * (D / 16);
     static constexpr int kStage = kStageVb + kStep * (D / 16);
     static constexpr int kTile = kStep * kWarps;
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
     constexpr int HT = 8 * NT, NG = S::kGroups, KV = S::kKv, VV = S::kVv, VW = S::kVw, KK = S::kK;
     constexpr bool STAGED = kStaged<STORE, GRAN>;
     __shared__ MergeSmem<D, HT> sm;
-    extern __shared__ __align__(16) char stages[];   // STAGED: two of each warp
+    extern __shared__ __align__(128) char stages[];   // STAGED: two of each warp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const int heads = p.c.n_kv_heads * p.chunks;
     pdl_trigger();
@@ -691,44 +691,60 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
                 if ((live_next[g] >> (2 * c + kRows[i])) & 1u) load_v_row(g, i, from, blocks);
             }
     };
-    // STAGED: the step whose rows are placed, into buffer b of the warp.
-    const uint32_t stage_lane = STAGED ? smem_addr(stages) + warp * 2 * S::kStage : 0;
+    // STAGED: the step whose rows are placed, into buffer b of the warp. A group's rows lie together in the pool, so its lanes
+    // copy 16 bytes each, whosever they are. In shared memory the 16-byte pieces of each 128 bytes change places by line, so that the
+    // lanes that read together, of rows 2c for V and r for K, find them in different banks.
+    auto swap = [](int piece) {   // where piece `piece` of a group goes (8 rows on: the same, 8 rows on)
+        const int line = piece >> 3;
+        return piece ^ (S::kRow == 128 ? (line & 6) ^ ((line & 1) << 2) : (S::kRow == 64 ? (line & 3) << 1 : (line & 1) << 1));
+    };
+    constexpr int kGroupBytes = 16 * S::kRow, kGroupBlocks = 16 * kBlocks;
     auto stage = [&](int b) {
-        const uint32_t to = stage_lane + b * S::kStage;
+        const uint32_t to = smem_addr(stages) + (warp * 2 + b) * S::kStage;
         __syncwarp();   // every lane has read what was there
+        constexpr int kPiece = kBlocks > 8 ? 8 : 4, kPieces = kGroupBlocks / kPiece;   // of a group's scales
+        auto copy = [&](bool whole) {
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
+            for (int g = 0; g < NG; ++g) {
+                const char *k = static_cast<const char*>(p.c.k) + row[g][0] + lane * 16, *v = static_cast<const char*>(p.c.v) + row[g][0] + lane * 16;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int j = 0; j < KV; ++j)
-                    copy_async<S::kKb>(to + S::kStageK + (((g * 2 + i) * KV + j) * 32 + lane) * S::kKb,
-                                       k_lane + offset(g, r + 8 * i, 8 * i) + j * 4 * S::kKb, (live_next[g] >> (r + 8 * i)) & 1u);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                constexpr int kRows[4] = {0, 1, 8, 9};
-#pragma unroll
-                for (int j = 0; j < VV; ++j)
-                    copy_async<S::kVb>(to + S::kStageV + (((g * 4 + i) * VV + j) * 32 + lane) * S::kVb,
-                                       v_lane + offset(g, 2 * c + kRows[i], kRows[i]) + j * 8 * S::kVb,
-                                       (live_next[g] >> (2 * c + kRows[i])) & 1u);
+                for (int m = 0; m < kGroupBytes / 512; ++m) {
+                    const int piece = m * 32 + lane;
+                    const uint32_t at = to + g * kGroupBytes + swap(piece) * 16;
+                    const bool in = whole || ((live_next[g] >> (piece * 16 / S::kRow)) & 1u);
+                    copy_async<16>(at + S::kStageK, k + m * 512, in);
+                    copy_async<16>(at + S::kStageV, v + m * 512, in);
+                }
+                if (kPieces == 32 || lane < kPieces) {
+                    const bool in = whole || ((live_next[g] >> (lane * kPiece / kBlocks)) & 1u);
+                    const uint32_t at = to + g * kGroupBlocks + lane * kPiece;
+                    copy_async<kPiece>(at + S::kStageKb, static_cast<const char*>(p.c.k) + block[g][0] + lane * kPiece, in);
+                    copy_async<kPiece>(at + S::kStageVb, static_cast<const char*>(p.c.v) + block[g][0] + lane * kPiece, in);
+                }
             }
-            // A group's scales lie together: 16 rows of kBlocks bytes.
-            constexpr int kPiece = kBlocks > 8 ? 8 : 4, kPieces = 16 * kBlocks / kPiece;
-            if (lane < kPieces) {
-                const bool in = (live_next[g] >> (lane * kPiece / kBlocks)) & 1u;
-                copy_async<kPiece>(to + S::kStageKb + g * 16 * kBlocks + lane * kPiece, static_cast<const char*>(p.c.k) + block[g][0] + lane * kPiece, in);
-                copy_async<kPiece>(to + S::kStageVb + g * 16 * kBlocks + lane * kPiece, static_cast<const char*>(p.c.v) + block[g][0] + lane * kPiece, in);
-            }
-        }
+        };
+        if (full_next) copy(true);
+        else copy(false);
     };
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
     // This lane's vectors of the staged step, as load_k and load_v leave them.
-    auto unstage_k = [&](int b, int g, int j) {
+    int k_places[KV], v_places[2][VV];   // of row r of K, and rows 2c and 2c + 1 of V; 8 rows on: 8 kRow bytes on
+#pragma unroll
+    for (int j = 0; j < KV; ++j) {
+        const int at = r * S::kRow + (j * 4 + c) * S::kKb;
+        k_places[j] = STAGED ? swap(at / 16) * 16 + at % 16 : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < VV; ++j)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const char* from = stages + (warp * 2 + b) * S::kStage;
-            const char* at = from + S::kStageK + (((g * 2 + i) * KV + j) * 32 + lane) * S::kKb;
+            const int at = (2 * c + i) * S::kRow + (j * 8 + r) * S::kVb;
+            v_places[i][j] = STAGED ? swap(at / 16) * 16 + at % 16 : 0;
+        }
+    auto unstage_k = [&](const char* from, int g, int j) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const char* at = from + S::kStageK + g * kGroupBytes + i * 8 * S::kRow + k_places[j];
             if constexpr (S::kKw == 4) {
                 const uint4 x = *reinterpret_cast<const uint4*>(at);
                 kx[g][i][j][0] = x.x;
@@ -744,14 +760,13 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
             kb[g][i][j] = S::kKs == 2 ? *reinterpret_cast<const uint16_t*>(blocks) : *reinterpret_cast<const uint8_t*>(blocks);
         }
     };
-    auto unstage_v = [&](int b, int g) {
+    auto unstage_v = [&](const char* from, int g) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < VV; ++j) {
                 constexpr int kRows[4] = {0, 1, 8, 9};
-                const char* from = stages + (warp * 2 + b) * S::kStage;
-                const char* at = from + S::kStageV + (((g * 4 + i) * VV + j) * 32 + lane) * S::kVb;
+                const char* at = from + S::kStageV + g * kGroupBytes + i / 2 * 8 * S::kRow + v_places[i % 2][j];
                 if constexpr (VW == 4) {
                     const uint4 x = *reinterpret_cast<const uint4*>(at);
                     vx[g][i][j][0] = x.x;
@@ -906,6 +921,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
 #pragma unroll 1
         for (int tile = cur.key; tile <= last_tile; tile += S::kTile) {
         const bool more = tile < last_tile;
+        const char* const staged = stages + (warp * 2 + buffer) * S::kStage;
         if constexpr (STAGED) {
             asm volatile("cp.async.wait_group 1;" ::: "memory");
             __syncwarp();   // (lanes read scales that others copied)
@@ -934,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
         for (int j = 0; j < KV; ++j)
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-                if constexpr (STAGED) unstage_k(buffer, g, j);
+                if constexpr (STAGED) unstage_k(staged, g, j);
                 const auto &a = kx[g][0][j], &b = kx[g][1][j];
                 if constexpr (kF4) {
                     // Values of a block: codes times its scale, exact in f16 (2 and 4 significant bits, 2^-10 .. 2688).
@@ -1087,7 +1103,7 @@ __global__ void __launch_bounds__(kThreads, resident_ctas(D, STORE, NT))
                     }
                 }
             }
-            if constexpr (STAGED) unstage_v(buffer, g);
+            if constexpr (STAGED) unstage_v(staged, g);
 #pragma unroll
             for (int j = 0; j < VV; ++j)
 #pragma unroll
