@@ -65,7 +65,7 @@ struct PromptParams {
 int prompt_tiles(int head_dim);   // tiles of 128 query rows that a CTA works on at a time
 cudaError_t launch_prompt(const PromptParams& p, cudaStream_t s);
 cudaError_t device_error_flags_prompt(unsigned int* flags, bool clear);
-cudaError_t launch_rotary(const RotaryParams& p, int sms, cudaStream_t s);
+cudaError_t launch_rotary(const RotaryParams& p, cudaStream_t s);
 cudaError_t launch_kv_resize(const ResizeParams& p, cudaStream_t s);
 cudaError_t device_error_flags_kv_pages(unsigned int* flags, bool clear);
 

@@ -177,7 +177,7 @@ mbd_status mbd_rotary(void* out, int64_t out_stride, const void* x, int64_t x_st
     p.interleaved = layout == MBD_ROTARY_INTERLEAVED;
     p.units = static_cast<int>((in_place ? rotary_dim : head_dim) / 16);
     return static_cast<mbd_status>(mbd::kv_finish_launch(
-        mbd::launch_rotary(p, mbd::kv_sm_count(), reinterpret_cast<cudaStream_t>(stream))));
+        mbd::launch_rotary(p, reinterpret_cast<cudaStream_t>(stream))));
 }
 
 mbd_status mbd_rotary_table(uint64_t* turns, float* amplitude, int64_t rotary_dim, const mbd_rotary_scaling* scaling) {
