@@ -22,48 +22,45 @@ constexpr int kResizeWarps = kResizeThreads / 32;
 // Of each sequence: length before and after, tokens seen before, and how many tokens, pages taken and pages given up
 // come before it.
 struct ResizeSmem {
-    int64_t sum[2][kResizeWarps];
-    int64_t carry[2];
+    int64_t sum[3][kResizeWarps];
+    int64_t carry[3];
 };
 constexpr int kResizeArrays = 6;
 constexpr size_t resize_shared(int64_t n) { return static_cast<size_t>(n + 1) * kResizeArrays * sizeof(int32_t); }
 
-// Exclusive sums of a and b over the CTA's threads, on top of sm.carry, which grows by the totals.
-__device__ __forceinline__ void scan_block(ResizeSmem& sm, int64_t a, int64_t b, int64_t* before_a, int64_t* before_b) {
+// Exclusive sums of N values over the CTA's threads, on top of sm.carry, which grows by the totals.
+template <int N>
+__device__ __forceinline__ void scan_block(ResizeSmem& sm, const int64_t (&own)[N], int64_t (&before)[N]) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int64_t x = a, y = b;
+    int64_t upto[N];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) {
-            x += u;
-            y += v;
+    for (int k = 0; k < N; ++k) {
+        upto[k] = own[k];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, upto[k], o);
+            if (lane >= o) upto[k] += x;
         }
-    }
-    if (lane == 31) {
-        sm.sum[0][warp] = x;
-        sm.sum[1][warp] = y;
+        if (lane == 31) sm.sum[k][warp] = upto[k];
     }
     __syncthreads();
-    int64_t u = sm.sum[0][lane], v = sm.sum[1][lane];
-    const int64_t mine_u = u, mine_v = v;
+    int64_t base[N];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t s = __shfl_up_sync(0xffffffffu, u, o), t = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) {
-            u += s;
-            v += t;
+    for (int k = 0; k < N; ++k) {
+        const int64_t mine = sm.sum[k][lane];
+        int64_t all = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, all, o);
+            if (lane >= o) all += x;
         }
+        base[k] = sm.carry[k] + __shfl_sync(0xffffffffu, all - mine, warp);
+        before[k] = base[k] + upto[k] - own[k];
     }
-    const int64_t base_a = sm.carry[0] + __shfl_sync(0xffffffffu, u - mine_u, warp);
-    const int64_t base_b = sm.carry[1] + __shfl_sync(0xffffffffu, v - mine_v, warp);
-    *before_a = base_a + x - a;
-    *before_b = base_b + y - b;
     __syncthreads();
-    if (threadIdx.x == kResizeThreads - 1) {
-        sm.carry[0] = base_a + x;
-        sm.carry[1] = base_b + y;
-    }
+    if (threadIdx.x == kResizeThreads - 1)
+#pragma unroll
+        for (int k = 0; k < N; ++k) sm.carry[k] = base[k] + upto[k];
     __syncthreads();
 }
 
@@ -92,13 +89,24 @@ __global__ void __launch_bounds__(kResizeThreads) kv_resize_kernel(const __grid_
     const bool good = head >= 0 && head < p.n_pages && free_pages >= 0 && free_pages <= p.n_pages;
     if (!good && tid == 0) kv_bad_index();
     auto pages_of = [&](int64_t len) { return (len + (int64_t{1} << p.page_shift) - 1) >> p.page_shift; };
-    if (tid < 2) sm.carry[tid] = 0;
-    __syncthreads();
+    // Pages and rows that sequence b asks for.
+    auto asked = [&](int b, int64_t (&x)[2]) {
+        x[0] = x[1] = 0;
+        if (b >= n || new_len[b] <= old_len[b]) return;
+        x[0] = pages_of(new_len[b]) - pages_of(old_len[b]);
+        x[1] = static_cast<int64_t>(new_len[b]) - old_len[b];
+    };
+    auto restart = [&] {
+        __syncthreads();
+        if (tid < 3) sm.carry[tid] = 0;
+        __syncthreads();
+    };
+    restart();
 
-    // Lengths, and the pages that are given up. A sequence with a length out of range stays as it is.
+    // Lengths, and what is asked for and given up. A sequence with a length out of range stays as it is.
     for (int b0 = 0; b0 < n; b0 += kResizeThreads) {
         const int b = b0 + tid;
-        int64_t given = 0, unused;
+        int64_t x[3] = {0, 0, 0}, before[3];
         if (b < n) {
             const int32_t from = p.lens[b], to = p.want[b];
             const bool fits = from >= 0 && from <= p.capacity && to >= 0 && to <= p.capacity;
@@ -106,45 +114,41 @@ __global__ void __launch_bounds__(kResizeThreads) kv_resize_kernel(const __grid_
             old_len[b] = from;
             new_len[b] = fits && good ? to : from;
             seen[b] = p.seen ? p.seen[b] : from;
-            if (fits && good && to < from) given = pages_of(from) - pages_of(to);
+            int64_t of[2];
+            asked(b, of);
+            x[0] = of[0];
+            x[1] = of[1];
+            if (new_len[b] < from) x[2] = pages_of(from) - pages_of(to);
         }
-        int64_t before;
-        scan_block(sm, given, 0, &before, &unused);
-        if (b < n) given_before[b] = static_cast<int32_t>(before);   // (the host bounds the table's entries)
+        scan_block<3>(sm, x, before);
+        if (b < n) {   // (pages given up: the host bounds the table's entries; the others fit if all of them are granted)
+            taken_before[b] = static_cast<int32_t>(before[0]);
+            rows_before[b] = static_cast<int32_t>(before[1]);
+            given_before[b] = static_cast<int32_t>(before[2]);
+        }
     }
     // No more than n_pages have a place in the ring; more can only be pages that were named twice.
-    const int64_t all_given = sm.carry[0], given = min(all_given, good ? p.n_pages - free_pages : 0);
+    const int64_t all_given = sm.carry[2], given = min(all_given, good ? p.n_pages - free_pages : 0);
     if (all_given > given && tid == 0) kv_bad_index();
     const int64_t there = good ? free_pages + given : 0;
-    __syncthreads();
-    if (tid < 2) sm.carry[tid] = 0;
-    __syncthreads();
-
-    // What is asked for, in the order of the sequences, until it is more than there is.
-    for (int b0 = 0; b0 < n; b0 += kResizeThreads) {
-        const int b = b0 + tid;
-        int64_t pages = 0, rows = 0, pages_before, rows_asked;
-        if (b < n && new_len[b] > old_len[b]) {
-            pages = pages_of(new_len[b]) - pages_of(old_len[b]);
-            rows = static_cast<int64_t>(new_len[b]) - old_len[b];
+    if (sm.carry[0] > there || sm.carry[1] > p.n_tokens) {
+        // More is asked for than there is: granted in the order of the sequences, and summed anew.
+        restart();
+        for (int b0 = 0; b0 < n; b0 += kResizeThreads) {
+            int64_t x[2], before[2];
+            asked(b0 + tid, x);
+            scan_block<2>(sm, x, before);
+            if (x[1] > 0 && ((x[0] > 0 && before[0] + x[0] > there) || before[1] + x[1] > p.n_tokens))
+                new_len[b0 + tid] = old_len[b0 + tid];
         }
-        scan_block(sm, pages, rows, &pages_before, &rows_asked);
-        if (rows > 0 && ((pages > 0 && pages_before + pages > there) || rows_asked + rows > p.n_tokens)) new_len[b] = old_len[b];
-    }
-    __syncthreads();
-    if (tid < 2) sm.carry[tid] = 0;
-    __syncthreads();
-    for (int b0 = 0; b0 < n; b0 += kResizeThreads) {
-        const int b = b0 + tid;
-        int64_t pages = 0, rows = 0, pages_before, rows_before_b;
-        if (b < n && new_len[b] > old_len[b]) {
-            pages = pages_of(new_len[b]) - pages_of(old_len[b]);
-            rows = static_cast<int64_t>(new_len[b]) - old_len[b];
-        }
-        scan_block(sm, pages, rows, &pages_before, &rows_before_b);
-        if (b < n) {
-            taken_before[b] = static_cast<int32_t>(pages_before);
-            rows_before[b] = static_cast<int32_t>(rows_before_b);
+        restart();
+        for (int b0 = 0; b0 < n; b0 += kResizeThreads) {
+            int64_t x[2], before[2];
+            asked(b0 + tid, x);
+            scan_block<2>(sm, x, before);
+            if (b0 + tid >= n) continue;
+            taken_before[b0 + tid] = static_cast<int32_t>(before[0]);
+            rows_before[b0 + tid] = static_cast<int32_t>(before[1]);
         }
     }
     const int64_t taken = sm.carry[0], rows = sm.carry[1];
