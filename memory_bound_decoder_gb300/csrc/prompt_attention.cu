@@ -10,9 +10,27 @@
 //   - one thread issues S = Q K^T (both operands from shared memory) and O += P V (P from TMEM, V as it lies, its keys along
 //     the contraction), for the two tiles in turn;
 //   - a warpgroup for each tile, a thread for each row, takes S out of TMEM, keeps the row's running maximum and sum in its
-//     registers, and puts P = exp2(S - maximum), rounded to bf16, back over S.
-// While one tile's softmax runs, the tensor cores have the other tile's two products to do. The maximum that a row's sums are
-// relative to is kept until a logit exceeds it by 2^8, so O is rescaled in the first blocks and hardly ever after them.
+//     registers, and puts P = exp2(S - maximum), rounded to bf16, beside it.
+// While one tile's softmax runs, the tensor cores have the other tile's two products to do, and the next block's S is issued
+// ahead of this block's P V, so that it is there when the softmax is done. (At D 128 TMEM holds one S besides O and P of both
+// tiles: they use it in turn, as a row is read out at once.) The maximum that a row's sums are relative to is kept until a
+// logit exceeds it by 2^8, so O is rescaled in the first blocks and hardly ever after them.
+//
+// Work. An item is two row tiles of one or two query heads. The grid has a CTA for each, and the CTAs that run take the indexes
+// of those that have not begun from the launch (cluster launch control), one ahead: the tiles at the ends of the sequences, which
+// see the most keys, come first, so what is begun last is short (16 prompts of up to 2047 tokens, 32 and 8 heads, in an earlier
+// form of the loop: 245 us with items dealt out in advance, 209 so).
+//
+// Measured on one GB300 (operations of the places in view; 1932 TFLOP/s is the measured peak, 1727 under the power cap):
+//   one prompt of 16001 tokens, 64 and 8 heads of 128      2.64 ms, 1590 TFLOP/s (at the power cap: 1.75 GHz)
+//   16 prompts of 1..2047 tokens, 32 and 8 heads of 128    156 us, 1210 TFLOP/s
+//   24 prompts of 700..6001, windows of 1024, 16 heads of 64   498 us, 575 TFLOP/s
+//   one prompt of 4000 tokens, 16 and 4 heads of 256       123 us, 1070 TFLOP/s
+//   one prompt of 517 tokens, 12 and 2 heads of 128        15.8 us
+// A step of two tiles against one block takes 2650 cycles at D 128, 2048 of them the tensor cores', and 2400 at D 64, where the
+// products are 1024 and the softmax's own chain (TMEM, maximum, exp2 at 32 a cycle, bf16) is what is left. Tried and slower: two
+// threads a row (long 2.67 -> 3.60 ms: the four warps of a partition then do the same thing at the same time), P handed over in
+// halves, waits that sleep.
 //
 // P in bf16 is the operands' type (V is bf16, and both must agree); it is off by 2^-8 of itself, as the output's rounding is,
 // and adds up over a row's keys as a random walk does. Sums of P are kept in fp32 from the values before rounding.
@@ -434,203 +452,207 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
     int all_lo, all_hi;   // blocks that either tile sees
     // Registers: the launch gives every thread 168 where there are three warpgroups; a row of S takes more, the others less.
     if (warp >= TILES * 4) {
-    if constexpr (TILES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == TILES * 4 + 2) {
-        // ---- what to do: the CTA's own index, then those of CTAs that have not begun, which it takes from the launch
-        Rows rows;
-        rows.begin(p, p.pair_rows ? 8 : 7);
-        unsigned replies = 0;
-        // The index of a CTA that will not begin any more, or -1: all have.
-        auto steal = [&](bool* ok) {
-            int index = -1;
-            if (lane == 0) {
-                mbar_expect(&sm.stolen, 16);
-                asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
-                             ::"r"(smem_addr(&sm.reply)), "r"(smem_addr(&sm.stolen)) : "memory");
-            }
-            __syncwarp();
-            *ok = __all_sync(0xffffffffu, mbar_wait(sm, &sm.stolen, replies & 1));
-            ++replies;
-            if (*ok)
-                asm volatile("{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
-                             "ld.shared.b128 r, [%1];\n\t"
-                             "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
-                             "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, r;\n\t}"
-                             : "+r"(index) : "r"(smem_addr(&sm.reply)) : "memory");
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the reply is read before the next one is written
-            __syncwarp();
-            return __shfl_sync(0xffffffffu, index, 0);
-        };
-        // One item ahead of what the softmax is at, no more: what is taken earlier may be missing elsewhere at the end.
-        bool ok = true;
-        int64_t index = blockIdx.x;
-        for (unsigned k = 0; ok; ++k) {
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(sm, &sm.item_empty, (k & 1) ^ 1)))) break;
-            if (k > 0) index = steal(&ok);
-            bool found = false;
-            while (ok && index >= 0 && !(found = item_at<TILES>(p, rows, index, &it))) index = steal(&ok);
-            if (!ok) break;
-            if (!found) it.more = 0;
-            if (lane == 0) {
-                sm.item = it;
-                mbar_arrive(&sm.item_full);
-            }
-            if (!found) break;
-        }
-    } else if (warp == TILES * 4 + 1) {
-        // ---- loads
-        unsigned n = 0;                 // blocks of keys or values so far
-        uint32_t q_phase[2] = {0, 0};
-        bool ok = true;
-        for (unsigned k = 0; ok && next_item(k, &it); ++k) {
-            blocks_of<TILES>(it, &all_lo, &all_hi);
-            if (lane == 0) {
-                for (int i = 0; ok && i < TILES; ++i) {
-                    if (it.hi[i] < it.lo[i]) continue;
-                    if (!(ok = mbar_wait(sm, &sm.q_empty[i], q_phase[i] ^ 1))) break;
-                    q_phase[i] ^= 1;
-                    mbar_expect(&sm.q_full[i], P::kBlockBytes);
-                    for (int c = 0; c < P::kChunks; ++c)
-                        tma_load(q_tile(i) + c * P::kChunkBytes, &p.q_map, it.head[i] * D + c * 64,
-                                 it.base + it.row[i], &sm.q_full[i]);
+        if constexpr (TILES == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == TILES * 4 + 2) {
+            // ---- what to do: the CTA's own index, then those of CTAs that have not begun, which it takes from the launch
+            Rows rows;
+            rows.begin(p, p.pair_rows ? 8 : 7);
+            unsigned replies = 0;
+            // The index of a CTA that will not begin any more, or -1: all have.
+            auto steal = [&](bool* ok) {
+                int index = -1;
+                if (lane == 0) {
+                    mbar_expect(&sm.stolen, 16);
+                    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                                 ::"r"(smem_addr(&sm.reply)), "r"(smem_addr(&sm.stolen)) : "memory");
                 }
-                // K of block lo, then K of each next block and V of this one.
-                const int blocks = all_hi - all_lo + 1;
-                for (int m = 0; ok && m < 2 * blocks; ++m, ++n) {
-                    if (!(ok = mbar_wait(sm, &sm.kv_empty[n % P::kStages], (n / P::kStages & 1) ^ 1))) break;
-                    const bool values = m == 2 * blocks - 1 || (m > 0 && m % 2 == 0);
-                    const int j = all_lo + (values ? (m - 1) / 2 : (m + 1) / 2);
-                    void* const bar = &sm.kv_full[n % P::kStages];
-                    mbar_expect(bar, P::kBlockBytes);
-                    for (int c = 0; c < P::kChunks; ++c)
-                        tma_load(kv_stage(n) + c * P::kChunkBytes, values ? &p.v_map : &p.k_map, it.kv_head * D + c * 64,
-                                 it.base + j * kRows, bar);
-                }
-            }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-        }
-        if (lane == 0) {   // the copies in flight land before the CTA's memory goes to another
-            for (unsigned k = n > P::kStages ? n - P::kStages : 0; k < n; ++k) {
-                const long long t0 = clock64();
-                while (!mbar_try(&sm.kv_full[k % P::kStages], k / P::kStages & 1) && clock64() - t0 < kWaitLimitCycles) {}
-            }
-            for (int i = 0; i < TILES; ++i) {
-                const long long t0 = clock64();
-                while (!mbar_try(&sm.q_full[i], q_phase[i] ^ 1) && clock64() - t0 < kWaitLimitCycles) {}
-            }
-        }
-    } else if (warp == TILES * 4) {
-        // ---- products. The tensor cores take few instructions ahead, so what this warp does between two products has to be short:
-        // it looks at the next one's barriers while it issues this one, a wait that has run out is looked at once a block only (what
-        // is issued in between works on whatever lies in this CTA's memory), and stages are counted, not divided.
-        uint32_t elected;
-        asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(elected));
-        constexpr uint32_t kDescO = instr_desc(D, true);
-        const uint32_t desc_s = instr_desc(kRows, false) | (p.negate ? kNegateA : 0u);
-        const uint32_t low = __shfl_sync(0xffffffffu, smem_addr(base) >> 4, 0);   // of a tile: this and its place / 16
-        constexpr uint32_t kBlock = P::kBlockBytes >> 4;
-        uint32_t q_phase = 0, p_phase[2] = {0, 0}, s_phase[2] = {0, 0};
-        bool ok = true;
-        auto wait = [&](const void* bar, uint32_t parity) { ok &= mbar_wait(sm, bar, parity); };
-        struct Stage {
-            uint32_t at, phase;
-            __device__ __forceinline__ Stage next() const { return at + 1 == P::kStages ? Stage{0u, phase ^ 1u} : Stage{at + 1, phase}; }
-        };
-        Stage stage{0, 0};   // the next block of keys or values
-        for (unsigned k = 0; next_item(k, &it); ++k) {
-            int tile_lo[TILES], tile_hi[TILES], row[TILES];
-#pragma unroll
-            for (int i = 0; i < TILES; ++i) {
-                tile_lo[i] = __shfl_sync(0xffffffffu, it.lo[i], 0);
-                tile_hi[i] = __shfl_sync(0xffffffffu, it.hi[i], 0);
-                row[i] = __shfl_sync(0xffffffffu, it.row[i], 0);
-            }
-            blocks_of<TILES>(it, &all_lo, &all_hi);
-            const int lo = __shfl_sync(0xffffffffu, all_lo, 0), hi = __shfl_sync(0xffffffffu, all_hi, 0);
-            // S of tile i and block j: the block's keys are there, and what was in the buffer has been read. `look` is called before
-            // the last two instructions; `ready`: the barriers were seen complete.
-            auto s_ready = [&](int i, const Stage& keys) {
-                const int f = i & (P::kBuffers - 1);
-                return mbar_test(&sm.kv_full[keys.at], keys.phase) & mbar_test(&sm.s_free[f], s_phase[f] ^ 1);
+                __syncwarp();
+                *ok = __all_sync(0xffffffffu, mbar_wait(sm, &sm.stolen, replies & 1));
+                ++replies;
+                if (*ok)
+                    asm volatile("{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+                                 "ld.shared.b128 r, [%1];\n\t"
+                                 "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+                                 "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, r;\n\t}"
+                                 : "+r"(index) : "r"(smem_addr(&sm.reply)) : "memory");
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // the reply is read before the next one is written
+                __syncwarp();
+                return __shfl_sync(0xffffffffu, index, 0);
             };
-            auto product_s = [&](int i, int j, const Stage& keys, bool ready, auto look) {
-                const int f = i & (P::kBuffers - 1);
-                const uint32_t a = low + i * kBlock + (1u << 16), b = low + (TILES + keys.at) * kBlock + (1u << 16);
-                if (!ready) {
-                    wait(&sm.kv_full[keys.at], keys.phase);
-                    wait(&sm.s_free[f], s_phase[f] ^ 1);
+            // One item ahead of what the softmax is at, no more: what is taken earlier may be missing elsewhere at the end.
+            bool ok = true;
+            int64_t index = blockIdx.x;
+            for (unsigned k = 0; ok; ++k) {
+                if (!(ok = __all_sync(0xffffffffu, mbar_wait(sm, &sm.item_empty, (k & 1) ^ 1)))) break;
+                if (k > 0) index = steal(&ok);
+                bool found = false;
+                while (ok && index >= 0 && !(found = item_at<TILES>(p, rows, index, &it))) index = steal(&ok);
+                if (!ok) break;
+                if (!found) it.more = 0;
+                if (lane == 0) {
+                    sm.item = it;
+                    mbar_arrive(&sm.item_full);
                 }
-                s_phase[f] ^= 1;
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    if (k == D / 16 - 2) look();
-                    const uint32_t at = ((k / 4) * P::kChunkBytes + (k % 4) * 32) >> 4;
-                    mma_ss(tmem + P::kColumnsS + f * kRows, a + at, b + at, desc_s, k > 0, elected);
-                }
-                tc_commit(&sm.s_full[i], elected);
-                if (j == tile_hi[i]) tc_commit(&sm.q_empty[i], elected);
-            };
-            auto o_ready = [&](int i, const Stage& values) {
-                return mbar_test(&sm.kv_full[values.at], values.phase) & mbar_test(&sm.p_full[i], p_phase[i]);
-            };
-            auto product_o = [&](int i, int j, const Stage& values, bool ready, auto look) {
-                const uint32_t b = low + (TILES + values.at) * kBlock + (P::kChunkBytes >> 4 << 16);
-                if (!ready) {
-                    wait(&sm.kv_full[values.at], values.phase);
-                    wait(&sm.p_full[i], p_phase[i]);
-                }
-                p_phase[i] ^= 1;
-                tc_fence_after();
-                bool by_hand = false;
-                if (some_masked(p, row[i], j * kRows)) by_hand = __shfl_sync(0xffffffffu, sm.by_hand[i], 0);
-                if (!by_hand) {
-#pragma unroll
-                    for (int k = 0; k < kRows / 16; ++k) {
-                        if (k == kRows / 16 - 2) look();
-                        mma_ts(tmem + P::kColumnsO + i * D, tmem + P::kColumnsP + i * (kRows / 2) + k * 8, b + (k * 2048 >> 4), kDescO,
-                               k > 0 || j > tile_lo[i], elected);
+                if (!found) break;
+            }
+        } else if (warp == TILES * 4 + 1) {
+            // ---- loads
+            unsigned n = 0;                 // blocks of keys or values so far
+            uint32_t q_phase[2] = {0, 0};
+            bool ok = true;
+            for (unsigned k = 0; ok && next_item(k, &it); ++k) {
+                blocks_of<TILES>(it, &all_lo, &all_hi);
+                if (lane == 0) {
+                    for (int i = 0; ok && i < TILES; ++i) {
+                        if (it.hi[i] < it.lo[i]) continue;
+                        if (!(ok = mbar_wait(sm, &sm.q_empty[i], q_phase[i] ^ 1))) break;
+                        q_phase[i] ^= 1;
+                        mbar_expect(&sm.q_full[i], P::kBlockBytes);
+                        for (int c = 0; c < P::kChunks; ++c)
+                            tma_load(q_tile(i) + c * P::kChunkBytes, &p.q_map, it.head[i] * D + c * 64,
+                                     it.base + it.row[i], &sm.q_full[i]);
+                    }
+                    // K of block lo, then K of each next block and V of this one.
+                    const int blocks = all_hi - all_lo + 1;
+                    for (int m = 0; ok && m < 2 * blocks; ++m, ++n) {
+                        if (!(ok = mbar_wait(sm, &sm.kv_empty[n % P::kStages], (n / P::kStages & 1) ^ 1))) break;
+                        const bool values = m == 2 * blocks - 1 || (m > 0 && m % 2 == 0);
+                        const int j = all_lo + (values ? (m - 1) / 2 : (m + 1) / 2);
+                        void* const bar = &sm.kv_full[n % P::kStages];
+                        mbar_expect(bar, P::kBlockBytes);
+                        for (int c = 0; c < P::kChunks; ++c)
+                            tma_load(kv_stage(n) + c * P::kChunkBytes, values ? &p.v_map : &p.k_map, it.kv_head * D + c * 64,
+                                     it.base + j * kRows, bar);
                     }
                 }
-                tc_commit(&sm.pv_done[i], elected);
-            };
-            auto nothing = [] {};
-#pragma unroll
-            for (int i = 0; i < TILES; ++i) {
-                if (tile_hi[i] < tile_lo[i]) continue;
-                wait(&sm.q_full[i], q_phase >> i & 1);
-                q_phase ^= 1u << i;
-                if (tile_lo[i] == lo) product_s(i, lo, stage, false, nothing);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
             }
-            tc_commit(&sm.kv_empty[stage.at], elected);
-            stage = stage.next();
-            // The next block's S goes before this block's P V, which waits for the softmax.
-            bool ready_s = false;
-#pragma unroll 1
-            for (int j = lo; j <= hi; ++j) {
-                const Stage keys = stage, values = j < hi ? keys.next() : keys;
+            if (lane == 0) {   // the copies in flight land before the CTA's memory goes to another
+                for (unsigned k = n > P::kStages ? n - P::kStages : 0; k < n; ++k) {
+                    const long long t0 = clock64();
+                    while (!mbar_try(&sm.kv_full[k % P::kStages], k / P::kStages & 1) && clock64() - t0 < kWaitLimitCycles) {}
+                }
+                for (int i = 0; i < TILES; ++i) {
+                    const long long t0 = clock64();
+                    while (!mbar_try(&sm.q_full[i], q_phase[i] ^ 1) && clock64() - t0 < kWaitLimitCycles) {}
+                }
+            }
+        } else if (warp == TILES * 4) {
+            // ---- products. The tensor cores take few instructions ahead, so what this warp does between two products has to be short:
+            // it looks at the next one's barriers while it issues this one, a wait that has run out is looked at once a block only (what
+            // is issued in between works on whatever lies in this CTA's memory), and stages are counted, not divided.
+            uint32_t elected;
+            asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(elected));
+            constexpr uint32_t kDescO = instr_desc(D, true);
+            const uint32_t desc_s = instr_desc(kRows, false) | (p.negate ? kNegateA : 0u);
+            const uint32_t low = __shfl_sync(0xffffffffu, smem_addr(base) >> 4, 0);   // of a tile: this and its place / 16
+            constexpr uint32_t kBlock = P::kBlockBytes >> 4;
+            uint32_t q_phase = 0, p_phase[2] = {0, 0}, s_phase[2] = {0, 0};
+            bool ok = true;
+            auto wait = [&](const void* bar, uint32_t parity) { ok &= mbar_wait(sm, bar, parity); };
+            struct Stage {
+                uint32_t at, phase;
+                __device__ __forceinline__ Stage next() const { return at + 1 == P::kStages ? Stage{0u, phase ^ 1u} : Stage{at + 1, phase}; }
+            };
+            Stage stage{0, 0}, last{0, 1};   // the next block of keys or values, and the last one
+            for (unsigned k = 0; next_item(k, &it); ++k) {
+                int tile_lo[TILES], tile_hi[TILES], row[TILES];
 #pragma unroll
                 for (int i = 0; i < TILES; ++i) {
-                    bool ready = ready_s;
-                    ready_s = false;
-                    if (j < hi && j + 1 >= tile_lo[i] && j + 1 <= tile_hi[i])
-                        product_s(i, j + 1, keys, ready, [&] { ready = o_ready(i, values); });
-                    else ready = false;
-                    // (The next S: of the other tile, or of the next block.)
-                    if (j >= tile_lo[i] && j <= tile_hi[i])
-                        product_o(i, j, values, ready, [&] {
-                            if (i + 1 < TILES) ready_s = s_ready(i + 1, keys);
-                            else if (j + 1 < hi) ready_s = s_ready(0, values.next());
-                        });
+                    tile_lo[i] = __shfl_sync(0xffffffffu, it.lo[i], 0);
+                    tile_hi[i] = __shfl_sync(0xffffffffu, it.hi[i], 0);
+                    row[i] = __shfl_sync(0xffffffffu, it.row[i], 0);
                 }
-                if (j < hi) tc_commit(&sm.kv_empty[keys.at], elected);
-                tc_commit(&sm.kv_empty[values.at], elected);
-                stage = values.next();
+                blocks_of<TILES>(it, &all_lo, &all_hi);
+                const int lo = __shfl_sync(0xffffffffu, all_lo, 0), hi = __shfl_sync(0xffffffffu, all_hi, 0);
+                // S of tile i and block j: the block's keys are there, and what was in the buffer has been read. `look` is called before
+                // the last two instructions; `ready`: the barriers were seen complete.
+                auto s_ready = [&](int i, const Stage& keys) {
+                    const int f = i & (P::kBuffers - 1);
+                    return mbar_test(&sm.kv_full[keys.at], keys.phase) & mbar_test(&sm.s_free[f], s_phase[f] ^ 1);
+                };
+                auto product_s = [&](int i, int j, const Stage& keys, bool ready, auto look) {
+                    const int f = i & (P::kBuffers - 1);
+                    const uint32_t a = low + i * kBlock + (1u << 16), b = low + (TILES + keys.at) * kBlock + (1u << 16);
+                    if (!ready) {
+                        wait(&sm.kv_full[keys.at], keys.phase);
+                        wait(&sm.s_free[f], s_phase[f] ^ 1);
+                    }
+                    s_phase[f] ^= 1;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        if (k == D / 16 - 2) look();
+                        const uint32_t at = ((k / 4) * P::kChunkBytes + (k % 4) * 32) >> 4;
+                        mma_ss(tmem + P::kColumnsS + f * kRows, a + at, b + at, desc_s, k > 0, elected);
+                    }
+                    tc_commit(&sm.s_full[i], elected);
+                    if (j == tile_hi[i]) tc_commit(&sm.q_empty[i], elected);
+                };
+                auto o_ready = [&](int i, const Stage& values) {
+                    return mbar_test(&sm.kv_full[values.at], values.phase) & mbar_test(&sm.p_full[i], p_phase[i]);
+                };
+                auto product_o = [&](int i, int j, const Stage& values, bool ready, auto look) {
+                    const uint32_t b = low + (TILES + values.at) * kBlock + (P::kChunkBytes >> 4 << 16);
+                    if (!ready) {
+                        wait(&sm.kv_full[values.at], values.phase);
+                        wait(&sm.p_full[i], p_phase[i]);
+                    }
+                    p_phase[i] ^= 1;
+                    tc_fence_after();
+                    bool by_hand = false;
+                    if (some_masked(p, row[i], j * kRows)) by_hand = __shfl_sync(0xffffffffu, sm.by_hand[i], 0);
+                    if (!by_hand) {
+#pragma unroll
+                        for (int k = 0; k < kRows / 16; ++k) {
+                            if (k == kRows / 16 - 2) look();
+                            mma_ts(tmem + P::kColumnsO + i * D, tmem + P::kColumnsP + i * (kRows / 2) + k * 8, b + (k * 2048 >> 4), kDescO,
+                                   k > 0 || j > tile_lo[i], elected);
+                        }
+                    }
+                    tc_commit(&sm.pv_done[i], elected);
+                };
+                auto nothing = [] {};
+#pragma unroll
+                for (int i = 0; i < TILES; ++i) {
+                    if (tile_hi[i] < tile_lo[i]) continue;
+                    wait(&sm.q_full[i], q_phase >> i & 1);
+                    q_phase ^= 1u << i;
+                    if (tile_lo[i] == lo) product_s(i, lo, stage, false, nothing);
+                }
+                tc_commit(&sm.kv_empty[stage.at], elected);
+                stage = stage.next();
+                // The next block's S goes before this block's P V, which waits for the softmax.
+                bool ready_s = false;
+#pragma unroll 1
+                for (int j = lo; j <= hi; ++j) {
+                    const Stage keys = stage, values = j < hi ? keys.next() : keys;
+#pragma unroll
+                    for (int i = 0; i < TILES; ++i) {
+                        bool ready = ready_s;
+                        ready_s = false;
+                        if (j < hi && j + 1 >= tile_lo[i] && j + 1 <= tile_hi[i])
+                            product_s(i, j + 1, keys, ready, [&] { ready = o_ready(i, values); });
+                        else ready = false;
+                        // (The next S: of the other tile, or of the next block.)
+                        if (j >= tile_lo[i] && j <= tile_hi[i])
+                            product_o(i, j, values, ready, [&] {
+                                if (i + 1 < TILES) ready_s = s_ready(i + 1, keys);
+                                else if (j + 1 < hi) ready_s = s_ready(0, values.next());
+                            });
+                    }
+                    if (j < hi) tc_commit(&sm.kv_empty[keys.at], elected);
+                    tc_commit(&sm.kv_empty[values.at], elected);
+                    last = values;
+                    stage = values.next();
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                }
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
             }
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            // What the tensor cores have still to tell goes to this CTA's barriers: before its memory goes to another. (Before the
+            // first phase of a barrier the one of parity 1 counts as complete.)
+            wait(&sm.kv_empty[last.at], last.phase);
         }
-    }
     } else {
         if constexpr (TILES == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         // ---- softmax of tile i, this thread's row of it

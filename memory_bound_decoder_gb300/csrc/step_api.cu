@@ -17,22 +17,41 @@ constexpr double kTwoPi = 6.283185307179586476925286766559;
 bool positive(double x) { return std::isfinite(x) && x > 0.0; }
 double held(double x) { return x < 0.0 ? 0.0 : (x > 1.0 ? 1.0 : x); }
 
-// The runtime's way to the driver's encoder of tensor maps, so that the library links no driver library; null without one.
-using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
-EncodeTiled encoder() {
-    static const EncodeTiled entry = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
-        (void)cudaGetLastError();
-        return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeTiled>(p) : nullptr;
+// The driver's encoder of tensor maps and its current context, through the runtime, so that the library links no driver
+// library; null without one.
+struct Driver {
+    decltype(&cuTensorMapEncodeTiled) encode = nullptr;
+    decltype(&cuCtxGetCurrent) current = nullptr;
+};
+const Driver& driver() {
+    static const Driver entry = [] {
+        auto find = [](const char* name) {
+            void* p = nullptr;
+            cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+            const cudaError_t e = cudaGetDriverEntryPointByVersion(name, &p, 12000, cudaEnableDefault, &q);
+            (void)cudaGetLastError();
+            return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? p : nullptr;
+        };
+        Driver d;
+        d.encode = reinterpret_cast<decltype(d.encode)>(find("cuTensorMapEncodeTiled"));
+        d.current = reinterpret_cast<decltype(d.current)>(find("cuCtxGetCurrent"));
+        return d;
     }();
     return entry;
 }
 
+// Makes the current device's context current on a host thread that has not used CUDA yet: the runtime's calls do so on their own, the
+// driver's encoder does not.
+void have_context() {
+    CUcontext context = nullptr;
+    int device = 0;
+    if (!driver().current || driver().current(&context) != CUDA_SUCCESS || context) return;
+    if (cudaGetDevice(&device) != cudaSuccess || cudaSetDevice(device) != cudaSuccess) (void)cudaGetLastError();
+}
+
 // Rows of `width` bf16 in boxes of 64 elements and 128 rows.
 bool encode_rows(CUtensorMap* map, const void* base, int64_t width, int64_t rows, int64_t stride) {
-    const EncodeTiled encode = encoder();
+    const auto encode = driver().encode;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
     const cuuint32_t box[2] = {64, 128}, steps[2] = {1, 1};
@@ -119,6 +138,7 @@ mbd_status mbd_prompt_attention(void* out, const void* q, int64_t q_stride, cons
                            Range{cu_tokens, uint64_t(n_seqs + 1) * 4}})
         if (overlaps_any(r, writes)) return MBD_ERR_INVALID_ARG;
     if (overlap(writes[0], writes[1])) return MBD_ERR_INVALID_ARG;
+    have_context();
     mbd::PromptParams p{};
     if (!encode_rows(&p.q_map, q, width, n_tokens, q_stride) || !encode_rows(&p.k_map, k, kv_width, n_tokens, kv_stride) ||
         !encode_rows(&p.v_map, v, kv_width, n_tokens, kv_stride))
