@@ -18,6 +18,9 @@
 // or by 2^-31 of the largest p that the warp keeps where that is more, as subnormals end there. A warp's sums are relative
 // to its own maximum and joined in fp32, so what is lost that way is at most 2^-31 of the result's largest |v| for each key that
 // one warp takes of an item: 2^-16 at 32768 keys, a quarter of 131072.
+// E2M1 codes of an NVFP4 cache become f16 in the same way and are multiplied by their block's scale there, which is exact (2 and 4
+// significant bits, 2^-10 .. 2688); the tensor scales go into the logits' factor and the result's. That makes a step of it about
+// as many instructions as an FP8 step of half its keys' bytes, so steps go through shared memory (kStaged).
 // In the bf16 path p goes in as the sum of two bf16 terms (2^-16): rounding it once would cost as much accuracy as
 // rounding the output does, and the second product costs nothing measurable (64 sequences of up to 2047 tokens, 32 query
 // and 8 key-value heads: 48.6 us without it, 48.7 with it). Both terms are positive (of p above 2^-110), or an infinite value would
@@ -40,6 +43,8 @@
 //   FP8 static, 4 sequences of 13240..17308 tokens, 128 and 8 heads, pages of 128  38.5 us, 3250 GB/s
 //   bf16, 32 sequences of 100..8192 tokens, 16 and 2 heads of 256, pages of 16     56 us, 4830 GB/s
 //   bf16, 24 windows of 1024 tokens, 16 and 16 heads of 64                         23.4 us, 4230 GB/s
+//   NVFP4, 32 sequences of 100..8192 tokens, 64 and 8 heads, pages of 32           43 us, 3580 GB/s
+//   NVFP4, one sequence of 131071 tokens, 64 and 8 heads, pages of 128             42.3 us, 3570 GB/s
 // About ten microseconds of each do not depend on the bytes: launch, lengths, page table and first rows on the way in (each
 // a round trip of half a microsecond), shares that end up to 8% apart, and the joins.
 #pragma once
@@ -400,9 +405,10 @@ __device__ __forceinline__ void join_two(const AttendParams& p, const Cut& cut, 
                             m, t, mo);
 }
 
-// Where a step's keys and values go through shared memory: NVFP4, in pages of at least a group. A step of it is as many
-// instructions as in the other formats for half of their bytes, and the registers that hold a step of loads are not enough to keep the
-// next values on their way during all of this step's: 32 sequences of up to 8192 tokens take 52.7 us without it.
+// Where a step's keys and values go through shared memory: NVFP4, in pages of at least a group. A step of it is so many
+// instructions that loads into registers, which cannot be issued before the ones that they replace are used up, leave memory idle: 32
+// sequences of up to 8192 tokens take 52.6 us without it and 43.0 with it, one of 131071 53.9 and 42.3. Two steps are on their way. (Steps
+// of 32 keys: 50.2 and 43.1; with three CTAs an SM 44.4 and 52.0.)
 template <int STORE, int GRAN>
 constexpr bool kStaged = STORE == kKvNvfp4 && GRAN == 16;
 

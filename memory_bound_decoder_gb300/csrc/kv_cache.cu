@@ -1,7 +1,8 @@
 // Paged key-value cache: appending new tokens, and eviction by accumulated attention weight.
 //
 // Append. Row (token t, head h) of the stacked projection goes to slot lens[seq] - (new tokens of seq) + i of its
-// sequence, as it is (bf16) or as E4M3 codes of value / scale; the dynamic scale is amax / 448 of the head's row.
+// sequence, as it is (bf16), as E4M3 codes of value / scale (the dynamic scale is amax / 448 of the head's row), or as E2M1 codes of
+// value / (block scale * tensor scale), the block's scale the E4M3 code of amax / (6 tensor scale) of its 16 values.
 // Both divisions are rounded to nearest, so codes and scales are those of the definition, ties included. Bound by bytes (2 D
 // in, D or 2 D out for each of k and v) and, for a decode step's few rows, by latency: the rows need no slot to be read,
 // so their loads are under way while the slots are looked up. head_dim / 8 lanes own a row, 16 bytes of k and of v

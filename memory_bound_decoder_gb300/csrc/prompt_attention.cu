@@ -224,7 +224,7 @@ struct Rows {
     // begun last takes the shortest. Sequence 32 c + lane has tiles[c]; `before` tiles lie at higher places than `place`.
     static constexpr int kMany = 8;
     int tiles[kMany];
-    int place;
+    int place, top;
     int64_t before;
 
     __device__ __forceinline__ void begin(const PromptParams& p, int shift) {
@@ -240,13 +240,17 @@ struct Rows {
             else kv_bad_index();
             most = max(most, tiles[c]);
         }
-        place = __reduce_max_sync(0xffffffffu, most) - 1;
+        place = top = __reduce_max_sync(0xffffffffu, most) - 1;
         before = 0;
     }
-    // Sequence and place of tile `number` (ascending from call to call); false if there are not so many.
+    // Sequence and place of tile `number`; false if there are not so many. (Numbers mostly ascend from call to call.)
     __device__ __forceinline__ bool find(const PromptParams& p, int shift, int64_t number, int64_t* seq, int64_t* at) {
         const int lane = threadIdx.x & 31;
         if (p.n_seqs <= kMany * 32) {
+            if (number < before) {
+                place = top;
+                before = 0;
+            }
             for (; place >= 0; --place) {
                 unsigned there[kMany];
                 int count = 0;
@@ -408,6 +412,7 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_trigger();
     if (threadIdx.x == 0) {
+        for (const CUtensorMap* map : {&p.q_map, &p.k_map, &p.v_map}) asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.q_full[i], 1);
             mbar_init(&sm.q_empty[i], 1);
