@@ -36,8 +36,8 @@
 // and adds up over a row's keys as a random walk does. Sums of P are kept in fp32 from the values before rounding.
 //
 // Values in masked places. A masked P is 0, and 0 times an infinite or NaN value would be NaN. So in blocks that hold masked
-// places (the diagonal, the window's edge; rows behind the sequence's end are masked by causality) the warpgroup looks at V
-// first, and where it holds such a value adds that block's product itself, over the keys in view alone.
+// places (the diagonal, the window's edge; rows behind the sequence's end are masked by causality) a warp looks at V as it
+// arrives, and where it holds such a value the warpgroup adds that block's product itself, over the keys in view alone.
 //
 // Every wait is bounded: one that runs out sets the error bit, and all roles leave.
 #include <cuda.h>
@@ -79,14 +79,17 @@ struct Item {
     int more;            // 0: there is none, and none follows
 };
 
+// Blocks of V that may be looked at ahead of the softmax: more than the stages hold.
+constexpr int kLooks = 8;
+
 struct PromptSmem {
-    unsigned long long q_full[2], q_empty[2], s_full[2], s_free[2], p_full[2], pv_done[2], looked[2], kv_full[8], kv_empty[8];
+    unsigned long long q_full[2], q_empty[2], s_full[2], s_free[2], p_full[2], pv_done[2], looked[kLooks], kv_full[8], kv_empty[8];
     unsigned long long item_full, item_empty, stolen;
     alignas(16) uint4 reply;
     Item item;
     uint32_t tmem;
     int by_hand[2];             // this block's P V of the tile is the warpgroup's
-    volatile unsigned odd[2];   // the last of the looks at V, counted from 1, that found a value that is not finite
+    volatile int odd[kLooks];   // whether the block holds a value that is not finite
     volatile int abort;
 };
 
@@ -340,6 +343,21 @@ __device__ __forceinline__ bool some_masked(const PromptParams& p, int row, int 
     return key0 + kRows - 1 > row || (p.window > 0 && key0 < row + kRows - p.window);
 }
 
+// The blocks of an item in which some place is masked for either tile, and V is looked at: those before `low` (the window's edge) and
+// from `high` on (the diagonal).
+struct Looks {
+    int first, low, high;
+    template <int TILES>
+    __device__ __forceinline__ static Looks of(const PromptParams& p, const Item& it, int all_lo) {
+        const int last_row = TILES == 2 && it.hi[1] >= it.lo[1] ? it.row[1] : it.row[0];
+        const int64_t edge = p.window > 0 ? last_row + kRows - p.window : 0;   // keys before it are masked for the last row
+        const int low = max(all_lo, edge > 0 ? static_cast<int>((edge + kRows - 1) / kRows) : 0);
+        return Looks{all_lo, low, max(low, it.row[0] / kRows)};
+    }
+    // How many of them come before block j.
+    __device__ __forceinline__ int before(int j) const { return min(j, low) - first + max(0, j - high); }
+};
+
 // ------------------------------------------------------------------------------------------ softmax
 
 // This thread's row of one block's P V, over the keys klo .. khi in view, on top of what O holds (if `add`); p is in TMEM.
@@ -420,16 +438,15 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
             mbar_init(&sm.s_free[i], 4);
             mbar_init(&sm.p_full[i], 4);
             mbar_init(&sm.pv_done[i], 1);
-            mbar_init(&sm.looked[i], 4);
             sm.by_hand[i] = 0;
-            sm.odd[i] = 0;
         }
+        for (int i = 0; i < kLooks; ++i) mbar_init(&sm.looked[i], 1);
         for (int i = 0; i < P::kStages; ++i) {
             mbar_init(&sm.kv_full[i], 1);
-            mbar_init(&sm.kv_empty[i], 1);
+            mbar_init(&sm.kv_empty[i], 2);   // the products are done with it, and the look
         }
         mbar_init(&sm.item_full, 1);
-        mbar_init(&sm.item_empty, 2 + TILES * 4);
+        mbar_init(&sm.item_empty, 3 + TILES * 4);
         mbar_init(&sm.stolen, 1);
         sm.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -541,6 +558,53 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
                     const long long t0 = clock64();
                     while (!mbar_try(&sm.q_full[i], q_phase[i] ^ 1) && clock64() - t0 < kWaitLimitCycles) {}
                 }
+            }
+        } else if (warp == TILES * 4 + 3) {
+            // ---- looks at V where places are masked, ahead of the softmax
+            unsigned n = 0, looks = 0, seen = 0;
+            bool ok = true;
+            // Every load is waited for in its turn, and its place is free for the next one only when this warp has passed it, too: a
+            // barrier's parity says nothing to who is two phases away from it.
+            auto arrived = [&] { ok = __all_sync(0xffffffffu, mbar_wait(sm, &sm.kv_full[seen % P::kStages], seen / P::kStages & 1)); };
+            auto pass = [&] {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.kv_empty[seen % P::kStages]);
+                ++seen;
+            };
+            for (unsigned k = 0; ok && next_item(k, &it); ++k) {
+                blocks_of<TILES>(it, &all_lo, &all_hi);
+                const Looks masked = Looks::of<TILES>(p, it, all_lo);
+                for (int j = all_lo; ok && j <= all_hi; ++j) {
+                    const unsigned stage = n + 2 * (j - all_lo) + (j < all_hi ? 2 : 1);
+                    while (ok && seen < stage) {
+                        arrived();
+                        pass();
+                    }
+                    if (ok) arrived();
+                    if (!ok) break;
+                    if (j >= masked.low && j < masked.high) {
+                        pass();
+                        continue;
+                    }
+                    const char* v = kv_stage(stage);
+                    uint32_t odd = 0;
+#pragma unroll 8
+                    for (int i = 0; i < P::kBlockBytes / 512; ++i) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(v + (i * 32 + lane) * 16);
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)   // 0 times it: 0 if it is finite, else NaN
+                            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(odd) : "r"(w[e]), "r"(0u));
+                    }
+                    const bool any = __any_sync(0xffffffffu, odd != 0);
+                    if (lane == 0) {
+                        sm.odd[looks % kLooks] = any;
+                        mbar_arrive(&sm.looked[looks % kLooks]);
+                    }
+                    ++looks;
+                    pass();
+                }
+                n += 2 * (all_hi - all_lo + 1);
             }
         } else if (warp == TILES * 4) {
             // ---- products. The tensor cores take few instructions ahead, so what this warp does between two products has to be short:
@@ -673,6 +737,7 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
             blocks_of<TILES>(it, &all_lo, &all_hi);
             const int lo = i ? it.lo[1] : it.lo[0], hi = i ? it.hi[1] : it.hi[0], row0 = i ? it.row[1] : it.row[0];
             const int head = i ? it.head[1] : it.head[0], row = row0 + tid;
+            const Looks masks = Looks::of<TILES>(p, it, all_lo);
             const int klo = p.window > 0 && row >= p.window ? row - static_cast<int>(p.window) + 1 : 0;
             float ref = 0.0f, lim = -INFINITY;
             float2 sum[4] = {f2(0.0f), f2(0.0f), f2(0.0f), f2(0.0f)};
@@ -693,8 +758,14 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
                 const bool masked = some_masked(p, row0, key0);
                 if (masked) {
 #pragma unroll
-                    for (int c = 0; c < kRows; ++c)
-                        if (key0 + c > row || key0 + c < klo) s[c / 32][c % 32] = 0xff800000u;   // -inf
+                    for (int c = 0; c < 4; ++c) {   // bit e: the row sees key e of these 32
+                        const int to = row - (key0 + c * 32), from = klo - (key0 + c * 32);
+                        unsigned seen = to >= 31 ? 0xffffffffu : (to < 0 ? 0u : (2u << to) - 1u);
+                        if (from > 0) seen &= from > 31 ? 0u : ~0u << from;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(seen & (1u << e))) s[c][e] = 0xff800000u;   // -inf
+                    }
                 }
                 float m[4];
 #pragma unroll
@@ -733,29 +804,13 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
                 }
                 if (masked) {
                     // V's rows of this block: any value that is not finite?
-                    const unsigned stage = n + 2 * (j - all_lo) + (j < all_hi ? 2 : 1);
-                    ok &= mbar_wait(sm, &sm.kv_full[stage % P::kStages], stage / P::kStages & 1);
-                    uint32_t odd = 0;
-                    const char* v = kv_stage(stage);
-#pragma unroll
-                    for (int k = 0; k < D / 8; ++k) {
-                        const uint4 x = *reinterpret_cast<const uint4*>(v + (k / 8) * P::kChunkBytes + tid * 128 + ((k + tid) & 7) * 16);
-                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)   // 0 times it: 0 if it is finite, else NaN
-                            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(odd) : "r"(w[e]), "r"(0u));
-                    }
-                    // (The warpgroup agrees through a barrier in shared memory, whose wait is bounded.)
-                    ++looks;
-                    if (odd != 0) sm.odd[i] = looks;
+                    const unsigned look = looks + masks.before(j), stage = n + 2 * (j - all_lo) + (j < all_hi ? 2 : 1);
+                    ok &= mbar_wait(sm, &sm.looked[look % kLooks], look / kLooks & 1);
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.looked[i]);
-                    ok &= mbar_wait(sm, &sm.looked[i], (looks & 1) ^ 1);
-                    __syncwarp();
-                    const bool any = sm.odd[i] == looks;
+                    const bool any = sm.odd[look % kLooks] != 0;
                     if (any) {
                         tc_wait_st();
-                        product_by_hand<D>(v, p_at, o_at, key0, klo, row, j > lo);
+                        product_by_hand<D>(kv_stage(stage), p_at, o_at, key0, klo, row, j > lo);
                     }
                     if (tid == 0) sm.by_hand[i] = any;
                 }
@@ -772,26 +827,45 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
                 tc_fence_after();
                 const float2 both = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
                 const float total = both.x + both.y, f = total == 0.0f ? 0.0f : 1.0f / total;   // (0: every logit is -inf)
-                const bool in = ok && row < it.len;
-                char* out = static_cast<char*>(p.out) + (static_cast<int64_t>(it.base + row) * p.n_q_heads + head) * (D * 2);
+                // Four neighbouring lanes exchange pieces of 16 bytes of their four rows, so that they write 64 bytes of one row at once:
+                // the stores of a lane's own row, 32 rows in each, took four times as long.
+                const int quarter = lane & 3, row4 = row - quarter;
+                const int64_t pitch = static_cast<int64_t>(p.n_q_heads) * (D * 2);
+                char* out = static_cast<char*>(p.out) + (it.base + row4) * pitch + head * (D * 2) + quarter * 16;
 #pragma unroll 1
                 for (int d0 = 0; d0 < D; d0 += 32) {
-                    uint32_t o[32];
+                    uint32_t o[32], x[4][4];
                     __syncwarp();
                     tmem_ld32(o, o_at + d0);
                     tc_wait_ld();
-                    if (in) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            auto pair = [&](int k) { return pack_bf16x2(__uint_as_float(o[e + k]) * f, __uint_as_float(o[e + k + 1]) * f); };
-                            *reinterpret_cast<uint4*>(out + (d0 + e) * 2) = make_uint4(pair(0), pair(2), pair(4), pair(6));
+                    for (int a = 0; a < 4; ++a)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            x[a][e] = pack_bf16x2(__uint_as_float(o[a * 8 + 2 * e]) * f, __uint_as_float(o[a * 8 + 2 * e + 1]) * f);
+#pragma unroll
+                    for (int bit = 1; bit <= 2; bit <<= 1)
+#pragma unroll
+                        for (int a = 0; a < 4; ++a) {
+                            if (a & bit) continue;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const bool upper = quarter & bit;
+                                const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? x[a][e] : x[a | bit][e], bit);
+                                if (upper) x[a][e] = got;
+                                else x[a | bit][e] = got;
+                            }
                         }
-                    }
+#pragma unroll
+                    for (int a = 0; a < 4; ++a)
+                        if (row4 + a < it.len) *reinterpret_cast<uint4*>(out + a * pitch + d0 * 2) = make_uint4(x[a][0], x[a][1], x[a][2], x[a][3]);
                 }
-                if (in && p.lse) p.lse[static_cast<int64_t>(it.base + row) * p.n_q_heads + head] = total == 0.0f ? -INFINITY : (ref + log2f(total)) * kLn2;
+                if (row < it.len && p.lse)
+                    p.lse[static_cast<int64_t>(it.base + row) * p.n_q_heads + head] = total == 0.0f ? -INFINITY : (ref + log2f(total)) * kLn2;
                 tc_fence_before();
             }
             n += 2 * (all_hi - all_lo + 1);
+            looks += masks.before(all_hi + 1);
         }
     }
     tc_fence_before();
