@@ -22,15 +22,16 @@
 // form of the loop: 245 us with items dealt out in advance, 209 so).
 //
 // Measured on one GB300 (operations of the places in view; 1932 TFLOP/s is the measured peak, 1727 under the power cap):
-//   one prompt of 16001 tokens, 64 and 8 heads of 128      2.64 ms, 1590 TFLOP/s (at the power cap: 1.75 GHz)
-//   16 prompts of 1..2047 tokens, 32 and 8 heads of 128    156 us, 1210 TFLOP/s
-//   24 prompts of 700..6001, windows of 1024, 16 heads of 64   498 us, 575 TFLOP/s
-//   one prompt of 4000 tokens, 16 and 4 heads of 256       123 us, 1070 TFLOP/s
-//   one prompt of 517 tokens, 12 and 2 heads of 128        15.8 us
-// A step of two tiles against one block takes 2650 cycles at D 128, 2048 of them the tensor cores', and 2400 at D 64, where the
-// products are 1024 and the softmax's own chain (TMEM, maximum, exp2 at 32 a cycle, bf16) is what is left. Tried and slower: two
-// threads a row (long 2.67 -> 3.60 ms: the four warps of a partition then do the same thing at the same time), P handed over in
-// halves, waits that sleep.
+//   one prompt of 16001 tokens, 64 and 8 heads of 128      2.66 ms, 1580 TFLOP/s (at the power cap: 1.75 GHz)
+//   16 prompts of 1..2047 tokens, 32 and 8 heads of 128    178 us, 1060 TFLOP/s
+//   24 prompts of 700..6001, windows of 1024, 16 heads of 64   430 us, 665 TFLOP/s
+//   one prompt of 4000 tokens, 16 and 4 heads of 256       122 us, 1070 TFLOP/s
+//   one prompt of 517 tokens, 12 and 2 heads of 128        13.6 us
+// A step of two tiles against one block takes 2400 to 2650 cycles: at D 128 2048 of them are the tensor cores', at D 64 1024, and the
+// softmax's own chain (TMEM, maximum, exp2 at 32 a cycle, bf16) is what is left. An item costs some 6000 cycles besides: its masked
+// block, the last product, the output (2500), the first S of the next. Tried and slower: two threads a row (long 2.67 -> 3.60 ms: the
+// four warps of a partition then do the same thing at the same time), P handed over in halves, waits that sleep, the output's
+// columns loaded ahead. V was looked at by the softmax's threads before, and each wrote its own row: a batch 197 us, windows 498.
 //
 // P in bf16 is the operands' type (V is bf16, and both must agree); it is off by 2^-8 of itself, as the output's rounding is,
 // and adds up over a row's keys as a random walk does. Sums of P are kept in fp32 from the values before rounding.
