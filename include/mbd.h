@@ -109,7 +109,9 @@ uint64_t mbd_kernel_launches(void);
 
 /* Device-side error bits. A kernel that splits a row over a thread-block cluster exchanges partial sums
  * through distributed shared memory and waits for its peers with a bounded wait (about one second); if
- * the wait ever ran out, the kernel set this bit and returned without writing its outputs. */
+ * the wait ever ran out, the kernel set this bit and returned without writing its outputs. The waits of
+ * mbd_prompt_attention between its loads, products and softmax are bounded in the same way (its CTA then leaves,
+ * with rows unwritten). */
 #define MBD_DEVERR_EXCHANGE_TIMEOUT 1u
 /* A key-value cache kernel met a page number outside the pool, a length outside [0, pages_per_seq * page_size] or
  * a new token without a slot: it read and wrote nothing there (a length is clamped, a slot on such a page counts
