@@ -646,7 +646,7 @@ mbd_status mbd_kv_cache_resize(int32_t* page_table, int64_t pages_per_seq, int64
  *   scale     : finite (also times log2(e)), usually 1 / sqrt(head_dim).   window: 0 (none) or the number of tokens in view.
  *   lse       : fp32 [n_tokens, n_q_heads], written, or null.
  * Logits, maxima and sums are fp32; exp(x_ij - lse_i) is rounded to bf16 for the product with v_j (off by 2^-8 of it). The
- * result does not depend on what else runs, and equal calls give equal bits. head_dim: 64, 128 or 256. Limits: n_tokens and n_seqs
+ * result does not depend on what else runs or on other sequences' rows, and equal calls give equal bits. head_dim: 64, 128 or 256. Limits: n_tokens and n_seqs
  * <= MBD_KV_MAX_ROWS, n_q_heads <= 4096, (n_tokens / 128 + n_seqs) * n_q_heads < 2^31. n_tokens == 0 or n_seqs == 0 is a no-op. Bounded waits: see MBD_DEVERR_EXCHANGE_TIMEOUT.
  */
 mbd_status mbd_prompt_attention(void* out, const void* q, int64_t q_stride, const void* k, const void* v, int64_t kv_stride,

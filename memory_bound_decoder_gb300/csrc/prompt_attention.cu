@@ -23,9 +23,9 @@
 //
 // Measured on one GB300 (operations of the places in view; 1932 TFLOP/s is the measured peak, 1727 under the power cap):
 //   one prompt of 16001 tokens, 64 and 8 heads of 128      2.66 ms, 1580 TFLOP/s (at the power cap: 1.75 GHz)
-//   16 prompts of 1..2047 tokens, 32 and 8 heads of 128    178 us, 1060 TFLOP/s
-//   24 prompts of 700..6001, windows of 1024, 16 heads of 64   430 us, 665 TFLOP/s
-//   one prompt of 4000 tokens, 16 and 4 heads of 256       122 us, 1070 TFLOP/s
+//   16 prompts of 1..2047 tokens, 32 and 8 heads of 128    179 us, 1060 TFLOP/s
+//   24 prompts of 700..6001, windows of 1024, 16 heads of 64   440 us, 650 TFLOP/s
+//   one prompt of 4000 tokens, 16 and 4 heads of 256       126 us, 1040 TFLOP/s
 //   one prompt of 517 tokens, 12 and 2 heads of 128        13.6 us
 // A step of two tiles against one block takes 2400 to 2650 cycles: at D 128 2048 of them are the tensor cores', at D 64 1024, and the
 // softmax's own chain (TMEM, maximum, exp2 at 32 a cycle, bf16) is what is left. An item costs some 6000 cycles besides: its masked
@@ -37,8 +37,9 @@
 // and adds up over a row's keys as a random walk does. Sums of P are kept in fp32 from the values before rounding.
 //
 // Values in masked places. A masked P is 0, and 0 times an infinite or NaN value would be NaN. So in blocks that hold masked
-// places (the diagonal, the window's edge; rows behind the sequence's end are masked by causality) a warp looks at V as it
-// arrives, and where it holds such a value the warpgroup adds that block's product itself, over the keys in view alone.
+// places (the diagonal, the window's edge) a warp looks at V as it arrives, and where it holds such a value the warpgroup adds that
+// block's product itself, over the keys in view alone. Where such values lie behind the sequence's end, which causality masks for
+// all of its rows, the same warp puts zeros in their place.
 //
 // Every wait is bounded: one that runs out sets the error bit, and all roles leave.
 #include <cuda.h>
@@ -587,17 +588,29 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
                         pass();
                         continue;
                     }
-                    const char* v = kv_stage(stage);
-                    uint32_t odd = 0;
+                    char* const v = kv_stage(stage);
+                    auto some_odd = [&] {
+                        uint32_t odd = 0;
 #pragma unroll 8
-                    for (int i = 0; i < P::kBlockBytes / 512; ++i) {
-                        const uint4 x = *reinterpret_cast<const uint4*>(v + (i * 32 + lane) * 16);
-                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                        for (int i = 0; i < P::kBlockBytes / 512; ++i) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(v + (i * 32 + lane) * 16);
+                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)   // 0 times it: 0 if it is finite, else NaN
-                            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(odd) : "r"(w[e]), "r"(0u));
+                            for (int e = 0; e < 4; ++e)   // 0 times it: 0 if it is finite, else NaN
+                                asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(odd) : "r"(w[e]), "r"(0u));
+                        }
+                        return __any_sync(0xffffffffu, odd != 0) != 0;
+                    };
+                    bool any = some_odd();
+                    const int rows = it.len - j * kRows;
+                    if (any && rows < kRows) {   // rows behind the sequence's end, which are masked for all of it: zeros, and once more
+                        for (int c = 0; c < P::kChunks; ++c)
+                            for (int i = rows * 8 + lane; i < kRows * 8; i += 32)
+                                *reinterpret_cast<uint4*>(v + c * P::kChunkBytes + i * 16) = make_uint4(0, 0, 0, 0);
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (the products read them by another way)
+                        __syncwarp();
+                        any = some_odd();
                     }
-                    const bool any = __any_sync(0xffffffffu, odd != 0);
                     if (lane == 0) {
                         sm.odd[looks % kLooks] = any;
                         mbar_arrive(&sm.looked[looks % kLooks]);
@@ -781,7 +794,9 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
                     ok &= mbar_wait(sm, &sm.pv_done[i], pv_phase ^ 1);
                     tc_fence_after();
                 }
-                if (__any_sync(0xffffffffu, top > lim)) {
+                // All rows of the warp follow if one has to (each on its own has more such blocks: windows 453 us, 440 so); rows behind
+                // the sequence's end have no say, so that what lies there changes no bit of it.
+                if (__any_sync(0xffffffffu, top > lim && row < it.len)) {
                     const float t = fmaxf(top, lim - kLazy), next = t == -INFINITY ? 0.0f : t;   // (lim - kLazy: the kept maximum)
                     const float old = lim == -INFINITY ? 0.0f : ex2(ref - next);
                     ref = next;

@@ -138,6 +138,29 @@ def test_masked_places_hold_anything(mbd, d, hq, hkv):
         assert np.isnan(lo[dirty]).all()                      # a NaN or infinite key among 2 d * hkv random ones: NaN logits
 
 
+@pytest.mark.parametrize("d,hq,hkv", [(128, 4, 2), (64, 3, 3), (256, 2, 1)])
+@pytest.mark.parametrize("window", [0, 70])
+def test_other_rows_change_no_bit(mbd, d, hq, hkv, window):
+    """What lies behind a sequence's end, in padding or in the next sequence, changes no bit of its rows."""
+    rng = np.random.default_rng(13)
+    qkv, cu = make(rng, [300, 5, 129, 0, 200], hq, hkv, d, pad=90)
+    want = None
+    for fill in (0, NAN, 0x7F80, 0x4640):
+        x = qkv.copy()
+        x[cu[-1]:] = fill
+        x[cu[1]:cu[2]] = fill                                # the second sequence
+        out, lse = run(mbd, x, cu, hq, hkv, d, d ** -0.5, window)
+        keep = np.ones(len(x), bool)
+        keep[cu[-1]:] = keep[cu[1]:cu[2]] = False
+        if want is None:
+            want = out[keep], lse[keep]
+        np.testing.assert_array_equal(out[keep], want[0])
+        np.testing.assert_array_equal(lse[keep], want[1])
+        alone, alone_lse = run(mbd, np.ascontiguousarray(x[:300]), cu[:2], hq, hkv, d, d ** -0.5, window)
+        np.testing.assert_array_equal(alone, out[:300])
+        np.testing.assert_array_equal(alone_lse, lse[:300])
+
+
 def test_infinite_values_in_view(mbd):
     """An infinity where one sign is in view, NaN where both are or a NaN is, in the columns concerned alone."""
     rng = np.random.default_rng(8)
