@@ -94,7 +94,8 @@ typedef enum {
 #define MBD_MAX_REDUCED_WIDTH 262144
 
 /* ABI version of this header (bumped on any signature change or added entry point). The key-value cache's
- * section at the end has a version of its own, MBD_KV_ABI_VERSION. */
+ * section at the end has a version of its own, MBD_KV_ABI_VERSION, and so has what goes with it in a serving step,
+ * MBD_STEP_ABI_VERSION. */
 #define MBD_ABI_VERSION 9
 int mbd_abi_version(void);
 
@@ -485,7 +486,7 @@ mbd_status mbd_launch_shape(int kind, int mode, int64_t n_tokens, int64_t width,
  * tensors of a call.
  * n_seqs == 0 (append: n_tokens == 0) is a no-op; the cache's description and the sizes are checked even so.
  */
-#define MBD_KV_ABI_VERSION 1
+#define MBD_KV_ABI_VERSION 1   /* (a format may be added without a new one: a library that lacks it refuses it) */
 int mbd_kv_abi_version(void);
 
 typedef enum { MBD_KV_BF16 = 0, MBD_KV_FP8 = 1, MBD_KV_NVFP4 = 4 } mbd_kv_format;
