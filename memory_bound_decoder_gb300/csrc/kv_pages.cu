@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kResizeThreads) kv_resize_kernel(const __grid_
         if (to != from) p.lens[b] = to;
         if (p.seen) {
             if (to > from) p.seen[b] = seen[b] + (to - from);
-            else if (to == 0) p.seen[b] = 0;
+            else if (to == 0 && good && p.want[b] == 0) p.seen[b] = 0;   // (not where an empty row was refused, or stays as it is)
         }
     }
     if (rank == 0 && tid == 0) {
