@@ -164,7 +164,9 @@ __global__ void __launch_bounds__(kResizeThreads) kv_resize_kernel(const __grid_
     for (int64_t i = static_cast<int64_t>(rank) * kResizeThreads + tid; i < all_given; i += threads) {
         const int b = sequence_of(given_before, n, i);
         int32_t* entry = p.table + b * p.pages_per_seq + pages_of(new_len[b]) + (i - given_before[b]);
-        if (i < given) p.ring[ring_place(free_pages + i)] = *entry;
+        const int32_t page = *entry;
+        if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.n_pages)) kv_bad_index();
+        if (i < given) p.ring[ring_place(free_pages + i)] = page;
         *entry = -1;
     }
     if (p.ctas > 1) cg::this_cluster().sync();   // (of global memory too: release and acquire at cluster scope)

@@ -44,3 +44,20 @@ def test_tokens_seen_of_empty_rows(mbd, room):
     p = emptied(rng, 9)
     p.step(mbd, [2, 0, 0, 0], room)
     assert mbd.device_error_flags() == 0
+
+
+@pytest.mark.parametrize("room", [6, 3000])
+@pytest.mark.parametrize("page", [-1, -7, 11, 1 << 30])
+def test_given_up_pages_outside_the_pool(mbd, page, room):
+    """Flagged in the call that gives them up, which hands them on to the ring as they are; so is the call that takes one."""
+    rng = np.random.default_rng(1)
+    p = Pages(rng, [20, 5], 4, 5, 4)
+    assert p.n_pages == 11
+    p.table[0, 3] = page
+    p.device()
+    mbd.device_error_flags(clear=True)
+    p.step(mbd, [4, 5], room)
+    assert mbd.device_error_flags(clear=True) == mbd.DEVERR_BAD_INDEX
+    assert page in p.ring
+    p.step(mbd, [4, 6], room)                        # nothing bad is touched
+    assert mbd.device_error_flags() == 0
