@@ -527,8 +527,9 @@ typedef struct {
  * FP8: code = e4m3(value / scale), both divisions rounded to nearest; dynamic: scale = amax / 448 of the head's
  * head_dim values, zero codes where that is 0. NVFP4: block scale = e4m3(amax / (6 * tensor scale)) of its 16 values, code =
  * e2m1(value / (block scale * tensor scale)), each product and division in fp32, rounded to nearest; zero codes where the
- * block scale is 0. (A tensor scale outside [2^-64, 2^64] gives zeros, and counts as 0 in the attention.) If the cache has
- * `weight`, the new slots' is set to 0.
+ * block scale is 0. (A tensor scale outside [2^-64, 2^64] gives zeros, and counts as 0 in the attention.) E2M1 has no NaN: a
+ * block with one gets the scale NaN (0x7F) and zero codes, so that all of it reads as NaN; an infinity counts as a value above
+ * all others (block scale 448, code 6). If the cache has `weight`, the new slots' is set to 0.
  */
 mbd_status mbd_kv_cache_append(const mbd_kv_cache* cache, const void* k, const void* v, int64_t row_stride,
                                const int32_t* page_table, int64_t pages_per_seq, const int32_t* seq_lens, int64_t n_seqs,

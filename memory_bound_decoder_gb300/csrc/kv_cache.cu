@@ -107,7 +107,7 @@ __device__ __forceinline__ uint32_t encode_nvfp4(const uint4& x, float amax, flo
     *block = 0;
     if (tensor_scale == 0.0f) return 0u;
     *block = pack_e4m3x2(__fdiv_rn(amax, 6.0f * tensor_scale), 0.0f) & 0xffu;
-    if (*block == 0u) return 0u;
+    if (*block == 0u || *block == 0x7fu) return 0u;   // (0x7f: NaN)
     const Divisor s = divisor(e4m3_value(*block) * tensor_scale);
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     float2 d[4];
@@ -126,6 +126,22 @@ __device__ __forceinline__ float amax(const uint4& x) {
     uint32_t m = max_bf16x2_bits(max_bf16x2_bits(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
                                  max_bf16x2_bits(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
     return fmaxf(bf16_lo(m), bf16_hi(m));
+}
+
+// The same, and NaN if one of them is: E2M1 has no NaN, so it is the block's scale that has to say so.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float amax_nan(const uint4& x) {
+    auto max2 = [](uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a & 0x7fff7fffu), "r"(b & 0x7fff7fffu));
+        return r;
+    };
+    const uint32_t m = max2(max2(x.x, x.y), max2(x.z, x.w));
+    return max_nan(bf16_lo(m), bf16_hi(m));
 }
 
 template <int STORE, int LANES>   // LANES = head_dim / 8: the lanes that own one head's row
@@ -204,9 +220,9 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
                     *reinterpret_cast<uint4*>(static_cast<char*>(p.c.v) + to) = v[u];
                 }
             } else if constexpr (STORE == kKvNvfp4) {   // a lane has half of a block
-                float ka = amax(k[u]), va = amax(v[u]);
-                ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, 1));
-                va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, 1));
+                float ka = amax_nan(k[u]), va = amax_nan(v[u]);
+                ka = max_nan(ka, __shfl_xor_sync(0xffffffffu, ka, 1));
+                va = max_nan(va, __shfl_xor_sync(0xffffffffu, va, 1));
                 uint32_t kf, vf;
                 const uint32_t kq = encode_nvfp4(k[u], ka, k_tensor, &kf), vq = encode_nvfp4(v[u], va, v_tensor, &vf);
                 if (live) {

@@ -26,9 +26,10 @@ def e2m1_codes(x: np.ndarray) -> np.ndarray:
 
 
 def encode(x: np.ndarray, s: float):
-    """Rows [..., d] -> (codes [..., d / 2], block scales [..., d / 16])."""
+    """Rows [..., d] -> (codes [..., d / 2], block scales [..., d / 16]). A block with a NaN: the scale NaN, zero codes."""
     y, s = x.astype(np.float32).reshape(x.shape[:-1] + (-1, 16)), np.float32(s)
-    sf = base.e4m3_codes(np.abs(y).max(-1) / (np.float32(6) * s))
+    amax = np.abs(y).max(-1)
+    sf = np.where(np.isnan(amax), np.uint8(0x7F), base.e4m3_codes(amax / (np.float32(6) * s)))
     scale = (base.E4M3[sf].astype(np.float32) * s)[..., None]
     q = np.where(scale > 0, e2m1_codes(y / np.where(scale > 0, scale, np.float32(1))), 0).astype(np.uint8).reshape(x.shape)
     return q[..., 0::2] | (q[..., 1::2] << 4), sf
