@@ -692,8 +692,8 @@ mbd_status mbd_rotary(void* out, int64_t out_stride, const void* x, int64_t x_st
  *   MBD_ROTARY_FACTORS : f_i = g_i / factors[i], a factor for each pair.
  * amplitude: as given; 0 means 1 (MBD_ROTARY_YARN: 0.1 ln(factor) + 1, and 1 for a factor up to 1). All in fp64. Host only: no stream, no launch.
  * MBD_ERR_INVALID_ARG for a null pointer, an unknown kind, a non-zero reserved, a rotary_dim that is not positive and even (NTK:
- * or is 2), a base or factor that is not positive and finite, an amplitude that is negative or not finite, and for values of a
- * kind's own that give no finite frequencies (low >= high; base 1 or betas or original not positive).
+ * or is 2), a base or factor that is not positive and finite, an amplitude that is negative or not finite (in fp32), and for values
+ * of a kind's own that give no finite frequencies (low >= high; base 1 or betas or original not positive).
  */
 typedef enum {
     MBD_ROTARY_PLAIN = 0,

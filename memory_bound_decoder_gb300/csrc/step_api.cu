@@ -205,7 +205,8 @@ mbd_status mbd_rotary_table(uint64_t* turns, float* amplitude, int64_t rotary_di
         return MBD_ERR_INVALID_ARG;
     const mbd_rotary_scaling& a = *scaling;
     const double dim = static_cast<double>(rotary_dim);
-    if (!positive(a.base) || !std::isfinite(a.amplitude) || a.amplitude < 0.0) return MBD_ERR_INVALID_ARG;
+    // (finite in fp32, as mbd_rotary takes it)
+    if (!positive(a.base) || !std::isfinite(static_cast<float>(a.amplitude)) || a.amplitude < 0.0) return MBD_ERR_INVALID_ARG;
     double base = a.base, first = 0.0, last = 0.0;
     switch (a.kind) {
         case MBD_ROTARY_PLAIN: break;

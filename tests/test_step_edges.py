@@ -1,7 +1,30 @@
 """Host-side edges of the serving step: entry points and references (no GPU)."""
-import numpy as np
+import ctypes
 
+import numpy as np
+import pytest
+
+import memory_bound_decoder_gb300 as mbd
+from memory_bound_decoder_gb300 import build as mbd_build
 from oracle import kv_nvfp4
+
+
+@pytest.fixture(scope="module")
+def lib():
+    mbd_build.build()
+    return mbd.get_lib()
+
+
+@pytest.mark.parametrize("kw", [dict(amplitude=1e39), dict(amplitude=3.4028236e38), dict(amplitude=1.7e308)])
+def test_amplitudes_that_fp32_does_not_hold_are_refused(lib, kw):
+    """rotary() takes the amplitude in fp32 and refuses an infinite one: the table that leads there is refused, and not written."""
+    args = mbd.RotaryScaling(0, 0, 10000.0, 1.0, 0.0, 1.0, 4.0, 32.0, 1.0, kw["amplitude"], None)
+    turns, amp = (ctypes.c_uint64 * 8)(*[7] * 8), ctypes.c_float(5.0)
+    assert lib.mbd_rotary_table(turns, ctypes.byref(amp), 16, ctypes.byref(args)) == mbd.ERR_INVALID_ARG
+    assert list(turns) == [7] * 8 and amp.value == 5.0
+    with pytest.raises(mbd.MbdError):
+        mbd.rotary_table(16, **kw)
+    assert mbd.rotary_table(16, amplitude=float(np.finfo(np.float32).max))[1] == np.finfo(np.float32).max
 
 
 def test_reference_of_blocks_that_are_not_finite():
