@@ -223,32 +223,61 @@ __device__ __forceinline__ void tmem_ld4(uint32_t (&r)[4], uint32_t at) {
 
 // ------------------------------------------------------------------------------------------ work
 
-// The row tiles (pairs of them) of all sequences, numbered, by a whole warp.
+// The row tiles (pairs of them) of all sequences, numbered, by a whole warp. Numbers mostly ascend from call to call.
 struct Rows {
     // Up to 256 sequences: by their place in their sequence, the last places first, as they see the most keys, so that what is
     // begun last takes the shortest. Sequence 32 c + lane has tiles[c]; `before` tiles lie at higher places than `place`.
     static constexpr int kMany = 8;
     int tiles[kMany];
     int place, top;
+    // More: one sequence behind the other, in each the last place first. Sequence first + 8 lane + c has tiles[c]; `upto` tiles belong to
+    // this lane's sequences and to those of the lanes before it, `before` to sequences before `first`. These are sums over whatever
+    // offsets there are: nothing is taken for ascending, so that a bad one costs the two sequences that it bounds and no others.
+    int first, upto;
     int64_t before;
 
+    // Tiles of a sequence from its bounds, none if they are not in order.
+    __device__ __forceinline__ static int tiles_of(const PromptParams& p, int shift, int from, int end) {
+        if (from >= 0 && end >= from && end <= static_cast<int>(p.n_tokens)) return (end - from + (1 << shift) - 1) >> shift;
+        kv_bad_index();
+        return 0;
+    }
+    // The kMany * 32 sequences from `first` on.
+    __device__ __forceinline__ void load(const PromptParams& p, int shift) {
+        const int lane = threadIdx.x & 31, b = first + lane * kMany, n = static_cast<int>(p.n_seqs);
+        int at[kMany + 1];
+#pragma unroll
+        for (int c = 0; c <= kMany; ++c) at[c] = b + c <= n ? p.cu[b + c] : 0;
+        upto = 0;
+#pragma unroll
+        for (int c = 0; c < kMany; ++c) {
+            tiles[c] = b + c < n ? tiles_of(p, shift, at[c], at[c + 1]) : 0;
+            upto += tiles[c];
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
+        }
+    }
     __device__ __forceinline__ void begin(const PromptParams& p, int shift) {
         const int lane = threadIdx.x & 31;
+        first = 0;
+        before = 0;
+        if (p.n_seqs > kMany * 32) {
+            load(p, shift);
+            return;
+        }
         int most = 0;
 #pragma unroll
         for (int c = 0; c < kMany; ++c) {
-            tiles[c] = 0;
-            const int64_t b = c * 32 + lane;
-            if (c * 32 >= p.n_seqs || b >= p.n_seqs || p.n_seqs > kMany * 32) continue;
-            const int64_t first = p.cu[b], end = p.cu[b + 1];
-            if (first >= 0 && end >= first && end <= p.n_tokens) tiles[c] = static_cast<int>((end - first + (1 << shift) - 1) >> shift);
-            else kv_bad_index();
+            const int b = c * 32 + lane;
+            tiles[c] = b < p.n_seqs ? tiles_of(p, shift, p.cu[b], p.cu[b + 1]) : 0;
             most = max(most, tiles[c]);
         }
         place = top = __reduce_max_sync(0xffffffffu, most) - 1;
-        before = 0;
     }
-    // Sequence and place of tile `number`; false if there are not so many. (Numbers mostly ascend from call to call.)
+    // Sequence and place of tile `number`; false if there are not so many.
     __device__ __forceinline__ bool find(const PromptParams& p, int shift, int64_t number, int64_t* seq, int64_t* at) {
         const int lane = threadIdx.x & 31;
         if (p.n_seqs <= kMany * 32) {
@@ -281,25 +310,39 @@ struct Rows {
             }
             return false;
         }
-        // More: one sequence behind the other, with room for one tile more in each, which needs no sums (sequence b's begin at cu[b]
-        // / rows + b); some numbers are no tile's.
-        const int64_t slot = p.slots - 1 - number;
-        int64_t lo = 0, hi = p.n_seqs;   // the last b whose tiles begin at or before slot
-        while (hi - lo > 1) {
-            const int64_t step = (hi - lo + 31) / 32, to = lo + (lane + 1) * step;
-            const unsigned above = __ballot_sync(0xffffffffu, to >= hi || (static_cast<int64_t>(p.cu[to]) >> shift) + to > slot);
-            const int64_t from = lo + (__ffs(above) - 1) * step;
-            hi = min(hi, from + step);
-            lo = from;
+        while (true) {
+            const int count = __shfl_sync(0xffffffffu, upto, 31);
+            if (number < before && first > 0) {
+                first -= kMany * 32;
+                load(p, shift);
+                before -= __shfl_sync(0xffffffffu, upto, 31);
+            } else if (number < before + count) {
+                break;
+            } else {
+                if (first + kMany * 32 >= p.n_seqs) return false;
+                before += count;
+                first += kMany * 32;
+                load(p, shift);
+            }
         }
-        const int64_t first = p.cu[lo], end = p.cu[lo + 1];
-        if (first < 0 || end < first || end > p.n_tokens) {
-            kv_bad_index();
-            return false;
-        }
-        *seq = lo;
-        *at = slot - ((first >> shift) + lo);
-        return *at >= 0 && *at << shift < end - first;
+        const int k = static_cast<int>(number - before), it = __ffs(__ballot_sync(0xffffffffu, upto > k)) - 1;
+        // Lane `it` has the sequence: `left` is the number's place among the lane's tiles, then among those of its sequence c.
+        int left = k - upto, c = 0;
+#pragma unroll
+        for (int i = 0; i < kMany; ++i) left += tiles[i];
+#pragma unroll
+        for (int i = 0; i < kMany - 1; ++i)
+            if (c == i && left >= tiles[i]) {
+                left -= tiles[i];
+                ++c;
+            }
+        int here = tiles[kMany - 1];
+#pragma unroll
+        for (int i = 0; i < kMany - 1; ++i)
+            if (c == i) here = tiles[i];
+        *seq = first + it * kMany + __shfl_sync(0xffffffffu, c, it);
+        *at = __shfl_sync(0xffffffffu, here - 1 - left, it);
+        return true;
     }
 };
 
@@ -307,7 +350,7 @@ struct Rows {
 template <int TILES>
 __device__ __forceinline__ bool item_at(const PromptParams& p, Rows& rows, int64_t index, Item* item) {
     const int shift = p.pair_rows ? 8 : 7;
-    const int64_t number = index / p.units, unit = index - number * p.units;
+    const unsigned units = static_cast<unsigned>(p.units), number = static_cast<unsigned>(index) / units, unit = static_cast<unsigned>(index) - number * units;
     int64_t seq, at;
     if (!rows.find(p, shift, number, &seq, &at)) return false;
     const int64_t first = p.cu[seq];

@@ -51,9 +51,8 @@ struct PromptParams {
     int64_t n_seqs;
     int64_t n_tokens;
     int64_t window;             // 0: no window
-    int64_t slots;              // numbers of row tiles, some of them no tile's
     int64_t units;              // query heads, or pairs of them, that share a row tile's number
-    int64_t items;              // slots * units, at most 2^31 - 1: the grid
+    int64_t items;              // numbers of row tiles (some of them no tile's) * units, at most 2^31 - 1: the grid
     float scale_log2;           // |scale| * log2(e), not 0
     int negate;                 // the scale is negative
     int pair_rows;              // a CTA's two tiles are neighbours in the rows, not two heads

@@ -153,7 +153,6 @@ mbd_status mbd_prompt_attention(void* out, const void* q, int64_t q_stride, cons
     p.group = static_cast<int>(n_q_heads / n_kv_heads);
     p.head_dim = static_cast<int>(head_dim);
     p.pair_rows = pair_rows;
-    p.slots = slots;
     p.units = units;
     p.items = slots * units;
     p.negate = scale < 0.0f;
