@@ -78,8 +78,12 @@ struct Item {
     int kv_head;
     int head[2], row[2]; // query head and first row (in the sequence) of each tile
     int lo[2], hi[2];    // blocks that the tile's rows see any key of; none if lo > hi
-    int more;            // 0: there is none, and none follows
+    int more;            // 0: there is none, and none follows; kLater: none yet
 };
+
+// After this many indexes that are no tile's the search tells those who wait for an item that there is none yet, and goes on: where nearly
+// all are no tile's, as with millions of empty sequences, it takes longer than a wait may (some 0.6 us each).
+constexpr int kSearch = 1 << 14, kLater = 2;
 
 // Blocks of V that may be looked at ahead of the softmax: more than the stages hold.
 constexpr int kLooks = 8;
@@ -507,12 +511,15 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
     const uint32_t tmem = sm.tmem;
 
     // Items come by way of shared memory: k counts them.
-    auto next_item = [&](unsigned k, Item* it) {
-        const bool ok = __all_sync(0xffffffffu, mbar_wait(sm, &sm.item_full, k & 1));
-        if (!ok) return false;
-        *it = sm.item;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.item_empty);
+    auto next_item = [&](unsigned& k, Item* it) {
+        do {
+            const bool ok = __all_sync(0xffffffffu, mbar_wait(sm, &sm.item_full, k & 1));
+            if (!ok) return false;
+            *it = sm.item;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.item_empty);
+            ++k;
+        } while (it->more == kLater);
         return it->more != 0;
     };
     Item it;
@@ -553,21 +560,22 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
                 if (!(ok = __all_sync(0xffffffffu, mbar_wait(sm, &sm.item_empty, (k & 1) ^ 1)))) break;
                 if (k > 0) index = steal(&ok);
                 bool found = false;
-                while (ok && index >= 0 && !(found = item_at<TILES>(p, rows, index, &it))) index = steal(&ok);
+                for (int steps = 1; ok && index >= 0 && !(found = item_at<TILES>(p, rows, index, &it)) && steps < kSearch; ++steps)
+                    index = steal(&ok);
                 if (!ok) break;
-                if (!found) it.more = 0;
+                if (!found) it.more = index >= 0 ? kLater : 0;
                 if (lane == 0) {
                     sm.item = it;
                     mbar_arrive(&sm.item_full);
                 }
-                if (!found) break;
+                if (it.more == 0) break;
             }
         } else if (warp == TILES * 4 + 1) {
             // ---- loads
             unsigned n = 0;                 // blocks of keys or values so far
             uint32_t q_phase[2] = {0, 0};
             bool ok = true;
-            for (unsigned k = 0; ok && next_item(k, &it); ++k) {
+            for (unsigned k = 0; ok && next_item(k, &it);) {
                 blocks_of<TILES>(it, &all_lo, &all_hi);
                 if (lane == 0) {
                     for (int i = 0; ok && i < TILES; ++i) {
@@ -616,7 +624,7 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
                 if (lane == 0) mbar_arrive(&sm.kv_empty[seen % P::kStages]);
                 ++seen;
             };
-            for (unsigned k = 0; ok && next_item(k, &it); ++k) {
+            for (unsigned k = 0; ok && next_item(k, &it);) {
                 blocks_of<TILES>(it, &all_lo, &all_hi);
                 const Looks masked = Looks::of<TILES>(p, it, all_lo);
                 for (int j = all_lo; ok && j <= all_hi; ++j) {
@@ -681,7 +689,7 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
                 __device__ __forceinline__ Stage next() const { return at + 1 == P::kStages ? Stage{0u, phase ^ 1u} : Stage{at + 1, phase}; }
             };
             Stage stage{0, 0}, last{0, 1};   // the next block of keys or values, and the last one
-            for (unsigned k = 0; next_item(k, &it); ++k) {
+            for (unsigned k = 0; next_item(k, &it);) {
                 int tile_lo[TILES], tile_hi[TILES], row[TILES];
 #pragma unroll
                 for (int i = 0; i < TILES; ++i) {
@@ -790,7 +798,7 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
         uint32_t s_phase = 0, pv_phase = 0;   // of the next S, of the next P V
         bool ok = true;
         const float scale = p.scale_log2;
-        for (unsigned k = 0; ok && next_item(k, &it); ++k) {
+        for (unsigned k = 0; ok && next_item(k, &it);) {
             blocks_of<TILES>(it, &all_lo, &all_hi);
             const int lo = i ? it.lo[1] : it.lo[0], hi = i ? it.hi[1] : it.hi[0], row0 = i ? it.row[1] : it.row[0];
             const int head = i ? it.head[1] : it.head[0], row = row0 + tid;

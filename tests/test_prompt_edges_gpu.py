@@ -34,3 +34,21 @@ def test_bad_offsets_among_many(mbd, n, hq, hkv, d):
         np.testing.assert_array_equal(out[~left], want[~left], f"{at} {value}")
         np.testing.assert_array_equal(lse[~left], want_lse[~left], f"{at} {value}")
         assert (out[left] == 0x5A5A).all()
+
+
+def test_rows_of_mostly_empty_sequences(mbd):
+    """Sixteen million sequences, nearly all of them empty, and 64 pairs of heads: each CTA goes through seven million indexes
+    that are no tile's, which takes longer than a wait's limit, while its other warps wait."""
+    n, hq, hkv, d = 1 << 24, 128, 1, 64
+    rng = np.random.default_rng(3)
+    lens = np.zeros(n, np.int64)
+    at = [0, 1, 31, 32, 1000, n // 2, n - 33, n - 2, n - 1]
+    lens[at] = [1, 40, 3, 129, 2, 300, 5, 1, 130]
+    qkv, cu = make(rng, lens, hq, hkv, d, pad=30)
+    mbd.device_error_flags(clear=True)
+    out, lse = run(mbd, qkv, cu, hq, hkv, d, 0.1)
+    assert mbd.device_error_flags() == 0
+    some = np.concatenate([[0], np.cumsum(lens[at])]).astype(np.int32)
+    want, want_lse = run(mbd, qkv, some, hq, hkv, d, 0.1)
+    np.testing.assert_array_equal(out, want)
+    np.testing.assert_array_equal(lse, want_lse)
