@@ -845,16 +845,18 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
                     ok &= mbar_wait(sm, &sm.pv_done[i], pv_phase ^ 1);
                     tc_fence_after();
                 }
-                // All rows of the warp follow if one has to (each on its own has more such blocks: windows 453 us, 440 so); rows behind
-                // the sequence's end have no say, so that what lies there changes no bit of it.
-                if (__any_sync(0xffffffffu, top > lim && row < it.len)) {
-                    const float t = fmaxf(top, lim - kLazy), next = t == -INFINITY ? 0.0f : t;   // (lim - kLazy: the kept maximum)
-                    const float old = lim == -INFINITY ? 0.0f : ex2(ref - next);
-                    ref = next;
-                    lim = t + kLazy;
+                // A row goes by its own logits alone, so that the rows after it, whose tokens it does not see, change no bit of it. (Those
+                // behind the sequence's end have no say at all.)
+                const bool up = top > lim;
+                if (__any_sync(0xffffffffu, up && row < it.len)) {
+                    if (j > lo) {
+                        const float old = !up ? 1.0f : (lim == -INFINITY ? 0.0f : ex2(ref - top));
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) sum[c] = __fmul2_rn(sum[c], f2(old));
-                    if (j > lo) rescale<D>(o_at, old);
+                        for (int c = 0; c < 4; ++c) sum[c] = __fmul2_rn(sum[c], f2(old));
+                        rescale<D>(o_at, old);
+                    }
+                    ref = up ? top : ref;
+                    lim = up ? top + kLazy : lim;
                 }
                 const float2 scale2 = f2(scale), ref2 = f2(-ref);
 #pragma unroll

@@ -52,3 +52,23 @@ def test_rows_of_mostly_empty_sequences(mbd):
     want, want_lse = run(mbd, qkv, some, hq, hkv, d, 0.1)
     np.testing.assert_array_equal(out, want)
     np.testing.assert_array_equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(128, 4, 2), (64, 3, 3), (64, 2, 1), (256, 2, 1), (128, 1, 1)])
+@pytest.mark.parametrize("window", [0, 1, 70, 200])
+def test_prefixes(mbd, d, hq, hkv, window):
+    """A prompt's first rows have the bits that they have without the rest of it, and with another rest."""
+    rng = np.random.default_rng(d + window)
+    qkv, cu = make(rng, [420], hq, hkv, d, sigma=3.0)
+    # logits whose maximum moves: late queries meet the keys of every block with growing size
+    qkv[:, :hq * d] = np.where(rng.random((420, 1)) < 0.2, qkv[:, :hq * d] + 0x100, qkv[:, :hq * d])   # (four times as large)
+    whole, whole_lse = run(mbd, qkv, cu, hq, hkv, d, d ** -0.5, window)
+    for length in (1, 2, 17, 33, 100, 127, 128, 129, 200, 255, 257, 300, 385):
+        cut, cut_lse = run(mbd, np.ascontiguousarray(qkv[:length]), np.array([0, length], np.int32), hq, hkv, d, d ** -0.5, window)
+        np.testing.assert_array_equal(cut, whole[:length], f"{length}")
+        np.testing.assert_array_equal(cut_lse, whole_lse[:length], f"{length}")
+        other = qkv.copy()
+        other[length:] = make(rng, [420 - length], hq, hkv, d, sigma=20.0)[0]
+        out, lse = run(mbd, other, cu, hq, hkv, d, d ** -0.5, window)
+        np.testing.assert_array_equal(out[:length], whole[:length], f"{length}")
+        np.testing.assert_array_equal(lse[:length], whole_lse[:length], f"{length}")
