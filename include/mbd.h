@@ -638,8 +638,9 @@ mbd_status mbd_kv_cache_resize(int32_t* page_table, int64_t pages_per_seq, int64
  * window > 0 the last `window` of them:
  *     x_ij = scale * (q_i . k_j),   lse_i = log(sum_j exp(x_ij)),   out_i = bf16(sum_j exp(x_ij - lse_i) * v_j)
  * A row whose logits are all -inf gives zeros and lse = -inf. A logit of NaN or +inf gives NaN. What lies in masked places (later
- * tokens, tokens before the window, other sequences' rows) changes nothing, NaN and infinities among it; an infinite value in view
- * gives an infinity (where its probability is above 2^-100: far below, the product with zero is NaN).
+ * tokens, tokens before the window, other sequences' rows) changes no bit, NaN and infinities among it, so a prefix has the bits that it
+ * has alone; an infinite value in view gives an infinity (where its probability is above 2^-100: far below, the product with zero is
+ * NaN).
  *   out       : [n_tokens, n_q_heads * head_dim] bf16, 16-byte aligned, written; rows from cu_tokens[n_seqs] on are left alone.
  *   q         : n_tokens rows of n_q_heads * head_dim bf16, q_stride elements apart (0: dense); k, v: rows of n_kv_heads *
  *               head_dim, kv_stride elements apart (0: dense): slices of the stacked projection need no copy.

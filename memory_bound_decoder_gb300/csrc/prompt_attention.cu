@@ -37,9 +37,9 @@
 // and adds up over a row's keys as a random walk does. Sums of P are kept in fp32 from the values before rounding.
 //
 // Values in masked places. A masked P is 0, and 0 times an infinite or NaN value would be NaN. So in blocks that hold masked
-// places (the diagonal, the window's edge) a warp looks at V as it arrives, and where it holds such a value the warpgroup adds that
-// block's product itself, over the keys in view alone. Where such values lie behind the sequence's end, which causality masks for
-// all of its rows, the same warp puts zeros in their place.
+// places (the diagonal, the window's edge) a warp looks at V as it arrives and puts zeros for such values, which leave every other
+// value's product as it is, bit for bit; before that product the softmax's threads add P times each of them that their row sees to O,
+// reading them from the call's V once more. In a block that all rows see whole the product does it.
 //
 // Every wait is bounded: one that runs out sets the error bit, and all roles leave.
 #include <cuda.h>
@@ -94,8 +94,9 @@ struct PromptSmem {
     alignas(16) uint4 reply;
     Item item;
     uint32_t tmem;
-    int by_hand[2];             // this block's P V of the tile is the warpgroup's
+    int begun[2];               // the tile's O holds something before its first block's product
     volatile int odd[kLooks];   // whether the block holds a value that is not finite
+    uint32_t odd_rows[kLooks][kRows / 32];   // its rows that do, if so
     volatile int abort;
 };
 
@@ -403,15 +404,18 @@ struct Looks {
         const int low = max(all_lo, edge > 0 ? static_cast<int>((edge + kRows - 1) / kRows) : 0);
         return Looks{all_lo, low, max(low, it.row[0] / kRows)};
     }
+    __device__ __forceinline__ bool has(int j) const { return j < low || j >= high; }
     // How many of them come before block j.
     __device__ __forceinline__ int before(int j) const { return min(j, low) - first + max(0, j - high); }
 };
 
 // ------------------------------------------------------------------------------------------ softmax
 
-// This thread's row of one block's P V, over the keys klo .. khi in view, on top of what O holds (if `add`); p is in TMEM.
+// P times the values that are not finite, of the block's rows in `odd`, over the keys klo .. khi in view, on top of what this thread's row
+// of O holds (if `add`). v: the block's first row in global memory, `stride` bytes apart; P is in TMEM.
 template <int D>
-__device__ __noinline__ void product_by_hand(const char* v, uint32_t p_at, uint32_t o_at, int key0, int klo, int khi, bool add) {
+__device__ __noinline__ void add_odd(const uint32_t (&odd)[kRows / 32], const char* v, int64_t stride, uint32_t p_at, uint32_t o_at,
+                                     int key0, int klo, int khi, bool add) {
 #pragma unroll 1
     for (int d0 = 0; d0 < D; d0 += 32) {
         uint32_t o[32];
@@ -424,6 +428,8 @@ __device__ __noinline__ void product_by_hand(const char* v, uint32_t p_at, uint3
         }
 #pragma unroll 1
         for (int c0 = 0; c0 < kRows; c0 += 8) {
+            const uint32_t some = odd[c0 / 32] >> (c0 % 32) & 0xffu;
+            if (some == 0) continue;
             uint32_t p[4];
             __syncwarp();
             tmem_ld4(p, p_at + c0 / 2);
@@ -431,17 +437,17 @@ __device__ __noinline__ void product_by_hand(const char* v, uint32_t p_at, uint3
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 const int at = c0 + c;
-                if (key0 + at < klo || key0 + at > khi) continue;
+                if (!(some >> c & 1u) || key0 + at < klo || key0 + at > khi) continue;
                 const float pc = c & 1 ? bf16_hi(p[c / 2]) : bf16_lo(p[c / 2]);
-                const char* row = v + (d0 / 64) * Prompt<D>::kChunkBytes + at * 128;
+                const uint4* row = reinterpret_cast<const uint4*>(v + at * stride + d0 * 2);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(row + ((((d0 % 64) / 8 + j) ^ (at & 7)) * 16));
+                    const uint4 x = row[j];
                     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        o[j * 8 + 2 * k] = __float_as_uint(fmaf(pc, bf16_lo(w[k]), __uint_as_float(o[j * 8 + 2 * k])));
-                        o[j * 8 + 2 * k + 1] = __float_as_uint(fmaf(pc, bf16_hi(w[k]), __uint_as_float(o[j * 8 + 2 * k + 1])));
+                    for (int k = 0; k < 8; ++k) {
+                        const float value = k & 1 ? bf16_hi(w[k / 2]) : bf16_lo(w[k / 2]);
+                        if (!isfinite(value)) o[j * 8 + k] = __float_as_uint(fmaf(pc, value, __uint_as_float(o[j * 8 + k])));
                     }
                 }
             }
@@ -487,7 +493,7 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
             mbar_init(&sm.s_free[i], 4);
             mbar_init(&sm.p_full[i], 4);
             mbar_init(&sm.pv_done[i], 1);
-            sm.by_hand[i] = 0;
+            sm.begun[i] = 0;
         }
         for (int i = 0; i < kLooks; ++i) mbar_init(&sm.looked[i], 1);
         for (int i = 0; i < P::kStages; ++i) {
@@ -635,32 +641,44 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
                     }
                     if (ok) arrived();
                     if (!ok) break;
-                    if (j >= masked.low && j < masked.high) {
+                    if (!masked.has(j)) {
                         pass();
                         continue;
                     }
                     char* const v = kv_stage(stage);
-                    auto some_odd = [&] {
-                        uint32_t odd = 0;
+                    uint32_t odd = 0;
 #pragma unroll 8
-                        for (int i = 0; i < P::kBlockBytes / 512; ++i) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(v + (i * 32 + lane) * 16);
-                            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                    for (int i = 0; i < P::kBlockBytes / 512; ++i) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(v + (i * 32 + lane) * 16);
+                        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)   // 0 times it: 0 if it is finite, else NaN
-                                asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(odd) : "r"(w[e]), "r"(0u));
+                        for (int e = 0; e < 4; ++e)   // 0 times it: 0 if it is finite, else NaN
+                            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(odd) : "r"(w[e]), "r"(0u));
+                    }
+                    const bool any = __any_sync(0xffffffffu, odd != 0) != 0;
+                    if (any) {
+                        uint32_t* const rows = sm.odd_rows[looks % kLooks];
+                        constexpr uint32_t kOdd = 0x7f80u;   // the exponent of infinities and NaN
+                        if (lane < kRows / 32) rows[lane] = 0;
+                        __syncwarp();
+#pragma unroll 1
+                        for (int i = lane; i < P::kBlockBytes / 16; i += 32) {
+                            uint4* const at = reinterpret_cast<uint4*>(v + i * 16);
+                            const uint4 x = *at;
+                            uint32_t w[4] = {x.x, x.y, x.z, x.w}, cleared = 0;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t keep = ((w[e] & kOdd) == kOdd ? 0u : 0xffffu) | ((w[e] >> 16 & kOdd) == kOdd ? 0u : 0xffff0000u);
+                                cleared |= ~keep;
+                                w[e] &= keep;
+                            }
+                            if (cleared == 0) continue;
+                            *at = make_uint4(w[0], w[1], w[2], w[3]);
+                            const int row = i % (P::kChunkBytes / 16) / 8;
+                            atomicOr(&rows[row / 32], 1u << (row % 32));
                         }
-                        return __any_sync(0xffffffffu, odd != 0) != 0;
-                    };
-                    bool any = some_odd();
-                    const int rows = it.len - j * kRows;
-                    if (any && rows < kRows) {   // rows behind the sequence's end, which are masked for all of it: zeros, and once more
-                        for (int c = 0; c < P::kChunks; ++c)
-                            for (int i = rows * 8 + lane; i < kRows * 8; i += 32)
-                                *reinterpret_cast<uint4*>(v + c * P::kChunkBytes + i * 16) = make_uint4(0, 0, 0, 0);
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (the products read them by another way)
                         __syncwarp();
-                        any = some_odd();
                     }
                     if (lane == 0) {
                         sm.odd[looks % kLooks] = any;
@@ -734,15 +752,13 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
                     }
                     p_phase[i] ^= 1;
                     tc_fence_after();
-                    bool by_hand = false;
-                    if (some_masked(p, row[i], j * kRows)) by_hand = __shfl_sync(0xffffffffu, sm.by_hand[i], 0);
-                    if (!by_hand) {
+                    bool begun = j > tile_lo[i];
+                    if (!begun) begun = __shfl_sync(0xffffffffu, sm.begun[i], 0);
 #pragma unroll
-                        for (int k = 0; k < kRows / 16; ++k) {
-                            if (k == kRows / 16 - 2) look();
-                            mma_ts(tmem + P::kColumnsO + i * D, tmem + P::kColumnsP + i * (kRows / 2) + k * 8, b + (k * 2048 >> 4), kDescO,
-                                   k > 0 || j > tile_lo[i], elected);
-                        }
+                    for (int k = 0; k < kRows / 16; ++k) {
+                        if (k == kRows / 16 - 2) look();
+                        mma_ts(tmem + P::kColumnsO + i * D, tmem + P::kColumnsP + i * (kRows / 2) + k * 8, b + (k * 2048 >> 4), kDescO,
+                               k > 0 || begun, elected);
                     }
                     tc_commit(&sm.pv_done[i], elected);
                 };
@@ -794,7 +810,7 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) * 32 << 16;
         const uint32_t s_at = tmem + lanes + P::kColumnsS + (P::kBuffers == 2 ? i * kRows : 0);
         const uint32_t p_at = tmem + lanes + P::kColumnsP + i * (kRows / 2), o_at = tmem + lanes + P::kColumnsO + i * D;
-        unsigned n = 0, looks = 0;
+        unsigned looks = 0;
         uint32_t s_phase = 0, pv_phase = 0;   // of the next S, of the next P V
         bool ok = true;
         const float scale = p.scale_log2;
@@ -871,17 +887,19 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
                     }
                     tmem_st16(packed, p_at + c * 16);
                 }
-                if (masked) {
-                    // V's rows of this block: any value that is not finite?
-                    const unsigned look = looks + masks.before(j), stage = n + 2 * (j - all_lo) + (j < all_hi ? 2 : 1);
+                if (masks.has(j)) {   // V's rows of this block: any value that is not finite?
+                    const unsigned look = looks + masks.before(j);
                     ok &= mbar_wait(sm, &sm.looked[look % kLooks], look / kLooks & 1);
                     __syncwarp();
                     const bool any = sm.odd[look % kLooks] != 0;
                     if (any) {
                         tc_wait_st();
-                        product_by_hand<D>(kv_stage(stage), p_at, o_at, key0, klo, row, j > lo);
+                        add_odd<D>(sm.odd_rows[look % kLooks], static_cast<const char*>(p.v) + (it.base + key0) * p.v_bytes + it.kv_head * (D * 2), p.v_bytes, p_at, o_at,
+                                   key0, klo, min(row, it.len - 1), j > lo);
                     }
-                    if (tid == 0) sm.by_hand[i] = any;
+                    if (j == lo && tid == 0) sm.begun[i] = any;
+                } else if (j == lo && tid == 0) {
+                    sm.begun[i] = 0;
                 }
                 pv_phase ^= 1;
                 tc_wait_st();
@@ -933,7 +951,6 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
                     p.lse[static_cast<int64_t>(it.base + row) * p.n_q_heads + head] = total == 0.0f ? -INFINITY : (ref + log2f(total)) * kLn2;
                 tc_fence_before();
             }
-            n += 2 * (all_hi - all_lo + 1);
             looks += masks.before(all_hi + 1);
         }
     }

@@ -45,6 +45,8 @@ struct ResizeParams {
 
 struct PromptParams {
     CUtensorMap q_map, k_map, v_map;   // boxes of 64 elements and 128 rows, swizzled by 128 bytes
+    const void* v;              // rows v_bytes apart, as in v_map
+    int64_t v_bytes;
     void* out;                  // [n_tokens, n_q_heads * head_dim] bf16
     float* lse;                 // [n_tokens, n_q_heads] or null
     const int32_t* cu;          // [n_seqs + 1]

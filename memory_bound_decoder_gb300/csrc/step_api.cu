@@ -143,6 +143,8 @@ mbd_status mbd_prompt_attention(void* out, const void* q, int64_t q_stride, cons
     if (!encode_rows(&p.q_map, q, width, n_tokens, q_stride) || !encode_rows(&p.k_map, k, kv_width, n_tokens, kv_stride) ||
         !encode_rows(&p.v_map, v, kv_width, n_tokens, kv_stride))
         return static_cast<mbd_status>(mbd::kv_finish_launch(cudaErrorInvalidValue));
+    p.v = v;
+    p.v_bytes = kv_stride * 2;
     p.out = out;
     p.lse = lse;
     p.cu = cu_tokens;

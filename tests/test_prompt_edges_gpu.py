@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 
 from tests.test_kv_gpu import mbd  # noqa: F401  (mbd is the fixture)
-from tests.test_prompt_gpu import make, run
+from tests.test_prompt_gpu import NAN, make, run
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -72,3 +72,36 @@ def test_prefixes(mbd, d, hq, hkv, window):
         out, lse = run(mbd, other, cu, hq, hkv, d, d ** -0.5, window)
         np.testing.assert_array_equal(out[:length], whole[:length], f"{length}")
         np.testing.assert_array_equal(lse[:length], whole_lse[:length], f"{length}")
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(128, 4, 2), (64, 3, 3), (64, 2, 1), (256, 2, 1), (128, 1, 1)])
+@pytest.mark.parametrize("window", [0, 1, 50, 128, 200])
+def test_masked_values_change_no_bit(mbd, d, hq, hkv, window):
+    """NaN and infinite rows after a row and before its window: the bits are those of a prompt where they are finite. Rows that see
+    an infinite value alone have it, beside the finite columns' bits."""
+    rng = np.random.default_rng(d + window)
+    length = 520
+    qkv, cu = make(rng, [150, length], hq, hkv, d, pad=20, sigma=0.5)
+    base, base_lse = run(mbd, qkv, cu, hq, hkv, d, 0.02, window)
+    kv = slice(hq * d, (hq + 2 * hkv) * d)
+    v0 = (hq + hkv) * d
+    for at in (0, 1, 100, 127, 128, 200, 255, 256, 300, 383, 384, 519):
+        row = int(cu[1]) + at
+        sees = np.zeros(len(qkv), bool)
+        sees[row:min(cu[2], row + window) if window else cu[2]] = True
+        odd = qkv.copy()
+        odd[row, kv] = rng.choice([NAN, 0x7F80, 0xFF80], odd[0, kv].shape)
+        odd[row, :hq * d] = NAN
+        out, lse = run(mbd, odd, cu, hq, hkv, d, 0.02, window)
+        keep = ~sees
+        keep[cu[-1]:] = False
+        np.testing.assert_array_equal(out[keep], base[keep], f"{at}")
+        np.testing.assert_array_equal(lse[keep], base_lse[keep], f"{at}")
+        one = qkv.copy()                             # an infinite value alone: of the last key-value head, in one column
+        one[row, v0 + hkv * d - 3] = 0xFF80
+        out, lse = run(mbd, one, cu, hq, hkv, d, 0.02, window)
+        want = base.copy()
+        want[sees, (hkv - 1) * (hq // hkv):, d - 3] = 0xFF80
+        want[cu[-1]:] = 0x5A5A
+        np.testing.assert_array_equal(out, want, f"{at}")
+        np.testing.assert_array_equal(lse, base_lse)
