@@ -634,7 +634,8 @@ mbd_status mbd_kv_cache_resize(int32_t* page_table, int64_t pages_per_seq, int64
 
 /*
  * Causal attention of whole prompts, packed one behind the other: rows cu_tokens[b] .. cu_tokens[b + 1] - 1 are sequence b's
- * tokens in order. Query head h reads key-value head h / (n_q_heads / n_kv_heads). Row i of a sequence sees its rows j <= i, with
+ * tokens in order, all that it has: tokens that a cache holds from earlier steps are not seen, so the row of a sequence that is decoded
+ * (one more token, by mbd_kv_cache_resize) gets its result from mbd_paged_attention_decode. Query head h reads key-value head h / (n_q_heads / n_kv_heads). Row i of a sequence sees its rows j <= i, with
  * window > 0 the last `window` of them:
  *     x_ij = scale * (q_i . k_j),   lse_i = log(sum_j exp(x_ij)),   out_i = bf16(sum_j exp(x_ij - lse_i) * v_j)
  * A row whose logits are all -inf gives zeros and lse = -inf. A logit of NaN or +inf gives NaN. What lies in masked places (later
