@@ -634,9 +634,9 @@ mbd_status mbd_kv_cache_resize(int32_t* page_table, int64_t pages_per_seq, int64
 
 /*
  * Causal attention of whole prompts, packed one behind the other: rows cu_tokens[b] .. cu_tokens[b + 1] - 1 are sequence b's
- * tokens in order, all that it has: tokens that a cache holds from earlier steps are not seen, so the row of a sequence that is decoded
- * (one more token, by mbd_kv_cache_resize) gets its result from mbd_paged_attention_decode. Query head h reads key-value head h / (n_q_heads / n_kv_heads). Row i of a sequence sees its rows j <= i, with
- * window > 0 the last `window` of them:
+ * tokens in order, all that it has: tokens that a cache holds from earlier steps are not seen, so the row of a sequence that is
+ * decoded (one more token, by mbd_kv_cache_resize) gets its result from mbd_paged_attention_decode. Query head h reads key-value
+ * head h / (n_q_heads / n_kv_heads). Row i of a sequence sees its rows j <= i, with window > 0 the last `window` of them:
  *     x_ij = scale * (q_i . k_j),   lse_i = log(sum_j exp(x_ij)),   out_i = bf16(sum_j exp(x_ij - lse_i) * v_j)
  * A row whose logits are all -inf gives zeros and lse = -inf. A logit of NaN or +inf gives NaN. What lies in masked places (later
  * tokens, tokens before the window, other sequences' rows) changes no bit, NaN and infinities among it, so a prefix has the bits that it
@@ -649,9 +649,12 @@ mbd_status mbd_kv_cache_resize(int32_t* page_table, int64_t pages_per_seq, int64
  *               sequence whose bounds are not (MBD_DEVERR_BAD_INDEX) is left out.
  *   scale     : finite (also times log2(e)), usually 1 / sqrt(head_dim).   window: 0 (none) or the number of tokens in view.
  *   lse       : fp32 [n_tokens, n_q_heads], written, or null.
- * Logits, maxima and sums are fp32; exp(x_ij - lse_i) is rounded to bf16 for the product with v_j (off by 2^-8 of it). The
- * result does not depend on what else runs or on other sequences' rows, and equal calls give equal bits. head_dim: 64, 128 or 256. Limits: n_tokens and n_seqs
- * <= MBD_KV_MAX_ROWS, n_q_heads <= 4096, (n_tokens / 128 + n_seqs) * n_q_heads < 2^31. n_tokens == 0 or n_seqs == 0 is a no-op. Bounded waits: see MBD_DEVERR_EXCHANGE_TIMEOUT.
+ * Logits, maxima and sums are fp32 (sums for |v| up to 2^88); exp(x_ij - lse_i) is rounded to bf16 for the product with v_j (off
+ * by 2^-8 of it). The result does not depend on what else runs or on other sequences' rows, and equal calls give equal bits.
+ * n_tokens and n_seqs are the room of a call, cu_tokens says how much of it there is; room that is not used costs a little (at 64
+ * query heads of 128 some 33 us for 65000 rows). head_dim: 64, 128 or 256. Limits: n_tokens and n_seqs <= MBD_KV_MAX_ROWS,
+ * n_q_heads <= 4096, (n_tokens / 128 + n_seqs) * n_q_heads < 2^31. n_tokens == 0 or n_seqs == 0 is a no-op. Bounded waits: see
+ * MBD_DEVERR_EXCHANGE_TIMEOUT.
  */
 mbd_status mbd_prompt_attention(void* out, const void* q, int64_t q_stride, const void* k, const void* v, int64_t kv_stride,
                                 const int32_t* cu_tokens, int64_t n_seqs, int64_t n_tokens, int64_t n_q_heads,
@@ -692,7 +695,8 @@ mbd_status mbd_rotary(void* out, int64_t out_stride, const void* x, int64_t x_st
  *                        min(rotary_dim - 1, ceil(d(beta_slow))) and r_i = (i - first) / max(last - first, 0.001) held to
  *                        [0, 1]: f_i = r_i g_i / factor + (1 - r_i) g_i.
  *   MBD_ROTARY_FACTORS : f_i = g_i / factors[i], a factor for each pair.
- * amplitude: as given; 0 means 1 (MBD_ROTARY_YARN: 0.1 ln(factor) + 1, and 1 for a factor up to 1). All in fp64. Host only: no stream, no launch.
+ * amplitude: as given; 0 means 1 (MBD_ROTARY_YARN: 0.1 ln(factor) + 1, and 1 for a factor up to 1). All in fp64. Host only: no
+ * stream, no launch.
  * MBD_ERR_INVALID_ARG for a null pointer, an unknown kind, a non-zero reserved, a rotary_dim that is not positive and even (NTK:
  * or is 2), a base or factor that is not positive and finite, an amplitude that is negative or not finite (in fp32), and for values
  * of a kind's own that give no finite frequencies (low >= high; base 1 or betas or original not positive).

@@ -2,8 +2,9 @@
 import numpy as np
 import pytest
 
+import workloads as wl
 from tests.test_kv_gpu import mbd  # noqa: F401  (mbd is the fixture)
-from tests.test_prompt_gpu import NAN, make, run
+from tests.test_prompt_gpu import NAN, check, make, run
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -105,3 +106,17 @@ def test_masked_values_change_no_bit(mbd, d, hq, hkv, window):
         want[cu[-1]:] = 0x5A5A
         np.testing.assert_array_equal(out, want, f"{at}")
         np.testing.assert_array_equal(lse, base_lse)
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(128, 4, 2), (64, 3, 3), (256, 1, 1)])
+@pytest.mark.parametrize("rise", [4.0, 10.9, 11.3, 40.0])   # of the logits, from each block to the next: 2^16 is 11.09
+def test_large_values_under_rising_logits(mbd, d, hq, hkv, rise):
+    """Sums stay in range for the values that the header allows (2^16 times 700 keys times 2^100 is below 2^126), whether the maximum
+    that they are relative to is kept from block to block or not."""
+    rng = np.random.default_rng(d)
+    qkv, cu = make(rng, [700], hq, hkv, d)
+    k0, v0 = hq * d, (hq + hkv) * d
+    qkv[:, :k0] = wl.f32_to_bf16_bits(np.full((700, hq * d), 0.5, np.float32))
+    qkv[:, k0:v0] = wl.f32_to_bf16_bits(np.repeat(np.arange(700, dtype=np.float32)[:, None] // 128 * (rise / d * 20), hkv * d, 1))
+    qkv[:, v0:v0 + hkv * d] += 100 << 7
+    check(mbd, qkv, cu, hq, hkv, d, scale=0.1)
