@@ -43,7 +43,7 @@
 //   FP8 static, 4 sequences of 13240..17308 tokens, 128 and 8 heads, pages of 128  38.5 us, 3250 GB/s
 //   bf16, 32 sequences of 100..8192 tokens, 16 and 2 heads of 256, pages of 16     56 us, 4830 GB/s
 //   bf16, 24 windows of 1024 tokens, 16 and 16 heads of 64                         23.4 us, 4230 GB/s
-//   NVFP4, 32 sequences of 100..8192 tokens, 64 and 8 heads, pages of 32           43 us, 3580 GB/s
+//   NVFP4, 32 sequences of 100..8192 tokens, 64 and 8 heads, pages of 32           43 to 46 us, 3350 to 3580 GB/s
 //   NVFP4, one sequence of 131071 tokens, 64 and 8 heads, pages of 128             42.3 us, 3570 GB/s
 // About ten microseconds of each do not depend on the bytes: launch, lengths, page table and first rows on the way in (each
 // a round trip of half a microsecond), shares that end up to 8% apart, and the joins.

@@ -22,9 +22,9 @@
 // form of the loop: 245 us with items dealt out in advance, 209 so).
 //
 // Measured on one GB300 (operations of the places in view; 1932 TFLOP/s is the measured peak, 1727 under the power cap):
-//   one prompt of 16001 tokens, 64 and 8 heads of 128      2.66 ms, 1580 TFLOP/s (at the power cap: 1.75 GHz)
-//   16 prompts of 1..2047 tokens, 32 and 8 heads of 128    179 us, 1060 TFLOP/s
-//   24 prompts of 700..6001, windows of 1024, 16 heads of 64   440 us, 650 TFLOP/s
+//   one prompt of 16001 tokens, 64 and 8 heads of 128      2.62 ms, 1600 TFLOP/s (at the power cap, 1.73 GHz: up to 2.77 on other boards)
+//   16 prompts of 1..2047 tokens, 32 and 8 heads of 128    176 us, 1070 TFLOP/s
+//   24 prompts of 700..6001, windows of 1024, 16 heads of 64   427 us, 670 TFLOP/s
 //   one prompt of 4000 tokens, 16 and 4 heads of 256       126 us, 1040 TFLOP/s
 //   one prompt of 517 tokens, 12 and 2 heads of 128        13.6 us
 // A step of two tiles against one block takes 2400 to 2650 cycles: at D 128 2048 of them are the tensor cores', at D 64 1024, and the
@@ -39,7 +39,8 @@
 // Values in masked places. A masked P is 0, and 0 times an infinite or NaN value would be NaN. So in blocks that hold masked
 // places (the diagonal, the window's edge) a warp looks at V as it arrives and puts zeros for such values, which leave every other
 // value's product as it is, bit for bit; before that product the softmax's threads add P times each of them that their row sees to O,
-// reading them from the call's V once more. In a block that all rows see whole the product does it.
+// reading them from the call's V once more (16 prompts of 1000 tokens, 32 and 8 heads of 128: 129 us, with an infinite row of V in
+// every 128 270). In a block that all rows see whole the product does it.
 //
 // Every wait is bounded: one that runs out sets the error bit, and all roles leave.
 #include <cuda.h>
@@ -175,10 +176,9 @@ __device__ __forceinline__ void tc_commit(const void* bar, uint32_t elected) {
                  ::"r"(smem_addr(bar)), "r"(elected) : "memory");
 }
 
-// Shared memory descriptor of a tile in rows of 128 swizzled bytes, its low word: address and leading offset (in 16 bytes). K-major
-// (rows are the operand's M or N): groups of 8 rows are 1024 bytes apart. MN-major (rows are the contraction): so are groups of
-// 8 rows, and chunks of 64 elements, the leading dimension, kChunkBytes.
-__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t leading) { return (addr >> 4) | (leading >> 4 << 16); }
+// Shared memory descriptor of a tile in rows of 128 swizzled bytes. Its low word: address and, from bit 16 on, leading offset (both in
+// 16 bytes). K-major (rows are the operand's M or N): groups of 8 rows are 1024 bytes apart. MN-major (rows are the contraction): so
+// are groups of 8 rows, and chunks of 64 elements, the leading dimension, kChunkBytes.
 constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 // bf16 x bf16 -> fp32, M 128.
 constexpr uint32_t instr_desc(int n, bool b_rows_are_k) {
@@ -240,7 +240,9 @@ struct Rows {
     int place, top;
     // More: one sequence behind the other, in each the last place first. Sequence first + 8 lane + c has tiles[c]; `upto` tiles belong to
     // this lane's sequences and to those of the lanes before it, `before` to sequences before `first`. These are sums over whatever
-    // offsets there are: nothing is taken for ascending, so that a bad one costs the two sequences that it bounds and no others.
+    // offsets there are: nothing is taken for ascending, so that a bad one costs the two sequences that it bounds and no others. (Levels of
+    // so many would take a pass over all of them for each item. Of up to 500 tokens, 32 and 8 heads of 128: 256 sequences with
+    // 65800 tokens take 395 us by levels, 257 with 62400 474 so; 16 heads of 64: 246 and 242.)
     int first, upto;
     int64_t before;
 
