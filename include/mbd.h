@@ -649,7 +649,7 @@ mbd_status mbd_kv_cache_resize(int32_t* page_table, int64_t pages_per_seq, int64
  *               sequence whose bounds are not (MBD_DEVERR_BAD_INDEX) is left out.
  *   scale     : finite (also times log2(e)), usually 1 / sqrt(head_dim).   window: 0 (none) or the number of tokens in view.
  *   lse       : fp32 [n_tokens, n_q_heads], written, or null.
- * Logits, maxima and sums are fp32 (sums for |v| up to 2^88); exp(x_ij - lse_i) is rounded to bf16 for the product with v_j (off
+ * Logits, maxima and sums are fp32 (sums for |v| up to 2^96); exp(x_ij - lse_i) is rounded to bf16 for the product with v_j (off
  * by 2^-8 of it). The result does not depend on what else runs or on other sequences' rows, and equal calls give equal bits.
  * n_tokens and n_seqs are the room of a call, cu_tokens says how much of it there is; room that is not used costs a little (at 64
  * query heads of 128 some 33 us for 65000 rows). head_dim: 64, 128 or 256. Limits: n_tokens and n_seqs <= MBD_KV_MAX_ROWS,

@@ -14,7 +14,7 @@
 // While one tile's softmax runs, the tensor cores have the other tile's two products to do, and the next block's S is issued
 // ahead of this block's P V, so that it is there when the softmax is done. (At D 128 TMEM holds one S besides O and P of both
 // tiles: they use it in turn, as a row is read out at once.) The maximum that a row's sums are relative to is kept until a
-// logit exceeds it by 2^16, so O is rescaled in the first blocks and hardly ever after them.
+// logit exceeds it by 2^8, so O is rescaled in the first blocks and hardly ever after them.
 //
 // Work. An item is two row tiles of one or two query heads. The grid has a CTA for each, and the CTAs that run take the indexes
 // of those that have not begun from the launch (cluster launch control), one ahead: the tiles at the ends of the sequences, which
@@ -22,9 +22,9 @@
 // form of the loop: 245 us with items dealt out in advance, 209 so).
 //
 // Measured on one GB300 (operations of the places in view; 1932 TFLOP/s is the measured peak, 1727 under the power cap):
-//   one prompt of 16001 tokens, 64 and 8 heads of 128      2.62 ms, 1600 TFLOP/s (at the power cap, 1.73 GHz: up to 2.77 on other boards)
-//   16 prompts of 1..2047 tokens, 32 and 8 heads of 128    176 us, 1070 TFLOP/s
-//   24 prompts of 700..6001, windows of 1024, 16 heads of 64   427 us, 670 TFLOP/s
+//   one prompt of 16001 tokens, 64 and 8 heads of 128      2.64 to 2.77 ms, 1510 to 1590 TFLOP/s (at the power cap, 1.73 GHz)
+//   16 prompts of 1..2047 tokens, 32 and 8 heads of 128    178 us, 1070 TFLOP/s
+//   24 prompts of 700..6001, windows of 1024, 16 heads of 64   460 us, 620 TFLOP/s (one size of heads: 429)
 //   one prompt of 4000 tokens, 16 and 4 heads of 256       126 us, 1040 TFLOP/s
 //   one prompt of 517 tokens, 12 and 2 heads of 128        13.6 us
 // A step of two tiles against one block takes 2400 to 2650 cycles: at D 128 2048 of them are the tensor cores', at D 64 1024, and the
@@ -53,10 +53,11 @@ namespace mbd {
 namespace {
 
 constexpr int kRows = 128;       // query rows of a tile, keys of a block
-// Units of log2 that a logit may exceed the kept maximum by. Rows change theirs one by one, and a warp rescales when any of its rows does:
-// 24 prompts in windows of 1024 whose queries' heads differ in size, 460 us at 8, 437 at 12, 426 at 16, 422 at 24. Sums of P V
-// reach 2^16 times the number of keys times |v|, which leaves |v| up to 2^88 for the longest prompt.
-constexpr float kLazy = 16.0f;
+// Units of log2 that a logit may exceed the kept maximum by. 12 and 16 take less time (24 prompts in windows of 1024 437 and 427 us for
+// 460), but a row whose maximum is the kept one has an exact P for its largest logit: the error of one prompt of 16001 tokens against
+// 64 bits is 0.00212 of the norm at 8, 0.00225 at 12 and 0.00229 at 16. Sums of P V reach 2^8 times the number of keys times |v|, which
+// leaves |v| up to 2^96 for the longest prompt.
+constexpr float kLazy = 8.0f;
 constexpr float kLn2 = 0.693147180559945309f;
 
 template <int D>
@@ -867,7 +868,8 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1) prompt_kernel(const __
                     tc_fence_after();
                 }
                 // A row goes by its own logits alone, so that the rows after it, whose tokens it does not see, change no bit of it. (Those
-                // behind the sequence's end have no say at all.)
+                // behind the sequence's end have no say at all.) Where heads differ in size it makes for more blocks in which some row of
+                // a warp moves than if all of them moved together: windows of 1024 460 us, 440 so.
                 const bool up = top > lim;
                 if (__any_sync(0xffffffffu, up && row < it.len)) {
                     if (j > lo) {

@@ -109,9 +109,9 @@ def test_masked_values_change_no_bit(mbd, d, hq, hkv, window):
 
 
 @pytest.mark.parametrize("d,hq,hkv", [(128, 4, 2), (64, 3, 3), (256, 1, 1)])
-@pytest.mark.parametrize("rise", [4.0, 10.9, 11.3, 40.0])   # of the logits, from each block to the next: 2^16 is 11.09
+@pytest.mark.parametrize("rise", [4.0, 5.5, 5.6, 10.9, 11.3, 40.0])   # of the logits, from each block to the next: 2^8 is 5.55
 def test_large_values_under_rising_logits(mbd, d, hq, hkv, rise):
-    """Sums stay in range for the values that the header allows (2^16 times 700 keys times 2^100 is below 2^126), whether the maximum
+    """Sums stay in range for the values that the header allows (2^8 times 700 keys times 2^102 is below 2^120), whether the maximum
     that they are relative to is kept from block to block or not."""
     rng = np.random.default_rng(d)
     qkv, cu = make(rng, [700], hq, hkv, d)
